@@ -48,6 +48,8 @@ EP_FP8 = 0x1
 EP_FP8_ROUND_SCALE = 0x2
 EP_FP8_UE8M0 = 0x4
 
+EP_LINEAR_GLU = 0x1
+
 EP_MAX_EXPERTS = 1024
 EP_MAX_TOPK = 32
 EP_MAX_HIDDEN = 16384
@@ -90,6 +92,22 @@ class ep_recv_buffer_t(ctypes.Structure):
     ]
 
 
+class ep_kv_cache_t(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("num_seqs", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -129,6 +147,13 @@ def lib() -> ctypes.CDLL:
         "ep_ll_update_mask": (I, [P, SZ, I, I, I, P]),
         "ep_ll_query_mask": (I, [P, SZ, I, P, P]),
         "ep_ll_clean_mask": (I, [P, SZ, I, P]),
+        "ep_kv_append": (I, [ctypes.POINTER(ep_kv_cache_t), P, P, I, P, I64, P, I64, P, I64, P, I64, I, P, I, I, I,
+                             P, P]),
+        "ep_kv_attention_workspace_bytes": (SZ, [I, I, I, I]),
+        "ep_kv_attention": (I, [ctypes.POINTER(ep_kv_cache_t), P, P, I, P, I64, I, ctypes.c_float, I, P, P, P, SZ, P,
+                                P]),
+        "ep_expert_linear_workspace_bytes": (SZ, [I, I64, I, I]),
+        "ep_expert_linear": (I, [P, P, I64, I, P, P, I64, I, I64, P, P, I, I, P, P, SZ, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -357,6 +382,61 @@ def ep_fp8_quantize(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, fp8:
     """x [rows, H] bf16 -> q [rows, H] uint8 (E4M3) and scales [rows, H/128] (fp32, or uint8 UE8M0)."""
     _check(lib().ep_fp8_quantize(_p(x), x.shape[0], x.shape[1], int(fp8), _p(q), _p(scales), _stream(stream)),
            "ep_fp8_quantize")
+
+
+def _heads(t: Optional[torch.Tensor], what: str, dtype=torch.bfloat16):
+    """Pointer and token stride of a [tokens, heads, dim] tensor whose heads are contiguous."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 3:
+        raise ValueError(f"{what}: expected a CUDA tensor [tokens, heads, dim] of {dtype}")
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise ValueError(f"{what}: heads must be contiguous")
+    # One token (or none) has no stride of its own.
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return ctypes.c_void_p(t.data_ptr()), stride
+
+
+def _typed(t: Optional[torch.Tensor], what: str, dtype, shape=None) -> Optional[torch.Tensor]:
+    if t is not None and (t.dtype != dtype or (shape is not None and tuple(t.shape) != tuple(shape))):
+        raise ValueError(f"{what}: expected {dtype}" + (f" of shape {tuple(shape)}" if shape is not None else ""))
+    return t
+
+
+def ep_kv_append(cache: "KVCache", seq_lens, cu_tokens, k, v, q, q_out, rope, interleaved, status=None,
+                 stream=None) -> None:
+    kp, ks = _heads(k, "k")
+    vp, vs = _heads(v, "v")
+    qp, qs = _heads(q, "q")
+    op, os_ = _heads(q_out, "q_out")
+    rows, dim = rope.shape if rope is not None else (0, 0)
+    _check(lib().ep_kv_append(ctypes.byref(cache.c_struct()), _p(seq_lens), _p(cu_tokens), k.shape[0], kp, ks, vp, vs,
+                              qp, qs, op, os_, q.shape[1] if q is not None else 0, _p(rope), rows, dim,
+                              int(bool(interleaved)), _p(status), _stream(stream)), "ep_kv_append")
+
+
+def ep_kv_attention_workspace_bytes(num_tokens: int, num_q_heads: int, num_heads: int, head_dim: int) -> int:
+    return int(lib().ep_kv_attention_workspace_bytes(num_tokens, num_q_heads, num_heads, head_dim))
+
+
+def ep_kv_attention(cache: "KVCache", seq_lens, cu_tokens, q, scale, window, out, lse, workspace, status=None,
+                    stream=None) -> None:
+    qp, qs = _heads(q, "q")
+    _check(lib().ep_kv_attention(ctypes.byref(cache.c_struct()), _p(seq_lens), _p(cu_tokens), q.shape[0], qp, qs,
+                                 q.shape[1], float(scale), int(window), _p(out), _p(lse), _p(workspace),
+                                 workspace.numel(), _p(status), _stream(stream)), "ep_kv_attention")
+
+
+def ep_expert_linear_workspace_bytes(num_experts: int, max_rows: int, in_features: int, x_is_fp8: bool) -> int:
+    return int(lib().ep_expert_linear_workspace_bytes(num_experts, max_rows, in_features, int(bool(x_is_fp8))))
+
+
+def ep_expert_linear(x, x_scale, x_rows, in_features, row_count, row_offset, rows_per_expert, max_rows, w, w_scale,
+                     flags, y, workspace, status=None, stream=None) -> None:
+    _check(lib().ep_expert_linear(_p(x), _p(x_scale), x_rows, in_features, _p(row_count), _p(row_offset),
+                                  rows_per_expert, w.shape[0], max_rows, _p(w), _p(w_scale), w.shape[1], int(flags),
+                                  _p(y), _p(workspace), workspace.numel(), _p(status), _stream(stream)),
+           "ep_expert_linear")
 
 
 # -------------------------------------------------------------- page-level ----
@@ -651,3 +731,152 @@ def low_latency_clean_mask_buffer(handle, num_ranks: Optional[int] = None, strea
     """Restore every rank."""
     ws, R = _ws_ranks(handle, num_ranks)
     ep_ll_clean_mask(ws, R, stream)
+
+
+# ------------------------------------- the decode step around the dispatch ----
+@dataclasses.dataclass
+class KVCache:
+    """A paged key/value cache in E4M3 with a power-of-two scale per (page, head)."""
+    k: torch.Tensor           # [num_pages, num_heads, page_size, head_dim] uint8 (E4M3)
+    v: torch.Tensor
+    k_scale: torch.Tensor     # [num_pages, num_heads] fp32
+    v_scale: torch.Tensor
+    page_table: torch.Tensor  # [num_seqs, max_pages] int32
+    _c: Optional[ep_kv_cache_t] = dataclasses.field(default=None, init=False, repr=False, compare=False)
+
+    def c_struct(self) -> ep_kv_cache_t:
+        """The C handle, built once: a cache's arrays are fixed when it is made."""
+        if self._c is None:
+            if self.k.dim() != 4 or self.page_table.dim() != 2:
+                raise ValueError("KVCache: k is [pages, heads, page_size, head_dim], page_table [seqs, max_pages]")
+            pages, heads, size, dim = self.k.shape
+            _typed(self.k, "k", torch.uint8)
+            _typed(self.v, "v", torch.uint8, self.k.shape)
+            _typed(self.k_scale, "k_scale", torch.float32, (pages, heads))
+            _typed(self.v_scale, "v_scale", torch.float32, (pages, heads))
+            _typed(self.page_table, "page_table", torch.int32)
+            self._c = ep_kv_cache_t(_p(self.k), _p(self.v), _p(self.k_scale), _p(self.v_scale), _p(self.page_table),
+                                    pages, heads, size, dim, *self.page_table.shape)
+        return self._c
+
+
+def new_kv_cache(num_pages: int, num_heads: int, page_size: int, head_dim: int, page_table: torch.Tensor) -> KVCache:
+    """An empty cache on page_table's device."""
+    dev = page_table.device
+    shape = (num_pages, num_heads, page_size, head_dim)
+    return KVCache(torch.zeros(shape, dtype=torch.uint8, device=dev), torch.zeros(shape, dtype=torch.uint8, device=dev),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=dev),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=dev), page_table.to(torch.int32).contiguous())
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, seq_lens: torch.Tensor,
+              cu_tokens: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None,
+              q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+              status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Append k, v [tokens, heads, dim] bf16 to the cache, rotating k (and q) by position.
+
+    seq_lens [seqs] int32 counts the appended tokens; cu_tokens [seqs + 1]
+    int32 delimits each sequence's tokens (None: one each). rope [positions,
+    rope_dim] fp32 holds cosines, then sines. k, v and q may be slices of one
+    fused projection. Returns the rotated queries (q_out, made if not given).
+    """
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _, heads, _, dim = cache.k.shape
+    _typed(k, "k", torch.bfloat16, (k.shape[0], heads, dim))
+    _typed(v, "v", torch.bfloat16, k.shape)
+    if q is not None:
+        _typed(q, "q", torch.bfloat16, (k.shape[0], q.shape[1], dim))
+        _typed(q_out, "q_out", torch.bfloat16, q.shape)
+    seqs = cache.page_table.shape[0]
+    _typed(seq_lens, "seq_lens", torch.int32, (seqs,))
+    _typed(cu_tokens, "cu_tokens", torch.int32, (seqs + 1,))
+    _typed(rope, "rope", torch.float32)
+    ep_kv_append(cache, seq_lens, cu_tokens, k, v, q, q_out, rope, interleaved, status, stream)
+    return q_out
+
+
+def kv_attention_workspace(q: torch.Tensor, cache: KVCache) -> torch.Tensor:
+    """A zero-filled workspace for kv_attention of queries shaped like q, to keep between calls."""
+    need = ep_kv_attention_workspace_bytes(q.shape[0], q.shape[1], cache.k.shape[1], cache.k.shape[3])
+    if need == 0:
+        raise EPError("kv_attention", EP_ERR_INVALID_ARG)
+    return torch.zeros(need, dtype=torch.uint8, device=q.device)
+
+
+def kv_attention(q: torch.Tensor, cache: KVCache, seq_lens: torch.Tensor, cu_tokens: Optional[torch.Tensor] = None,
+                 scale: Optional[float] = None, window: int = 0, out: Optional[torch.Tensor] = None,
+                 return_lse: bool = False, workspace: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None, stream=None):
+    """Attention of q [tokens, q_heads, dim] bf16 over each token's sequence in the cache.
+
+    Token i of a sequence's n sees positions up to seq_len - n + i, the last
+    `window` of them when window > 0. scale defaults to dim ** -0.5. A
+    workspace passed in must have been zero-filled once (kv_attention_workspace
+    makes one); without it, one is made. Returns out, or (out, lse).
+    """
+    T, QH, dim = q.shape
+    _typed(q, "q", torch.bfloat16, (T, QH, cache.k.shape[3]))
+    seqs = cache.page_table.shape[0]
+    _typed(seq_lens, "seq_lens", torch.int32, (seqs,))
+    _typed(cu_tokens, "cu_tokens", torch.int32, (seqs + 1,))
+    if out is None:
+        out = torch.empty((T, QH, dim), dtype=torch.bfloat16, device=q.device)
+    _typed(out, "out", torch.bfloat16, q.shape)
+    lse = torch.empty((T, QH), dtype=torch.float32, device=q.device) if return_lse else None
+    if workspace is None:
+        workspace = kv_attention_workspace(q, cache)
+    ep_kv_attention(cache, seq_lens, cu_tokens, q, dim ** -0.5 if scale is None else scale, window, out, lse, workspace,
+                    status, stream)
+    return (out, lse) if return_lse else out
+
+
+def expert_linear_workspace(x: torch.Tensor, weight: torch.Tensor, max_rows: Optional[int] = None) -> torch.Tensor:
+    """A zero-filled workspace for expert_linear of rows shaped like x, to keep between calls."""
+    K = x.shape[-1]
+    rows = x.numel() // K if max_rows is None else int(max_rows)
+    need = ep_expert_linear_workspace_bytes(weight.shape[0], rows, K, x.dtype == torch.uint8)
+    if need == 0:
+        raise EPError("expert_linear", EP_ERR_INVALID_ARG)
+    return torch.zeros(need, dtype=torch.uint8, device=x.device)
+
+
+def expert_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor, row_count: torch.Tensor,
+                  row_offset: Optional[torch.Tensor] = None, x_scale: Optional[torch.Tensor] = None, glu: bool = False,
+                  out: Optional[torch.Tensor] = None, max_rows: Optional[int] = None,
+                  workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """Each expert's product of its received rows with its 4-bit weights.
+
+    x is a dispatch's expert-major buffer [rows, in] with row_offset =
+    expert_offset, or the low-latency [E, cap, in] (row_offset None); bf16, or
+    uint8 E4M3 with x_scale [.., in/128] uint8 (UE8M0, use_ue8m0=True of the
+    dispatch). weight [E, out, in/2] uint8 holds two E2M1 codes a byte,
+    weight_scale [E, out, in/32] UE8M0 bytes. glu: y = silu(gate) * up of the
+    two halves of the outputs. Rows that no expert received are left as they
+    are in out. max_rows bounds the rows received by all experts (default: all
+    of x's), and sizes the workspace.
+    """
+    E, M, half = weight.shape
+    K = x.shape[-1]
+    _typed(weight, "weight", torch.uint8, (E, M, K // 2))
+    _typed(weight_scale, "weight_scale", torch.uint8, (E, M, K // 32))
+    _typed(row_count, "row_count", torch.int32, (E,))
+    _typed(row_offset, "row_offset", torch.int32)
+    _typed(x, "x", torch.bfloat16 if x_scale is None else torch.uint8)
+    _typed(x_scale, "x_scale", torch.uint8, (*x.shape[:-1], K // 128))
+    if row_offset is None and (x.dim() != 3 or x.shape[0] != E):
+        raise ValueError("x: expected [num_experts, cap, in] without row_offset")
+    if row_offset is not None and row_offset.numel() < E:
+        raise ValueError("row_offset: expected an offset for each expert")
+    rows = x.numel() // K
+    shape = (*x.shape[:-1], M // 2 if glu else M)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    _typed(out, "out", torch.bfloat16, shape)
+    limit = rows if max_rows is None else int(max_rows)
+    if workspace is None:
+        workspace = expert_linear_workspace(x, weight, limit)
+    ep_expert_linear(x, x_scale, rows, K, row_count, row_offset, x.shape[1] if row_offset is None else 0, limit, weight,
+                     weight_scale, EP_LINEAR_GLU if glu else 0, out, workspace, status, stream)
+    return out

@@ -211,4 +211,68 @@ cudaError_t launch_e4m3_encode(const float* in, uint8_t* out, int64_t n, cudaStr
 cudaError_t launch_quantize_rows(const uint16_t* x, int64_t rows, int H, int fp8_flags, uint8_t* q, void* scales,
                                  cudaStream_t s);
 
+// ---- the decode step around the dispatch ------------------------------------
+// A cache and the tokens of one call (ep.h: ep_kv_cache_t, cu_tokens, seq_lens).
+struct KVParams {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;  // [B, MP]
+  const int32_t* lens;   // [B], this call's tokens included
+  const int32_t* cu;     // [B + 1], or null: one token per sequence
+  int pages, KH, P, D, B, MP;
+  int log2P;
+  int N;                 // tokens of the call
+  int32_t* status;
+};
+
+struct KVAppendParams {
+  KVParams c;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  const uint16_t* q;     // null: keys and values only
+  uint16_t* q_out;
+  int64_t k_stride, v_stride, q_stride, q_out_stride;  // elements between tokens
+  int QH;
+  const float* rope;     // [rope_rows, rot]: cosines, then sines (null: rot == 0)
+  int rope_rows, rot, interleaved;
+  int units;             // (sequence, page) places of the grid
+};
+
+struct KVAttentionParams {
+  KVParams c;
+  const uint16_t* q;
+  int64_t q_stride;
+  int QH, G;             // G = QH / KH query heads share a cache head
+  float scale_log2;      // scale * log2(e)
+  int window;
+  uint16_t* out;
+  float* lse;            // or null
+  uint8_t* ws;
+};
+
+struct ExpertLinearParams {
+  const void* x;             // BF16, or E4M3 with x_scale
+  const uint8_t* x_scale;
+  int64_t x_rows;
+  const int32_t* count;      // [E]
+  const int32_t* offset;     // [E], or null: e * region
+  int64_t region;
+  int E, K, M;               // M output features (gates and ups together)
+  int glu;
+  int64_t max_rows;
+  const uint8_t* w;
+  const uint8_t* w_scale;
+  uint16_t* y;
+  uint8_t* ws;
+  int32_t* status;
+};
+
+cudaError_t launch_kv_append(const KVAppendParams& p, cudaStream_t s);
+size_t kv_attention_ws_bytes(int N, int QH, int KH, int D);
+cudaError_t launch_kv_attention(const KVAttentionParams& p, cudaStream_t s);
+size_t expert_linear_ws_bytes(int E, int64_t max_rows, int K, bool fp8);
+cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s);
+
 }  // namespace ep

@@ -551,6 +551,165 @@ int ep_fp8_e4m3_encode(const float* in, uint8_t* out, int64_t n, void* stream);
 int ep_fp8_quantize(const void* x, int64_t rows, int hidden, int fp8_flags, uint8_t* q, void* scales,
                     void* stream);
 
+/*
+ * ---- the decode step around the dispatch -----------------------------------
+ * A paged key/value cache held in E4M3, attention over it, and the experts'
+ * products with 4-bit weights: what a decode step runs before the low-latency
+ * send and between its receive and combine. Same conventions as above.
+ *
+ * Tokens of a call lie in sequence order: sequence b's are rows
+ * [cu_tokens[b], cu_tokens[b + 1]) (cu_tokens [num_seqs + 1] int32, ascending
+ * from 0; NULL = one token per sequence, num_tokens == num_seqs). seq_lens[b]
+ * counts the sequence's tokens with this call's included, so its i-th of n
+ * tokens here has position seq_lens[b] - n + i.
+ *
+ * The cache: pages of page_size tokens; page_table[b, j] names the page that
+ * holds positions [j * page_size, (j + 1) * page_size) of sequence b. The
+ * tokens of one page and one head form a block: E4M3 codes with one fp32
+ * scale s, a power of two; a code stands for code * s.
+ *   k, v              [num_pages, num_heads, page_size, head_dim] E4M3, 16-byte aligned
+ *   k_scale, v_scale  [num_pages, num_heads] fp32
+ *   page_table        [num_seqs, max_pages] int32; entries past a sequence's
+ *                     length are not read; an entry outside [0, num_pages)
+ *                     below it flags EP_ST_BAD_INDEX (append skips the page's
+ *                     tokens, attention treats them as masked)
+ *   page_size         16, 32, 64 or 128; head_dim 64 or 128
+ * Neither the codes past a sequence's last token nor the scales of unused
+ * pages need to be initialised.
+ */
+typedef struct ep_kv_cache {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  int32_t num_pages;
+  int32_t num_heads;
+  int32_t page_size;
+  int32_t head_dim;
+  int32_t num_seqs;
+  int32_t max_pages;
+} ep_kv_cache_t;
+
+/*
+ * Append this call's keys and values to the cache, keys (and queries) rotated
+ * by their position on the way.
+ *
+ * Rotation: of a head's channels [0, rope_dim), pairs (x, y) at position p and
+ * pair index i become (x c - y s, y c + x s) with c = rope[p, i], s = rope[p,
+ * rope_dim / 2 + i], each product and sum rounded to fp32; pairs are channels
+ * (i, i + rope_dim / 2), or (2i, 2i + 1) when interleaved. Other channels and
+ * values pass unchanged.
+ *
+ * Blocks: amax is the largest finite magnitude that the call appends to the
+ * block. If the block holds earlier tokens of the sequence its scale becomes
+ * s = max(s_old, p(amax)), otherwise p(amax), where p(a) is the smallest power
+ * of two >= fl(a / 448), at least 2^-100. When s grows over s_old, the earlier
+ * tokens' codes c are re-encoded as e4m3(c * s_old / s). New codes are
+ * e4m3(x / s), to nearest even, saturated to +-448 (so infinities become
+ * +-448 s); NaN stays NaN. The same call made twice changes nothing more.
+ *
+ *   C             the cache; a page must not appear in two sequences' tables at
+ *                 positions that this call writes
+ *   seq_lens      [num_seqs] int32
+ *   k, v          [num_tokens, C->num_heads, head_dim] BF16, heads contiguous,
+ *                 tokens k_stride / v_stride elements apart (a multiple of 8)
+ *   q, q_out      [num_tokens, num_q_heads, head_dim] BF16 with token strides of
+ *                 their own, or both NULL; q_out may be q
+ *   rope          [rope_rows, rope_dim] fp32 (cosines, then sines), 16-byte
+ *                 aligned; NULL with rope_dim 0: no rotation (queries are copied)
+ *   rope_dim      a multiple of 16, <= head_dim
+ *   status        EP_ST_BAD_INDEX: a page outside the cache, cu_tokens out of
+ *                 order, a sequence shorter than its new tokens or longer than
+ *                 rope_rows; EP_ST_CAPACITY: longer than max_pages * page_size.
+ *                 The sequence's tokens are then skipped, their queries too; for
+ *                 a page outside the cache, its keys and values alone.
+ */
+int ep_kv_append(const ep_kv_cache_t* C, const int32_t* seq_lens, const int32_t* cu_tokens, int num_tokens,
+                 const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q, int64_t q_stride,
+                 void* q_out, int64_t q_out_stride, int num_q_heads, const float* rope, int rope_rows, int rope_dim,
+                 int interleaved, int32_t* status, void* stream);
+
+/* Bytes of device workspace ep_kv_attention needs (0: sizes out of range).
+ * Depends only on the arguments. */
+size_t ep_kv_attention_workspace_bytes(int num_tokens, int num_q_heads, int num_heads, int head_dim);
+
+/*
+ * Attention of each new token over its sequence's cache: for token t of
+ * sequence b at position p and query head h,
+ *   out[t, h] = sum_j softmax_j(scale * <q[t, h], k_j>) v_j
+ * over j <= p, and j > p - window when window > 0, with k_j and v_j the cached
+ * values (code * scale) of head h / (num_q_heads / C->num_heads). The cache
+ * already holds the new tokens (ep_kv_append). Products take q as an 11-bit
+ * significand scaled by its row's largest magnitude (a BF16 value keeps all
+ * its bits down to 2^-14 of it) and softmax weights as 11-bit significands;
+ * sums, maxima and normalisers are fp32. A token with nothing to attend
+ * (seq_lens[b] = 0, a negative position) gets zeros, and lse -inf. Codes at
+ * masked positions are never used, NaN among them.
+ *
+ *   q            [num_tokens, num_q_heads, head_dim] BF16, tokens q_stride
+ *                elements apart (a multiple of 8)
+ *   num_q_heads  a multiple of C->num_heads
+ *   out          [num_tokens, num_q_heads, head_dim] BF16
+ *   lse          [num_tokens, num_q_heads] fp32, the log of the softmax's sum of
+ *                exponentials, or NULL
+ *   workspace    at least ep_kv_attention_workspace_bytes(...) bytes, 16-byte
+ *                aligned, zero-filled before its first use; every call leaves it
+ *                ready for the next. Not to be shared by calls in flight.
+ *   status       EP_ST_BAD_INDEX: a page outside the cache (masked) or cu_tokens
+ *                out of order; EP_ST_CAPACITY: a sequence longer than
+ *                max_pages * page_size (the rest of it is masked)
+ * Results do not depend on the order in which blocks run.
+ */
+int ep_kv_attention(const ep_kv_cache_t* C, const int32_t* seq_lens, const int32_t* cu_tokens, int num_tokens,
+                    const void* q, int64_t q_stride, int num_q_heads, float scale, int window, void* out, float* lse,
+                    void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/* Flags of ep_expert_linear. */
+#define EP_LINEAR_GLU 0x1 /* y = silu(gate) * up: the first half of the outputs are gates */
+
+/* Bytes of device workspace ep_expert_linear needs (0: sizes out of range).
+ * Depends only on the arguments. */
+size_t ep_expert_linear_workspace_bytes(int num_experts, int64_t max_rows, int in_features, int x_is_fp8);
+
+/*
+ * The experts' products with 4-bit weights: for each expert e and each row j
+ * it received, y_row = x_row W_e^T, with W_e [out_features, in_features] of
+ * E2M1 codes and one UE8M0 scale 2^(b - 127) per 32 inputs; fp32 sums, rounded
+ * once to BF16. With EP_LINEAR_GLU, W_e's first out_features / 2 rows are gates
+ * g and the others u, and y = silu(g) * u, taken in fp32 before the rounding.
+ *
+ * Rows: row_count[e] rows (num_tokens_per_expert, or the receive's
+ * recv_count), starting at row_offset[e] (the expert-major buffer's
+ * expert_offset), or at e * rows_per_expert when row_offset is NULL (the
+ * low-latency [E, R*T] regions). y has the rows' layout; rows that no expert
+ * received are neither read nor written.
+ *
+ *   x             [x_rows, in_features] BF16, or E4M3 when x_scale is given
+ *   x_scale       [x_rows, in_features / 128] UE8M0 bytes (the FP8 dispatch with
+ *                 EP_FP8_UE8M0), or NULL: x is BF16. BF16 rows enter the products
+ *                 as two E4M3 terms with a scale per 32 inputs, which hold every
+ *                 bit down to 2^-14 of the 32's largest magnitude, and 2^-23 of it
+ *                 below that. A row with an infinity or a NaN gives NaNs.
+ *   in_features   a multiple of 128, <= EP_MAX_HIDDEN
+ *   out_features  a multiple of 8 (of 16 with EP_LINEAR_GLU), <= 2^20
+ *   max_rows      an upper bound of the rows received by all experts; rows beyond
+ *                 it are skipped and flagged EP_ST_CAPACITY
+ *   w             [num_experts, out_features, in_features / 2] bytes, two codes
+ *                 each, the lower channel in the low four bits; 32-byte aligned
+ *   w_scale       [num_experts, out_features, in_features / 32] UE8M0 bytes,
+ *                 16-byte aligned
+ *   y             [x_rows, out_features (/ 2 with EP_LINEAR_GLU)] BF16
+ *   workspace     at least ep_expert_linear_workspace_bytes(...) bytes, 256-byte
+ *                 aligned, zero-filled before its first use; every call leaves it
+ *                 ready for the next. Not to be shared by calls in flight.
+ *   status        EP_ST_CAPACITY: rows outside x, or more than max_rows
+ */
+int ep_expert_linear(const void* x, const uint8_t* x_scale, int64_t x_rows, int in_features,
+                     const int32_t* row_count, const int32_t* row_offset, int64_t rows_per_expert, int num_experts,
+                     int64_t max_rows, const uint8_t* w, const uint8_t* w_scale, int out_features, int flags, void* y,
+                     void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,82 +1,745 @@
 // The experts' products with 4-bit weights on sm_103a: y_row = x_row W_e^T.
 //
-// This form: a block for 4 outputs of an expert, a warp each (with GLU, a
-// gate and its up); every row in turn, fp32 fused multiply-adds.
+// Mathematics: W's E2M1 codes and UE8M0 scales (32 inputs each) are operands
+// of the tensor cores as they are: the block-scaled product multiplies E2M1 by
+// E4M3 exactly and applies both sides' power-of-two scales, so no weight is
+// ever converted. The weights are the product's 128-row side, the rows of x
+// its columns. An E4M3 x enters as it is. A BF16 x enters as two columns: with
+// s a power of two, 448 s >= the largest magnitude of 32 neighbours, h = e4m3(x / s)
+// and l = e4m3(16 (x / s - h)) with the scale s / 16; h keeps 4 of x's 8
+// significant bits and l the rest (exactly, down to 2^-14 of the largest), and
+// the two columns' sums are added at the end.
+//
+// What bounds it: the weights, read once from HBM (4.25 bits each), until an
+// expert has about 100 rows. So the work is laid out as one stream of weights:
+// every (expert, rows tile, 128 outputs) is a unit of in / 128 steps, and the
+// blocks (one an SM) take equal runs of consecutive steps, whatever the
+// experts' loads. A unit that several blocks share is joined by the last of
+// them to finish: each leaves its fp32 sums in the workspace, and the last
+// adds them in the order of the steps, so that the result does not depend on
+// which one that was.
+//
+// Two launches: expert_rows_kernel writes x in the tensor cores' shared-memory
+// layout (and splits BF16), expert_linear_kernel is its programmatic dependent
+// and starts reading weights meanwhile.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.cuh"
+#include "tensor.cuh"
 
 namespace ep {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kStep = 128;                  // inputs a step
+constexpr int kTileM = 128;                 // outputs a unit (with GLU: 64 gates, 64 ups)
+constexpr int kTileBytes = kTileM * kStep;  // weights of a step in shared memory (8-bit containers)
+constexpr int kTileTx = kTileBytes / 2;     // ... and as TMA counts them
+constexpr int kScaleBytes = 512;            // scale bytes of 128 rows for one step
+constexpr int kMaxCols = 192;
+constexpr int kMaxBlocks = 160;             // blocks a workspace has room for
+constexpr int kThreads = 256;
+constexpr int kMaxStages = 12;
+constexpr int kTmemCols = 512;              // two accumulators of kMaxCols, then scales
+constexpr int kTmemScales = 2 * kMaxCols;
+constexpr int kScaleSlots = 4;              // steps whose scales tensor memory holds
+constexpr int kMinSteps = 4;                // fewest steps worth a block of their own
+constexpr int kScaleCols = 12;              // columns a step: 4 of the weights', 8 of the rows'
 
-__device__ __forceinline__ float e2m1(unsigned c) {
-  const unsigned m = c & 7u;
-  const float v = m < 2u ? 0.5f * m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-  return c & 8u ? -v : v;
-}
+struct Params {
+  ExpertLinearParams p;
+  int mult;         // columns a row: 2 for BF16, 1 for E4M3
+  int tile_rows;    // rows of a full tile
+  int cols_cap;     // its columns
+  int KB;           // steps of a unit: K / 128
+  int MT;           // units of a tile: output tiles of an expert
+  int stages;
+  unsigned stage_bytes;
+  unsigned* counters;  // [kMaxBlocks]
+  float* partial;      // [kMaxBlocks][2][tile_rows][kTileM]
+  uint8_t* image;      // rows of x as shared memory holds them
+  uint8_t* image_scale;
+};
 
-__device__ __forceinline__ float ue8m0(unsigned b) {
-  if (b == 255u) return __uint_as_float(0x7FC00000u);
-  return b ? __uint_as_float(b << 23) : __uint_as_float(0x00400000u);
-}
+__device__ __forceinline__ int round8(int v) { return (v + 7) & ~7; }
 
-__device__ __forceinline__ float x_value(const ExpertLinearParams& p, int64_t row, int k) {
-  if (!p.x_scale) return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.x)[row * p.K + k]) << 16);
-  uint32_t f2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f2) : "h"(static_cast<uint16_t>(static_cast<const uint8_t*>(p.x)[row * p.K + k])));
-  return __low2float(*reinterpret_cast<const __half2*>(&f2)) * ue8m0(p.x_scale[row * (p.K / 128) + k / 128]);
-}
-
-__device__ float dot(const ExpertLinearParams& p, int e, int m, int64_t row, int lane) {
-  const uint8_t* w = p.w + (static_cast<int64_t>(e) * p.M + m) * (p.K / 2);
-  const uint8_t* ws = p.w_scale + (static_cast<int64_t>(e) * p.M + m) * (p.K / 32);
-  float acc = 0.0f;
-  for (int k = 2 * lane; k < p.K; k += 64) {
-    const unsigned c = w[k / 2];
-    const float s = ue8m0(ws[k / 32]);
-    acc = fmaf(x_value(p, row, k), e2m1(c & 15u) * s, acc);
-    acc = fmaf(x_value(p, row, k + 1), e2m1(c >> 4) * s, acc);
+// The rows expert e can have: within its region, and x.
+__device__ __forceinline__ int rows_of(const ExpertLinearParams& p, int e, int32_t count, int64_t& first) {
+  first = p.offset ? static_cast<int64_t>(__ldg(p.offset + e)) : e * p.region;
+  if (count <= 0) return 0;
+  int64_t n = count;
+  int64_t room = p.x_rows - first;
+  if (!p.offset && room > p.region) room = p.region;
+  if (first < 0) room = 0;
+  if (n > room) {
+    n = room > 0 ? room : 0;
+    flag(p.status, EP_ST_CAPACITY);
   }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  return acc;
+  return static_cast<int>(n);
 }
 
-__global__ void __launch_bounds__(kThreads) expert_linear_kernel(const ExpertLinearParams p) {
+// ---- rows of x -------------------------------------------------------------------
+// The place of a group of eight rows: warp-wide search over the experts' counts.
+struct RowGroup {
+  int e, n;        // expert (-1: no such group) and its rows
+  int64_t first;   // its first row in x
+  int row0;        // the group's first row within the expert
+  int slot0;       // rows (rounded up to 8) of the experts before
+  int tile0;       // row tiles of the experts before
+};
+
+__device__ RowGroup find_group(const Params& q, int group) {
+  const ExpertLinearParams& p = q.p;
   const int lane = threadIdx.x & 31;
-  grid_dependency_wait();
-  const int outs = p.glu ? p.M / 2 : p.M;
-  const int m = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), e = blockIdx.y;
-  if (m >= outs) return;
-  const int n = p.count[e];
-  const int64_t first = p.offset ? p.offset[e] : e * p.region;
-  int64_t before = 0;  // rows of the experts before this one
-  for (int i = 0; i < e; ++i) before += p.offset ? max(0, p.count[i]) : min(p.region, static_cast<int64_t>(max(0, p.count[i])));
-  for (int j = 0; j < n; ++j) {
-    const int64_t row = first + j;
-    if (row < 0 || row >= p.x_rows || (!p.offset && j >= p.region) || before + j >= p.max_rows) {
-      flag(p.status, EP_ST_CAPACITY);
-      break;
-    }
-    float v = dot(p, e, m, row, lane);
-    if (p.glu) {
-      const float u = dot(p, e, m + outs, row, lane);
-      v = v / (1.0f + expf(-v)) * u;
-    }
-    if (lane == 0) reinterpret_cast<__nv_bfloat16*>(p.y)[row * outs + m] = __float2bfloat16(v);
+  const int per = (p.E + 31) / 32;
+  const int e0 = lane * per, e1 = min(p.E, e0 + per);
+  // This lane's experts: rows without the bound of max_rows.
+  int64_t rows = 0;
+  int64_t first;
+  for (int e = e0; e < e1; ++e) rows += rows_of(p, e, __ldg(p.count + e), first);
+  int64_t before = rows;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
   }
+  before -= rows;
+  int slots = 0, tiles = 0;
+  int64_t used = before;
+  for (int e = e0; e < e1; ++e) {
+    int n = rows_of(p, e, __ldg(p.count + e), first);
+    const int64_t left = p.max_rows - used;
+    used += n;
+    if (n > left) {
+      n = left > 0 ? static_cast<int>(left) : 0;
+      flag(p.status, EP_ST_CAPACITY);
+    }
+    slots += round8(n);
+    tiles += (n + q.tile_rows - 1) / q.tile_rows;
+  }
+  int slot0 = slots, tile0 = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, slot0, o), b = __shfl_up_sync(0xffffffffu, tile0, o);
+    if (lane >= o) {
+      slot0 += a;
+      tile0 += b;
+    }
+  }
+  slot0 -= slots;
+  tile0 -= tiles;
+  RowGroup g{-1, 0, 0, 0, 0, 0};
+  if (group * 8 >= slot0 && group * 8 < slot0 + slots) {
+    used = before;
+    for (int e = e0; e < e1; ++e) {
+      int n = rows_of(p, e, __ldg(p.count + e), first);
+      const int64_t left = p.max_rows - used;
+      used += n;
+      if (n > left) n = left > 0 ? static_cast<int>(left) : 0;
+      if (group * 8 < slot0 + round8(n)) {
+        g = RowGroup{e, n, first, group * 8 - slot0, slot0, tile0};
+        break;
+      }
+      slot0 += round8(n);
+      tile0 += (n + q.tile_rows - 1) / q.tile_rows;
+    }
+  }
+  const unsigned who = __ballot_sync(0xffffffffu, g.e >= 0);
+  const int src = who ? __ffs(who) - 1 : 0;
+  g.e = __shfl_sync(0xffffffffu, g.e, src);
+  g.n = __shfl_sync(0xffffffffu, g.n, src);
+  g.first = __shfl_sync(0xffffffffu, g.first, src);
+  g.row0 = __shfl_sync(0xffffffffu, g.row0, src);
+  g.slot0 = __shfl_sync(0xffffffffu, g.slot0, src);
+  g.tile0 = __shfl_sync(0xffffffffu, g.tile0, src);
+  return g;
+}
+
+// Bytes of the image in front of a tile, and the columns of the tile.
+__device__ __forceinline__ int tile_cols(const Params& q, int n, int tile) {
+  return round8(min(q.tile_rows, n - tile * q.tile_rows)) * q.mult;
+}
+__device__ __forceinline__ int64_t image_at(const Params& q, int slot0, int tile) {
+  return (static_cast<int64_t>(slot0) + static_cast<int64_t>(tile) * q.tile_rows) * q.mult * q.p.K;
+}
+// Scale bytes of a step of a tile: 512 for each 128 columns a tile can have.
+__device__ __forceinline__ int scale_bytes(const Params& q) { return q.cols_cap > 128 ? 2 * kScaleBytes : kScaleBytes; }
+
+__device__ __forceinline__ unsigned scale_place(int col) {
+  return static_cast<unsigned>((col >> 7) * kScaleBytes + (col & 31) * 16 + ((col >> 5) & 3) * 4);
+}
+
+constexpr int kRowThreads = 256;  // a warp for each of a group's eight rows
+constexpr int kRowSpan = 1024;    // inputs a block takes
+
+// Grid: (groups of eight rows, spans of inputs).
+__global__ void __launch_bounds__(kRowThreads) expert_rows_kernel(const Params q) {
+  const ExpertLinearParams& p = q.p;
+  grid_dependency_wait();
+  launch_dependents();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const RowGroup g = find_group(q, blockIdx.x);
+  if (g.e < 0) return;
+  const int j = g.row0 + w;  // row within the expert
+  const int tile = g.row0 / q.tile_rows, r = j - tile * q.tile_rows;
+  const int cols = tile_cols(q, g.n, tile), rows8 = cols / q.mult;
+  uint8_t* image = q.image + image_at(q, g.slot0, tile);
+  uint8_t* scales = q.image_scale + static_cast<int64_t>(g.tile0 + tile) * q.KB * scale_bytes(q);
+  const bool live = j < g.n;
+  const int64_t row = g.first + j;
+  const int k1 = min(p.K, (static_cast<int>(blockIdx.y) + 1) * kRowSpan);
+  // Column c of step kb, 16-byte piece `piece`.
+  auto place = [&](int kb, int c, int piece) {
+    return image + static_cast<int64_t>(kb) * cols * kStep + (c >> 3) * 1024 + (c & 7) * 128 + ((piece ^ (c & 7)) << 4);
+  };
+  if (p.x_scale) {
+    // E4M3: a lane moves 16 inputs, a step's scale byte serves its four groups.
+    for (int k = blockIdx.y * kRowSpan + lane * 16; k < k1; k += 512) {
+      const int kb = k / kStep;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (live) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + row * p.K + k));
+      *reinterpret_cast<uint4*>(place(kb, r, (k % kStep) >> 4)) = v;
+      if (k % kStep == 0) {
+        const uint32_t s = live ? __ldg(p.x_scale + row * q.KB + kb) : 127u;
+        *reinterpret_cast<uint32_t*>(scales + static_cast<int64_t>(kb) * scale_bytes(q) + scale_place(r)) = s * 0x01010101u;
+      }
+    }
+    return;
+  }
+  // BF16: a lane splits 8 inputs, four lanes share a scale. Both columns of a
+  // row: its high terms at r, its low terms at rows8 + r.
+  const int span = (k1 - static_cast<int>(blockIdx.y) * kRowSpan + 255) / 256;
+  for (int i = 0; i < span; ++i) {
+    const int k = blockIdx.y * kRowSpan + i * 256 + lane * 8;
+    const bool in = k < k1;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (live && in) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.K + k));
+    float x[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
+                  bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
+    float m = 0.0f;
+    bool finite[8];
+#pragma unroll
+    for (int a = 0; a < 8; ++a) {
+      finite[a] = fabsf(x[a]) <= 3.4028234663852886e38f;
+      if (finite[a]) m = fmaxf(m, fabsf(x[a]));
+    }
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    // The exponent of the smallest power of two >= m / 448, kept so that the
+    // low terms' scale, 2^-4 of it, is a normal number.
+    const uint32_t up = (__float_as_uint(__fdiv_rn(m, 448.0f)) + 0x007FFFFFu) >> 23;
+    const uint32_t b = up < 5u ? 5u : up;
+    const float inv = __uint_as_float((254u - b) << 23);
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      hi[h] = lo[h] = 0;
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const int at = 4 * h + 2 * a;
+        const float x0 = x[at] * inv, x1 = x[at + 1] * inv;
+        const uint32_t c = pack_e4m3x2(finite[at] ? x0 : __int_as_float(0x7FC00000), finite[at + 1] ? x1 : __int_as_float(0x7FC00000));
+        uint32_t f2;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f2) : "h"(static_cast<uint16_t>(c)));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f2));
+        hi[h] |= c << (16 * a);
+        lo[h] |= pack_e4m3x2((x0 - f.x) * 16.0f, (x1 - f.y) * 16.0f) << (16 * a);
+      }
+    }
+    // A step's four scale bytes, gathered into its first lane.
+    uint32_t s = b;
+#pragma unroll
+    for (int a = 1; a < 4; ++a) s |= __shfl_down_sync(0xffffffffu, b, 4 * a) << (8 * a);
+    if (!in) continue;
+    const int kb = k / kStep, piece = (k % kStep) >> 4, half = (k >> 3 & 1) * 8;
+    *reinterpret_cast<uint2*>(place(kb, r, piece) + half) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(place(kb, rows8 + r, piece) + half) = make_uint2(lo[0], lo[1]);
+    if ((lane & 15) == 0) {
+      uint8_t* at = scales + static_cast<int64_t>(kb) * scale_bytes(q);
+      *reinterpret_cast<uint32_t*>(at + scale_place(r)) = s;
+      *reinterpret_cast<uint32_t*>(at + scale_place(rows8 + r)) = s - 0x04040404u;
+    }
+  }
+}
+
+// ---- the products ------------------------------------------------------------------
+struct Shared {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint32_t tmem;
+  int last;                       // this block is the last to finish its shared unit
+  long long row_sum[kThreads / 32];
+  int slot_sum[kThreads / 32], tile_sum[kThreads / 32];
+  int tiles;                      // row tiles of all experts
+  int tile0[EP_MAX_EXPERTS + 1];  // row tiles of the experts before
+  int slot0[EP_MAX_EXPERTS];      // rows, rounded up to 8, of the experts before
+  int rows[EP_MAX_EXPERTS];
+  float swap[2][8][64];           // GLU: ups on their way to the gates' threads
+};
+
+// A run of steps of one unit.
+struct Segment {
+  int e, tile, mt;
+  int k0, k1;     // steps
+  int cols;       // columns of its tile
+  int rows;       // rows of its tile
+  int64_t unit;
+};
+
+struct Run {  // a block's steps: positions [at, end) of units * KB
+  int64_t at, end;
+};
+
+__device__ __forceinline__ int64_t run_begin(int64_t total, int blocks, int c) { return total * c / blocks; }
+// The block that owns position i.
+__device__ __forceinline__ int owner_of(int64_t total, int blocks, int64_t i) {
+  return static_cast<int>(((i + 1) * blocks + total - 1) / total) - 1;
+}
+
+__device__ bool next_segment(const Params& q, const Shared& sh, Run& run, Segment& s) {
+  if (run.at >= run.end) return false;
+  s.unit = run.at / q.KB;
+  s.k0 = static_cast<int>(run.at - s.unit * q.KB);
+  s.k1 = static_cast<int>(min(static_cast<int64_t>(q.KB), s.k0 + (run.end - run.at)));
+  run.at += s.k1 - s.k0;
+  const int t = static_cast<int>(s.unit / q.MT);
+  int lo = 0, hi = q.p.E;  // the last expert with tile0 <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (sh.tile0[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  s.e = lo;
+  const int tiles = sh.tile0[lo + 1] - sh.tile0[lo];
+  // Tiles of one (expert, outputs) follow one another, so that its weights
+  // come from L2 after the first.
+  const int u = static_cast<int>(s.unit - static_cast<int64_t>(sh.tile0[lo]) * q.MT);
+  s.mt = u / tiles;
+  s.tile = u - s.mt * tiles;
+  s.rows = min(q.tile_rows, sh.rows[lo] - s.tile * q.tile_rows);
+  s.cols = round8(s.rows) * q.mult;
+  return true;
+}
+
+// Counts -> tiles, by the whole block.
+__device__ void tile_experts(const Params& q, Shared& sh) {
+  const ExpertLinearParams& p = q.p;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int per = (p.E + kThreads - 1) / kThreads;
+  const int e0 = min(p.E, tid * per), e1 = min(p.E, e0 + per);
+  int mine[EP_MAX_EXPERTS / kThreads];
+  int64_t first;
+  long long rows = 0;
+#pragma unroll
+  for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i) {
+    mine[i] = e0 + i < e1 ? rows_of(p, e0 + i, __ldg(p.count + e0 + i), first) : 0;
+    rows += mine[i];
+  }
+  auto scan = [&](auto v, auto* sums) {  // exclusive over the block
+    auto s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const auto u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane == 31) sums[w] = s;
+    __syncthreads();
+    auto before = s - v;
+    for (int i = 0; i < w; ++i) before += sums[i];
+    return before;
+  };
+  // Rows are counted in 64 bits up to max_rows; what is left of them fits 27.
+  long long used = scan(rows, sh.row_sum);
+  int slots = 0, tiles = 0;
+#pragma unroll
+  for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i) {
+    const long long left = used < p.max_rows ? p.max_rows - used : 0;
+    used += mine[i];
+    if (mine[i] > left) mine[i] = static_cast<int>(left);
+    slots += round8(mine[i]);
+    tiles += (mine[i] + q.tile_rows - 1) / q.tile_rows;
+  }
+  int s0 = scan(slots, sh.slot_sum), t0 = scan(tiles, sh.tile_sum);
+#pragma unroll
+  for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i) {
+    if (e0 + i < e1) {
+      sh.rows[e0 + i] = mine[i];
+      sh.slot0[e0 + i] = s0;
+      sh.tile0[e0 + i] = t0;
+    }
+    s0 += round8(mine[i]);
+    t0 += (mine[i] + q.tile_rows - 1) / q.tile_rows;
+  }
+  if (tid == kThreads - 1) sh.tile0[p.E] = sh.tiles = t0;
+  __syncthreads();
+}
+
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
+                                                                 const __grid_constant__ CUtensorMap map) {
+  extern __shared__ uint8_t dynamic[];
+  // The stages start on a 1024-byte boundary (the swizzle's period).
+  uint8_t* smem = dynamic + (1024 - (smem_addr(dynamic) & 1023)) % 1024;
+  __shared__ Shared sh;
+  const ExpertLinearParams& p = q.p;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < q.stages; ++i) {
+      mbar_init(&sh.full[i], 2);  // the loads, and the weights' scales
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.acc_full[i], 1);
+      mbar_init(&sh.acc_empty[i], 128);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 3) tmem_alloc(&sh.tmem, kTmemCols);
+  // The counts are older than the rows kernel, which released this one only
+  // once everything before it had completed.
+  tile_experts(q, sh);  // (ends with a block barrier)
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int64_t total = static_cast<int64_t>(sh.tiles) * q.MT * q.KB;
+  const int outs = p.glu ? p.M / 2 : p.M;
+  // Every block that takes part has steps: the join counts on it.
+  const int blocks = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(total / kMinSteps, int64_t{1})));
+  Run run{0, 0};
+  if (blockIdx.x < blocks) run = Run{run_begin(total, blocks, blockIdx.x), run_begin(total, blocks, blockIdx.x + 1)};
+  const int sbytes = scale_bytes(q);
+  // A stage: weights, their scales, the rows' scales, the rows.
+  auto stage_w = [&](int s) { return smem + static_cast<size_t>(s) * q.stage_bytes; };
+  auto stage_x = [&](int s) { return stage_w(s) + kTileBytes; };
+  auto stage_ws = [&](int s) { return stage_x(s) + static_cast<size_t>(q.cols_cap) * kStep; };
+  auto stage_xs = [&](int s) { return stage_ws(s) + kScaleBytes; };
+  // First output row of half h (64 rows) of a unit's weights.
+  auto out_row = [&](int mt, int h) { return p.glu ? mt * 64 + h * outs : mt * kTileM + h * 64; };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // Loads. The rows' part waits for the rows kernel, the first stages'
+      // weights do not.
+      auto load_w = [&](const Segment& g, int kb, int s) {
+        const unsigned bytes = kTileTx + g.cols * kStep + sbytes;
+        mbar_arrive_expect_tx(&sh.full[s], bytes);
+        tma_load_3d(stage_w(s), &map, kb * kStep, out_row(g.mt, 0), g.e, &sh.full[s]);
+        tma_load_3d(stage_w(s) + kTileBytes / 2, &map, kb * kStep, out_row(g.mt, 1), g.e, &sh.full[s]);
+      };
+      auto load_x = [&](const Segment& g, int kb, int s) {
+        bulk_g2s(stage_x(s), q.image + image_at(q, sh.slot0[g.e], g.tile) + static_cast<int64_t>(kb) * g.cols * kStep,
+                 g.cols * kStep, &sh.full[s]);
+        bulk_g2s(stage_xs(s),
+                 q.image_scale + (static_cast<int64_t>(sh.tile0[g.e] + g.tile) * q.KB + kb) * sbytes, sbytes,
+                 &sh.full[s]);
+      };
+      const Run start = run;
+      Segment g;
+      int it = 0;
+      while (it < q.stages && next_segment(q, sh, run, g))
+        for (int kb = g.k0; kb < g.k1 && it < q.stages; ++kb, ++it) load_w(g, kb, it);
+      grid_dependency_wait();
+      const int ahead = it;
+      run = start;
+      it = 0;
+      bool ok = true;
+      while (ok && next_segment(q, sh, run, g)) {
+        for (int kb = g.k0; kb < g.k1; ++kb, ++it) {
+          const int s = it % q.stages;
+          if (it >= ahead) {
+            if (it >= q.stages && !mbar_wait(&sh.empty[s], (it / q.stages - 1) & 1, p.status)) {
+              ok = false;
+              break;
+            }
+            load_w(g, kb, s);
+          }
+          load_x(g, kb, s);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // Products.
+      Segment g;
+      int it = 0, seg = 0;
+      bool ok = true;
+      while (ok && next_segment(q, sh, run, g)) {
+        const int buf = seg & 1;
+        if (seg >= 2 && !mbar_wait(&sh.acc_empty[buf], (seg / 2 - 1) & 1, p.status)) break;
+        tmem_fence_after();
+        const uint32_t d = tmem + buf * kMaxCols;
+        const uint32_t idesc = idesc_e2m1_e4m3(g.cols);
+        for (int kb = g.k0; kb < g.k1; ++kb, ++it) {
+          const int s = it % q.stages;
+          if (!mbar_wait(&sh.full[s], (it / q.stages) & 1, p.status)) {
+            ok = false;
+            break;
+          }
+          tmem_fence_after();
+          const uint32_t sc = tmem + kTmemScales + (it % kScaleSlots) * kScaleCols;
+          const uint32_t xs = smem_addr(stage_xs(s));
+          tmem_copy_scales(sc, desc_rows16(smem_addr(stage_ws(s))));
+          tmem_copy_scales(sc + 4, desc_rows16(xs));
+          if (g.cols > 128) tmem_copy_scales(sc + 8, desc_rows16(xs + kScaleBytes));
+          const uint64_t a = desc_rows128(smem_addr(stage_w(s))), b = desc_rows128(smem_addr(stage_x(s)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // 32 inputs: 32 bytes on, 2 in the descriptors' units
+            mma_scaled(d, a + 2 * i, b + 2 * i, idesc_scale_byte(idesc, i), sc, sc + 4, kb > g.k0 || i > 0);
+          mma_commit(&sh.empty[s]);
+        }
+        mma_commit(&sh.acc_full[buf]);
+        ++seg;
+      }
+    }
+  } else if (warp == 2) {
+    // The weights' scales: four bytes a row and step, laid out for the copy to
+    // tensor memory (row r: place r % 32, word r / 32).
+    Segment g;
+    int it = 0;
+    bool ok = true;
+    const int64_t pitch = p.K / 32;
+    while (ok && next_segment(q, sh, run, g)) {
+      const uint8_t* src[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = out_row(g.mt, i / 2) + (i & 1) * 32 + lane;
+        src[i] = m < p.M ? p.w_scale + (static_cast<int64_t>(g.e) * p.M + m) * pitch : nullptr;
+      }
+      constexpr int kAhead = 4;
+      uint32_t v[kAhead][4];
+      auto fetch = [&](uint32_t* to, int kb) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          to[i] = src[i] && kb < g.k1 ? __ldg(reinterpret_cast<const uint32_t*>(src[i]) + kb) : 0x7F7F7F7Fu;
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) fetch(v[i], g.k0 + i);
+      for (int kb0 = g.k0; ok && kb0 < g.k1; kb0 += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (kb0 + i >= g.k1) break;
+          const int s = it % q.stages;
+          if (it >= q.stages && !mbar_wait(&sh.empty[s], (it / q.stages - 1) & 1, p.status)) {
+            ok = false;
+            break;
+          }
+          reinterpret_cast<uint4*>(stage_ws(s))[lane] = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.full[s]);
+          ++it;
+          fetch(v[i], kb0 + i + kAhead);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+    }
+  } else if (warp >= 4) {
+    // Results: thread m holds output row m of the unit's 128, a column a row of x.
+    const int m = tid - 128;
+    grid_dependency_wait();
+    Segment g;
+    int seg = 0;
+    while (next_segment(q, sh, run, g)) {
+      const int buf = seg & 1;
+      if (!mbar_wait(&sh.acc_full[buf], (seg / 2) & 1, p.status)) break;
+      ++seg;
+      tmem_fence_after();
+      const uint32_t acc = tmem + buf * kMaxCols + (static_cast<uint32_t>(warp & 3) << 21);
+      const int rows8 = round8(g.rows);
+      const bool whole = g.k0 == 0 && g.k1 == q.KB;
+      const int64_t base = p.offset ? static_cast<int64_t>(__ldg(p.offset + g.e)) : g.e * p.region;
+      const int64_t row0 = base + g.tile * q.tile_rows;
+      const int o = p.glu ? g.mt * 64 + (m & 63) : g.mt * kTileM + m;
+      auto slot = [&](int block, bool starts) {
+        return q.partial + (static_cast<int64_t>(block) * 2 + (starts ? 1 : 0)) * q.tile_rows * kTileM;
+      };
+      // Eight finished sums of this thread's output row: to y.
+      auto finish = [&](float* v, int c0) {
+        if (p.glu) {
+          float(*swap)[64] = sh.swap[(c0 >> 3) & 1];
+          if (m >= 64) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) swap[i][m - 64] = v[i];
+          }
+          epilogue_sync();
+          if (m >= 64) return;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * swap[i][m];
+        }
+        if (o >= outs) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c0 + i < g.rows)
+            reinterpret_cast<__nv_bfloat16*>(p.y)[(row0 + c0 + i) * outs + o] = __float2bfloat16(v[i]);
+      };
+      float* mine = slot(blockIdx.x, g.k0 == 0);
+      for (int c0 = 0; c0 < rows8; c0 += 8) {
+        float v[8];
+        tmem_load8(v, acc + c0);
+        if (q.mult == 2) {
+          float l[8];
+          tmem_load8(l, acc + rows8 + c0);
+          tmem_wait_load();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += l[i];
+        } else {
+          tmem_wait_load();
+        }
+        if (whole) {
+          finish(v, c0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) __stcg(mine + (c0 + i) * kTileM + m, v[i]);
+        }
+      }
+      tmem_fence_before();
+      mbar_arrive(&sh.acc_empty[buf]);
+      if (whole) {
+        if (p.glu) epilogue_sync();  // the swap buffers are free again
+        continue;
+      }
+      // A shared unit: the last block to arrive adds the parts, in order.
+      const int c_first = owner_of(total, blocks, g.unit * q.KB);
+      const int c_last = owner_of(total, blocks, (g.unit + 1) * q.KB - 1);
+      __threadfence();
+      epilogue_sync();
+      if (m == 0) {
+        const unsigned old = atomicAdd(&q.counters[c_first], 1u);
+        const bool last = old == static_cast<unsigned>(c_last - c_first);
+        if (last) q.counters[c_first] = 0u;
+        sh.last = last;
+      }
+      epilogue_sync();
+      if (sh.last) {
+        __threadfence();
+        for (int c0 = 0; c0 < rows8; c0 += 8) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __ldcg(slot(c_first, true) + (c0 + i) * kTileM + m);
+          for (int b = c_first + 1; b <= c_last; ++b) {
+            const float* part = slot(b, false);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += __ldcg(part + (c0 + i) * kTileM + m);
+          }
+          finish(v, c0);
+        }
+      }
+      epilogue_sync();  // sh.last and the swap buffers are free again
+    }
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 3) {
+    tmem_fence_after();
+    tmem_free(tmem, kTmemCols);
+  }
+}
+
+// Rows of a full tile: enough for nearly every expert's rows in one tile (the
+// mean and four standard deviations of a random routing), so that weights are
+// not read again, and no more, since a smaller tile leaves room for more
+// stages of weights in flight.
+int tile_rows_for(int E, int64_t max_rows, int mult) {
+  const int64_t active = std::max<int64_t>(1, std::min<int64_t>(E, max_rows));
+  const int64_t mean = (max_rows + active - 1) / active;
+  int64_t sd4 = 4;
+  while (sd4 * sd4 < 16 * mean) ++sd4;
+  const int caps[] = {16, 32, 64, 128, kMaxCols};
+  for (int cap : caps)
+    if (cap / mult >= mean + sd4) return cap / mult;
+  return kMaxCols / mult;
+}
+
+struct Sizes {
+  int tile_rows;
+  size_t counters, partial, scale, image, total;
+};
+
+Sizes sizes_of(int E, int64_t max_rows, int K, bool fp8) {
+  const int mult = fp8 ? 1 : 2;
+  Sizes z{};
+  z.tile_rows = tile_rows_for(E, max_rows, mult);
+  auto up = [](size_t v) { return (v + 1023) & ~static_cast<size_t>(1023); };
+  const int64_t active = std::min<int64_t>(E, max_rows);
+  const int64_t slots = max_rows + 7 * active;
+  const int64_t tiles = max_rows / z.tile_rows + active;
+  const int sb = z.tile_rows * mult > 128 ? 2 * kScaleBytes : kScaleBytes;
+  z.counters = 0;
+  z.partial = 1024;
+  z.scale = z.partial + up(sizeof(float) * kMaxBlocks * 2 * z.tile_rows * kTileM);
+  z.image = z.scale + up(static_cast<size_t>(tiles) * (K / kStep) * sb);
+  z.total = z.image + up(static_cast<size_t>(slots) * mult * K);
+  return z;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12080, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
 }
 
 }  // namespace
 
-size_t expert_linear_ws_bytes(int, int64_t, int, bool) { return 256; }
+size_t expert_linear_ws_bytes(int E, int64_t max_rows, int K, bool fp8) { return sizes_of(E, max_rows, K, fp8).total; }
 
 cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   if (p.max_rows <= 0 || p.x_rows <= 0) return cudaSuccess;
-  const int outs = p.glu ? p.M / 2 : p.M;
-  return launch_kernel(expert_linear_kernel, dim3((outs + 3) / 4, p.E), dim3(kThreads), 0, s, /*dependent=*/true, p);
+  const bool fp8 = p.x_scale != nullptr;
+  const Sizes z = sizes_of(p.E, p.max_rows, p.K, fp8);
+  Params q{};
+  q.p = p;
+  q.mult = fp8 ? 1 : 2;
+  q.tile_rows = z.tile_rows;
+  q.cols_cap = z.tile_rows * q.mult;
+  q.KB = p.K / kStep;
+  q.MT = p.glu ? (p.M / 2 + 63) / 64 : (p.M + kTileM - 1) / kTileM;
+  q.counters = reinterpret_cast<unsigned*>(p.ws + z.counters);
+  q.partial = reinterpret_cast<float*>(p.ws + z.partial);
+  q.image_scale = p.ws + z.scale;
+  q.image = p.ws + z.image;
+  const int sb = q.cols_cap > 128 ? 2 * kScaleBytes : kScaleBytes;
+  q.stage_bytes = (kTileBytes + q.cols_cap * kStep + kScaleBytes + sb + 1023) / 1024 * 1024;
+  constexpr unsigned kSmem = 227 * 1024 - sizeof(Shared) - 2048;
+  q.stages = std::min<int>(kMaxStages, kSmem / q.stage_bytes);
+  const size_t smem = static_cast<size_t>(q.stages) * q.stage_bytes + 1024;
+
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return cudaErrorNotSupported;
+  CUtensorMap map;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.M), static_cast<cuuint64_t>(p.E)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.K) / 2, static_cast<cuuint64_t>(p.M) * p.K / 2};
+  const cuuint32_t box[3] = {kStep, 64, 1}, ones[3] = {1, 1, 1};
+  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<uint8_t*>(p.w), dims, strides, box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+
+  const int dev = current_device();
+  const void* fn = reinterpret_cast<const void*>(expert_linear_kernel);
+  cudaError_t err = ensure_dynamic_smem(fn, dev, smem);
+  if (err != cudaSuccess) return err;
+  const int sms = device_sms(dev);
+  if (sms < 1) return cudaErrorInvalidDevice;
+  const int64_t groups = (p.max_rows + 7 * std::min<int64_t>(p.E, p.max_rows)) / 8;
+  err = launch_kernel(expert_rows_kernel, dim3(static_cast<unsigned>(groups), (p.K + kRowSpan - 1) / kRowSpan),
+                      dim3(kRowThreads), 0, s, /*dependent=*/true, q);
+  if (err != cudaSuccess) return err;
+  return launch_kernel(expert_linear_kernel, dim3(std::min(sms, kMaxBlocks)), dim3(kThreads), smem, s,
+                       /*dependent=*/true, q, map);
 }
 
 }  // namespace ep

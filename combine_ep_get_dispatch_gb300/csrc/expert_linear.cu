@@ -36,6 +36,7 @@ constexpr int kStep = 128;                  // inputs a step
 constexpr int kTileM = 128;                 // outputs a unit (with GLU: 64 gates, 64 ups)
 constexpr int kTileBytes = kTileM * kStep;  // weights of a step in shared memory (8-bit containers)
 constexpr int kTileTx = kTileBytes / 2;     // ... and as TMA counts them
+constexpr int kStageSteps = 2;              // steps a stage holds
 constexpr int kScaleBytes = 512;            // scale bytes of 128 rows for one step
 constexpr int kMaxCols = 192;
 constexpr int kMaxBlocks = 160;             // blocks a workspace has room for
@@ -43,8 +44,8 @@ constexpr int kThreads = 256;
 constexpr int kMaxStages = 12;
 constexpr int kTmemCols = 512;              // two accumulators of kMaxCols, then scales
 constexpr int kTmemScales = 2 * kMaxCols;
-constexpr int kScaleSlots = 4;              // steps whose scales tensor memory holds
-constexpr int kMinSteps = 4;                // fewest steps worth a block of their own
+constexpr int kScaleGroups = 6;              // groups of four steps of the weights' scales in shared memory
+constexpr int kMinStages = 2;               // fewest stages worth a block of their own
 constexpr int kScaleCols = 12;              // columns a step: 4 of the weights', 8 of the rows'
 
 struct Params {
@@ -53,13 +54,14 @@ struct Params {
   int tile_rows;    // rows of a full tile
   int cols_cap;     // its columns
   int KB;           // steps of a unit: K / 128
+  int KS;           // stages of a unit: two steps each, the last one perhaps one
   int MT;           // units of a tile: output tiles of an expert
   int stages;
   unsigned stage_bytes;
+  int scale_bytes;     // of a step's rows: 512 for each 128 columns that a tile can have
   unsigned* counters;  // [kMaxBlocks]
   float* partial;      // [kMaxBlocks][2][tile_rows][kTileM]
-  uint8_t* image;      // rows of x as shared memory holds them
-  uint8_t* image_scale;
+  uint8_t* image;      // rows of x, step by step as shared memory holds them: codes, then scales
 };
 
 __device__ __forceinline__ int round8(int v) { return (v + 7) & ~7; }
@@ -160,11 +162,10 @@ __device__ RowGroup find_group(const Params& q, int group) {
 __device__ __forceinline__ int tile_cols(const Params& q, int n, int tile) {
   return round8(min(q.tile_rows, n - tile * q.tile_rows)) * q.mult;
 }
-__device__ __forceinline__ int64_t image_at(const Params& q, int slot0, int tile) {
-  return (static_cast<int64_t>(slot0) + static_cast<int64_t>(tile) * q.tile_rows) * q.mult * q.p.K;
+__device__ __forceinline__ int64_t image_at(const Params& q, int slot0, int tile0, int tile) {
+  return (static_cast<int64_t>(slot0) + static_cast<int64_t>(tile) * q.tile_rows) * q.mult * q.p.K +
+         static_cast<int64_t>(tile0 + tile) * q.KB * q.scale_bytes;
 }
-// Scale bytes of a step of a tile: 512 for each 128 columns a tile can have.
-__device__ __forceinline__ int scale_bytes(const Params& q) { return q.cols_cap > 128 ? 2 * kScaleBytes : kScaleBytes; }
 
 __device__ __forceinline__ unsigned scale_place(int col) {
   return static_cast<unsigned>((col >> 7) * kScaleBytes + (col & 31) * 16 + ((col >> 5) & 3) * 4);
@@ -184,14 +185,20 @@ __global__ void __launch_bounds__(kRowThreads) expert_rows_kernel(const Params q
   const int j = g.row0 + w;  // row within the expert
   const int tile = g.row0 / q.tile_rows, r = j - tile * q.tile_rows;
   const int cols = tile_cols(q, g.n, tile), rows8 = cols / q.mult;
-  uint8_t* image = q.image + image_at(q, g.slot0, tile);
-  uint8_t* scales = q.image_scale + static_cast<int64_t>(g.tile0 + tile) * q.KB * scale_bytes(q);
+  uint8_t* image = q.image + image_at(q, g.slot0, g.tile0, tile);
+  // Of a stage's two steps (or the last one alone): their codes, then their scales.
+  auto stage = [&](int kb) {
+    return image + static_cast<int64_t>(kb / kStageSteps) * kStageSteps * (cols * kStep + q.scale_bytes);
+  };
+  auto scales = [&](int kb) {
+    return stage(kb) + ((kb | 1) < q.KB ? kStageSteps : 1) * cols * kStep + kb % kStageSteps * q.scale_bytes;
+  };
   const bool live = j < g.n;
   const int64_t row = g.first + j;
   const int k1 = min(p.K, (static_cast<int>(blockIdx.y) + 1) * kRowSpan);
   // Column c of step kb, 16-byte piece `piece`.
   auto place = [&](int kb, int c, int piece) {
-    return image + static_cast<int64_t>(kb) * cols * kStep + (c >> 3) * 1024 + (c & 7) * 128 + ((piece ^ (c & 7)) << 4);
+    return stage(kb) + kb % kStageSteps * cols * kStep + (c >> 3) * 1024 + (c & 7) * 128 + ((piece ^ (c & 7)) << 4);
   };
   if (p.x_scale) {
     // E4M3: a lane moves 16 inputs, a step's scale byte serves its four groups.
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(kRowThreads) expert_rows_kernel(const Params q
       *reinterpret_cast<uint4*>(place(kb, r, (k % kStep) >> 4)) = v;
       if (k % kStep == 0) {
         const uint32_t s = live ? __ldg(p.x_scale + row * q.KB + kb) : 127u;
-        *reinterpret_cast<uint32_t*>(scales + static_cast<int64_t>(kb) * scale_bytes(q) + scale_place(r)) = s * 0x01010101u;
+        *reinterpret_cast<uint32_t*>(scales(kb) + scale_place(r)) = s * 0x01010101u;
       }
     }
     return;
@@ -256,7 +263,7 @@ __global__ void __launch_bounds__(kRowThreads) expert_rows_kernel(const Params q
     *reinterpret_cast<uint2*>(place(kb, r, piece) + half) = make_uint2(hi[0], hi[1]);
     *reinterpret_cast<uint2*>(place(kb, rows8 + r, piece) + half) = make_uint2(lo[0], lo[1]);
     if ((lane & 15) == 0) {
-      uint8_t* at = scales + static_cast<int64_t>(kb) * scale_bytes(q);
+      uint8_t* at = scales(kb);
       *reinterpret_cast<uint32_t*>(at + scale_place(r)) = s;
       *reinterpret_cast<uint32_t*>(at + scale_place(rows8 + r)) = s - 0x04040404u;
     }
@@ -266,6 +273,7 @@ __global__ void __launch_bounds__(kRowThreads) expert_rows_kernel(const Params q
 // ---- the products ------------------------------------------------------------------
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t scale_full[kScaleGroups], scale_empty[kScaleGroups];
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem;
   int last;                       // this block is the last to finish its shared unit
@@ -281,14 +289,31 @@ struct Shared {
 // A run of steps of one unit.
 struct Segment {
   int e, tile, mt;
-  int k0, k1;     // steps
+  int s0, s1;     // stages
   int cols;       // columns of its tile
   int rows;       // rows of its tile
+  int slot0, tile0;  // the expert's (see Shared)
   int64_t unit;
 };
 
-struct Run {  // a block's steps: positions [at, end) of units * KB
+struct Run {  // a block's stages: positions [at, end) of units * KS
   int64_t at, end;
+};
+
+// A place in the ring of stages: the stage, its shared-memory address and the
+// parity of its current use.
+struct Ring {
+  int stage = 0;
+  unsigned parity = 0;
+  unsigned offset = 0;
+  __device__ __forceinline__ void advance(const Params& q) {
+    offset += q.stage_bytes;
+    if (++stage == q.stages) {
+      stage = 0;
+      offset = 0;
+      parity ^= 1;
+    }
+  }
 };
 
 __device__ __forceinline__ int64_t run_begin(int64_t total, int blocks, int c) { return total * c / blocks; }
@@ -297,12 +322,13 @@ __device__ __forceinline__ int owner_of(int64_t total, int blocks, int64_t i) {
   return static_cast<int>(((i + 1) * blocks + total - 1) / total) - 1;
 }
 
-__device__ bool next_segment(const Params& q, const Shared& sh, Run& run, Segment& s) {
+// The next run of steps of one unit, by a whole warp.
+__device__ __forceinline__ bool next_segment(const Params& q, const Shared& sh, Run& run, Segment& s) {
   if (run.at >= run.end) return false;
-  s.unit = run.at / q.KB;
-  s.k0 = static_cast<int>(run.at - s.unit * q.KB);
-  s.k1 = static_cast<int>(min(static_cast<int64_t>(q.KB), s.k0 + (run.end - run.at)));
-  run.at += s.k1 - s.k0;
+  s.unit = run.at / q.KS;
+  s.s0 = static_cast<int>(run.at - s.unit * q.KS);
+  s.s1 = static_cast<int>(min(static_cast<int64_t>(q.KS), s.s0 + (run.end - run.at)));
+  run.at += s.s1 - s.s0;
   const int t = static_cast<int>(s.unit / q.MT);
   int lo = 0, hi = q.p.E;  // the last expert with tile0 <= t
   while (hi - lo > 1) {
@@ -310,14 +336,16 @@ __device__ bool next_segment(const Params& q, const Shared& sh, Run& run, Segmen
     if (sh.tile0[mid] <= t) lo = mid;
     else hi = mid;
   }
-  s.e = lo;
-  const int tiles = sh.tile0[lo + 1] - sh.tile0[lo];
+  s.e = lo = uniform(lo);
+  s.slot0 = uniform(sh.slot0[lo]);
+  s.tile0 = uniform(sh.tile0[lo]);
+  const int tiles = uniform(sh.tile0[lo + 1]) - s.tile0;
   // Tiles of one (expert, outputs) follow one another, so that its weights
   // come from L2 after the first.
-  const int u = static_cast<int>(s.unit - static_cast<int64_t>(sh.tile0[lo]) * q.MT);
+  const int u = static_cast<int>(s.unit - static_cast<int64_t>(s.tile0) * q.MT);
   s.mt = u / tiles;
   s.tile = u - s.mt * tiles;
-  s.rows = min(q.tile_rows, sh.rows[lo] - s.tile * q.tile_rows);
+  s.rows = min(q.tile_rows, uniform(sh.rows[lo]) - s.tile * q.tile_rows);
   s.cols = round8(s.rows) * q.mult;
   return true;
 }
@@ -384,11 +412,15 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
   uint8_t* smem = dynamic + (1024 - (smem_addr(dynamic) & 1023)) % 1024;
   __shared__ Shared sh;
   const ExpertLinearParams& p = q.p;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   if (tid == 0) {
     for (int i = 0; i < q.stages; ++i) {
-      mbar_init(&sh.full[i], 2);  // the loads, and the weights' scales
+      mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < kScaleGroups; ++i) {
+      mbar_init(&sh.scale_full[i], 1);
+      mbar_init(&sh.scale_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.acc_full[i], 1);
@@ -403,137 +435,199 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  const uint32_t tmem = sh.tmem;
-  const int64_t total = static_cast<int64_t>(sh.tiles) * q.MT * q.KB;
+  const uint32_t tmem = uniform(sh.tmem);
+  const int64_t total = static_cast<int64_t>(uniform(sh.tiles)) * q.MT * q.KS;
   const int outs = p.glu ? p.M / 2 : p.M;
   // Every block that takes part has steps: the join counts on it.
-  const int blocks = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(total / kMinSteps, int64_t{1})));
+  const int blocks = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(total / kMinStages, int64_t{1})));
   Run run{0, 0};
   if (blockIdx.x < blocks) run = Run{run_begin(total, blocks, blockIdx.x), run_begin(total, blocks, blockIdx.x + 1)};
-  const int sbytes = scale_bytes(q);
-  // A stage: weights, their scales, the rows' scales, the rows.
-  auto stage_w = [&](int s) { return smem + static_cast<size_t>(s) * q.stage_bytes; };
-  auto stage_x = [&](int s) { return stage_w(s) + kTileBytes; };
-  auto stage_ws = [&](int s) { return stage_x(s) + static_cast<size_t>(q.cols_cap) * kStep; };
-  auto stage_xs = [&](int s) { return stage_ws(s) + kScaleBytes; };
+  // A stage: weights, rows, the rows' scales. Behind the stages: the ring of
+  // the weights' scales.
+  constexpr unsigned x_at = kStageSteps * kTileBytes;
+  const unsigned ws_at = q.stages * q.stage_bytes;
   // First output row of half h (64 rows) of a unit's weights.
   auto out_row = [&](int mt, int h) { return p.glu ? mt * 64 + h * outs : mt * kTileM + h * 64; };
 
   if (warp == 0) {
-    if (lane == 0) {
-      // Loads. The rows' part waits for the rows kernel, the first stages'
-      // weights do not.
-      auto load_w = [&](const Segment& g, int kb, int s) {
-        const unsigned bytes = kTileTx + g.cols * kStep + sbytes;
-        mbar_arrive_expect_tx(&sh.full[s], bytes);
-        tma_load_3d(stage_w(s), &map, kb * kStep, out_row(g.mt, 0), g.e, &sh.full[s]);
-        tma_load_3d(stage_w(s) + kTileBytes / 2, &map, kb * kStep, out_row(g.mt, 1), g.e, &sh.full[s]);
-      };
-      auto load_x = [&](const Segment& g, int kb, int s) {
-        bulk_g2s(stage_x(s), q.image + image_at(q, sh.slot0[g.e], g.tile) + static_cast<int64_t>(kb) * g.cols * kStep,
-                 g.cols * kStep, &sh.full[s]);
-        bulk_g2s(stage_xs(s),
-                 q.image_scale + (static_cast<int64_t>(sh.tile0[g.e] + g.tile) * q.KB + kb) * sbytes, sbytes,
-                 &sh.full[s]);
-      };
-      const Run start = run;
-      Segment g;
-      int it = 0;
-      while (it < q.stages && next_segment(q, sh, run, g))
-        for (int kb = g.k0; kb < g.k1 && it < q.stages; ++kb, ++it) load_w(g, kb, it);
-      grid_dependency_wait();
-      const int ahead = it;
-      run = start;
-      it = 0;
-      bool ok = true;
-      while (ok && next_segment(q, sh, run, g)) {
-        for (int kb = g.k0; kb < g.k1; ++kb, ++it) {
-          const int s = it % q.stages;
-          if (it >= ahead) {
-            if (it >= q.stages && !mbar_wait(&sh.empty[s], (it / q.stages - 1) & 1, p.status)) {
-              ok = false;
-              break;
-            }
-            load_w(g, kb, s);
-          }
-          load_x(g, kb, s);
+    // Loads. The rows' part waits for the rows kernel, the first stages'
+    // weights do not. (The instructions of a stage are what this loop costs:
+    // one load of weights, one of rows, addresses advanced, none computed anew.)
+    auto load_w = [&](const Segment& g, int st, unsigned bytes, const Ring& r) {
+      uint64_t* bar = &sh.full[r.stage];
+      mbar_arrive_expect_tx(bar, bytes);
+      tma_load_5d(smem + r.offset, &map, 0, out_row(g.mt, 0), 0, st * kStageSteps, g.e, bar);
+    };
+    // Bytes of rows in a stage: the last one of an odd number of steps holds one.
+    auto x_bytes = [&](int st, unsigned step) { return st * kStageSteps + 1 < q.KB ? 2 * step : step; };
+    const Run start = run;
+    Segment g;
+    Ring r;
+    int ahead = 0;
+    while (ahead < q.stages && next_segment(q, sh, run, g)) {
+      const unsigned step = g.cols * kStep + q.scale_bytes;
+      for (int st = g.s0; st < g.s1 && ahead < q.stages; ++st, ++ahead) {
+        if (elect_one()) load_w(g, st, kStageSteps * kTileTx + x_bytes(st, step), r);
+        r.advance(q);
+      }
+    }
+    grid_dependency_wait();
+    run = start;
+    r = Ring{};
+    unsigned round = 0;  // passes over the ring
+    bool ok = true;
+    while (ok && next_segment(q, sh, run, g)) {
+      const unsigned step = g.cols * kStep + q.scale_bytes;
+      const uint8_t* x =
+          q.image + image_at(q, g.slot0, g.tile0, g.tile) + static_cast<int64_t>(g.s0) * kStageSteps * step;
+      for (int st = g.s0; st < g.s1; ++st) {
+        const bool loaded = ahead > 0;
+        if (loaded) {
+          --ahead;
+        } else if (round > 0 && !mbar_wait_warp(&sh.empty[r.stage], r.parity ^ 1, p.status)) {
+          ok = false;
+          break;
         }
+        if (elect_one()) {
+          const unsigned bytes = x_bytes(st, step);
+          if (!loaded) load_w(g, st, kStageSteps * kTileTx + bytes, r);
+          bulk_g2s(smem + r.offset + x_at, x, bytes, &sh.full[r.stage]);
+        }
+        x += kStageSteps * step;
+        r.advance(q);
+        if (r.stage == 0) round = 1;
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // Products.
-      Segment g;
-      int it = 0, seg = 0;
-      bool ok = true;
-      while (ok && next_segment(q, sh, run, g)) {
-        const int buf = seg & 1;
-        if (seg >= 2 && !mbar_wait(&sh.acc_empty[buf], (seg / 2 - 1) & 1, p.status)) break;
-        tmem_fence_after();
-        const uint32_t d = tmem + buf * kMaxCols;
-        const uint32_t idesc = idesc_e2m1_e4m3(g.cols);
-        for (int kb = g.k0; kb < g.k1; ++kb, ++it) {
-          const int s = it % q.stages;
-          if (!mbar_wait(&sh.full[s], (it / q.stages) & 1, p.status)) {
-            ok = false;
-            break;
-          }
-          tmem_fence_after();
-          const uint32_t sc = tmem + kTmemScales + (it % kScaleSlots) * kScaleCols;
-          const uint32_t xs = smem_addr(stage_xs(s));
-          tmem_copy_scales(sc, desc_rows16(smem_addr(stage_ws(s))));
-          tmem_copy_scales(sc + 4, desc_rows16(xs));
-          if (g.cols > 128) tmem_copy_scales(sc + 8, desc_rows16(xs + kScaleBytes));
-          const uint64_t a = desc_rows128(smem_addr(stage_w(s))), b = desc_rows128(smem_addr(stage_x(s)));
-#pragma unroll
-          for (int i = 0; i < 4; ++i)  // 32 inputs: 32 bytes on, 2 in the descriptors' units
-            mma_scaled(d, a + 2 * i, b + 2 * i, idesc_scale_byte(idesc, i), sc, sc + 4, kb > g.k0 || i > 0);
-          mma_commit(&sh.empty[s]);
+    // Products.
+    Segment g;
+    Ring r;
+    int seg = 0, slot = 0;
+    bool ok = true;
+    const uint32_t base = smem_addr(smem);
+    const uint64_t a0 = desc_rows128(base), b0 = desc_rows128(base + x_at);
+    const uint64_t ws0 = desc_rows16(base + ws_at), xs0 = desc_rows16(base + x_at);
+    int group = 0;             // place in the ring of the weights' scales
+    unsigned group_parity = 0;
+    while (ok && next_segment(q, sh, run, g)) {
+      const int buf = seg & 1;
+      if (seg >= 2 && !mbar_wait_warp(&sh.acc_empty[buf], (seg / 2 - 1) & 1, p.status)) break;
+      tmem_fence_after();
+      const uint32_t d = tmem + buf * kMaxCols;
+      const uint32_t idesc = idesc_e2m1_e4m3(g.cols);
+      const bool wide = g.cols > 128;
+      const unsigned x_step = g.cols * kStep >> 4, xs_step = q.scale_bytes >> 4;
+      for (int st = g.s0; st < g.s1; ++st) {
+        if ((st == g.s0 || (st & 1) == 0) && !mbar_wait_warp(&sh.scale_full[group], group_parity, p.status)) {
+          ok = false;
+          break;
         }
-        mma_commit(&sh.acc_full[buf]);
-        ++seg;
+        if (!mbar_wait_warp(&sh.full[r.stage], r.parity, p.status)) {
+          ok = false;
+          break;
+        }
+        tmem_fence_after();
+        const bool last = st + 1 == g.s1, group_end = (st & 1) == 1 || last;
+        const unsigned at = r.offset >> 4;  // in the descriptors' units
+        const uint64_t ws = ws0 + (group * 4 + (st & 1) * 2) * (kScaleBytes / 16);
+        const uint32_t sc = tmem + kTmemScales + slot * 2 * kScaleCols;
+        const bool both = st * kStageSteps + 1 < q.KB;
+        if (elect_one()) {
+#pragma unroll
+          for (int h = 0; h < kStageSteps; ++h) {
+            if (h > 0 && !both) break;
+            const uint32_t c = sc + h * kScaleCols;
+            const uint64_t xs = xs0 + at + (both ? kStageSteps : 1) * x_step + h * xs_step;
+            tmem_copy_scales(c, ws + h * (kScaleBytes / 16));
+            tmem_copy_scales(c + 4, xs);
+            if (wide) tmem_copy_scales(c + 8, xs + kScaleBytes / 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // 32 inputs: 32 bytes on
+              mma_scaled(d, a0 + at + h * (kTileBytes / 16) + 2 * i, b0 + at + h * x_step + 2 * i,
+                         idesc_scale_byte(idesc, i), c, c + 4, st > g.s0 || h > 0 || i > 0);
+          }
+          mma_commit(&sh.empty[r.stage]);
+          if (group_end) mma_commit(&sh.scale_empty[group]);
+          if (last) mma_commit(&sh.acc_full[buf]);
+        }
+        __syncwarp();
+        slot ^= 1;
+        if (group_end && ++group == kScaleGroups) {
+          group = 0;
+          group_parity ^= 1;
+        }
+        r.advance(q);
       }
+      ++seg;
     }
   } else if (warp == 2) {
     // The weights' scales: four bytes a row and step, laid out for the copy to
-    // tensor memory (row r: place r % 32, word r / 32).
-    Segment g;
-    int it = 0;
-    bool ok = true;
+    // tensor memory (row r: place r % 32, word r / 32). A lane reads 16 bytes
+    // of a row, four steps, at once, and keeps kAhead such groups in flight,
+    // across units: with four steps ahead the loads' latency alone set the
+    // pace (experts_up 1513 us).
+    constexpr int kAhead = 5;
     const int64_t pitch = p.K / 32;
-    while (ok && next_segment(q, sh, run, g)) {
-      const uint8_t* src[4];
+    const bool vec = q.KB % 4 == 0;
+    uint32_t v[kAhead][4][4];  // [group][row][step]
+    int lo[kAhead], hi[kAhead];
+    Segment g;
+    int next = 0;
+    bool more = next_segment(q, sh, run, g);
+    if (more) next = g.s0 * kStageSteps;
+    // Steps [lo, hi) of one aligned group of four; lo == hi: none left.
+    auto fetch = [&](uint32_t(&to)[4][4], int& from, int& upto) {
+      from = upto = 0;
+      if (!more) return;
+      const int group = next & ~3;
+      from = next - group;
+      const int end = min(q.KB, g.s1 * kStageSteps);
+      upto = min(4, end - group);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int m = out_row(g.mt, i / 2) + (i & 1) * 32 + lane;
-        src[i] = m < p.M ? p.w_scale + (static_cast<int64_t>(g.e) * p.M + m) * pitch : nullptr;
-      }
-      constexpr int kAhead = 4;
-      uint32_t v[kAhead][4];
-      auto fetch = [&](uint32_t* to, int kb) {
+        const uint8_t* src = p.w_scale + (static_cast<int64_t>(g.e) * p.M + m) * pitch + 4 * group;
+        if (m >= p.M) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          to[i] = src[i] && kb < g.k1 ? __ldg(reinterpret_cast<const uint32_t*>(src[i]) + kb) : 0x7F7F7F7Fu;
-      };
+          for (int j = 0; j < 4; ++j) to[i][j] = 0x7F7F7F7Fu;
+        } else if (vec) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
+          to[i][0] = w.x; to[i][1] = w.y; to[i][2] = w.z; to[i][3] = w.w;
+        } else {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) fetch(v[i], g.k0 + i);
-      for (int kb0 = g.k0; ok && kb0 < g.k1; kb0 += kAhead) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          if (kb0 + i >= g.k1) break;
-          const int s = it % q.stages;
-          if (it >= q.stages && !mbar_wait(&sh.empty[s], (it / q.stages - 1) & 1, p.status)) {
-            ok = false;
-            break;
-          }
-          reinterpret_cast<uint4*>(stage_ws(s))[lane] = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.full[s]);
-          ++it;
-          fetch(v[i], kb0 + i + kAhead);
+          for (int j = 0; j < 4; ++j)
+            to[i][j] = j >= from && j < upto ? __ldg(reinterpret_cast<const uint32_t*>(src) + j) : 0;
         }
-        ok = __all_sync(0xffffffffu, ok);
+      }
+      next = group + 4;
+      if (next >= end) {
+        more = next_segment(q, sh, run, g);
+        if (more) next = g.s0 * kStageSteps;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(v[i], lo[i], hi[i]);
+    int at = 0;
+    unsigned parity = 0, round = 0;
+    bool ok = true;
+    while (ok && hi[0] > lo[0]) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (!ok || lo[i] >= hi[i]) continue;
+        if (round > 0) ok = mbar_wait_warp(&sh.scale_empty[at], parity ^ 1, p.status);
+        if (!ok) continue;
+        uint4* to = reinterpret_cast<uint4*>(smem + ws_at + at * 4 * kScaleBytes) + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[j * (kScaleBytes / 16)] = make_uint4(v[i][0][j], v[i][1][j], v[i][2][j], v[i][3][j]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.scale_full[at]);
+        if (++at == kScaleGroups) {
+          at = 0;
+          parity ^= 1;
+          round = 1;
+        }
+        fetch(v[i], lo[i], hi[i]);
       }
     }
   } else if (warp >= 4) {
@@ -549,7 +643,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
       tmem_fence_after();
       const uint32_t acc = tmem + buf * kMaxCols + (static_cast<uint32_t>(warp & 3) << 21);
       const int rows8 = round8(g.rows);
-      const bool whole = g.k0 == 0 && g.k1 == q.KB;
+      const bool whole = g.s0 == 0 && g.s1 == q.KS;
       const int64_t base = p.offset ? static_cast<int64_t>(__ldg(p.offset + g.e)) : g.e * p.region;
       const int64_t row0 = base + g.tile * q.tile_rows;
       const int o = p.glu ? g.mt * 64 + (m & 63) : g.mt * kTileM + m;
@@ -575,7 +669,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
           if (c0 + i < g.rows)
             reinterpret_cast<__nv_bfloat16*>(p.y)[(row0 + c0 + i) * outs + o] = __float2bfloat16(v[i]);
       };
-      float* mine = slot(blockIdx.x, g.k0 == 0);
+      float* mine = slot(blockIdx.x, g.s0 == 0);
       for (int c0 = 0; c0 < rows8; c0 += 8) {
         float v[8];
         tmem_load8(v, acc + c0);
@@ -602,8 +696,8 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
         continue;
       }
       // A shared unit: the last block to arrive adds the parts, in order.
-      const int c_first = owner_of(total, blocks, g.unit * q.KB);
-      const int c_last = owner_of(total, blocks, (g.unit + 1) * q.KB - 1);
+      const int c_first = owner_of(total, blocks, g.unit * q.KS);
+      const int c_last = owner_of(total, blocks, (g.unit + 1) * q.KS - 1);
       __threadfence();
       epilogue_sync();
       if (m == 0) {
@@ -656,7 +750,7 @@ int tile_rows_for(int E, int64_t max_rows, int mult) {
 
 struct Sizes {
   int tile_rows;
-  size_t counters, partial, scale, image, total;
+  size_t counters, partial, image, total;
 };
 
 Sizes sizes_of(int E, int64_t max_rows, int K, bool fp8) {
@@ -670,9 +764,8 @@ Sizes sizes_of(int E, int64_t max_rows, int K, bool fp8) {
   const int sb = z.tile_rows * mult > 128 ? 2 * kScaleBytes : kScaleBytes;
   z.counters = 0;
   z.partial = 1024;
-  z.scale = z.partial + up(sizeof(float) * kMaxBlocks * 2 * z.tile_rows * kTileM);
-  z.image = z.scale + up(static_cast<size_t>(tiles) * (K / kStep) * sb);
-  z.total = z.image + up(static_cast<size_t>(slots) * mult * K);
+  z.image = z.partial + up(sizeof(float) * kMaxBlocks * 2 * z.tile_rows * kTileM);
+  z.total = z.image + up(static_cast<size_t>(tiles) * (K / kStep) * sb + static_cast<size_t>(slots) * mult * K);
   return z;
 }
 
@@ -706,24 +799,32 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   q.tile_rows = z.tile_rows;
   q.cols_cap = z.tile_rows * q.mult;
   q.KB = p.K / kStep;
+  q.KS = (q.KB + kStageSteps - 1) / kStageSteps;
   q.MT = p.glu ? (p.M / 2 + 63) / 64 : (p.M + kTileM - 1) / kTileM;
   q.counters = reinterpret_cast<unsigned*>(p.ws + z.counters);
   q.partial = reinterpret_cast<float*>(p.ws + z.partial);
-  q.image_scale = p.ws + z.scale;
   q.image = p.ws + z.image;
-  const int sb = q.cols_cap > 128 ? 2 * kScaleBytes : kScaleBytes;
-  q.stage_bytes = (kTileBytes + q.cols_cap * kStep + kScaleBytes + sb + 1023) / 1024 * 1024;
-  constexpr unsigned kSmem = 227 * 1024 - sizeof(Shared) - 2048;
+  q.scale_bytes = q.cols_cap > 128 ? 2 * kScaleBytes : kScaleBytes;
+  q.stage_bytes = (kStageSteps * (kTileBytes + q.cols_cap * kStep + q.scale_bytes) + 1023) / 1024 * 1024;
+  constexpr unsigned kRing = kScaleGroups * 4 * kScaleBytes;
+  constexpr unsigned kSmem = 227 * 1024 - sizeof(Shared) - 2048 - kRing;
   q.stages = std::min<int>(kMaxStages, kSmem / q.stage_bytes);
-  const size_t smem = static_cast<size_t>(q.stages) * q.stage_bytes + 1024;
+  const size_t smem = static_cast<size_t>(q.stages) * q.stage_bytes + kRing + 1024;
 
   const EncodeTiled encode = encode_tiled();
   if (!encode) return cudaErrorNotSupported;
   CUtensorMap map;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.M), static_cast<cuuint64_t>(p.E)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.K) / 2, static_cast<cuuint64_t>(p.M) * p.K / 2};
-  const cuuint32_t box[3] = {kStep, 64, 1}, ones[3] = {1, 1, 1};
-  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<uint8_t*>(p.w), dims, strides, box, ones,
+  // Inputs in steps of 128, outputs in one part or two (gates, ups); a load
+  // brings two steps of a unit's 128 outputs, each step's 128 x 128 together.
+  const int parts = p.glu ? 2 : 1;
+  const cuuint64_t row = static_cast<cuuint64_t>(p.K) / 2, rows = static_cast<cuuint64_t>(p.M) / parts;
+  const cuuint64_t dims[5] = {kStep, rows, static_cast<cuuint64_t>(parts), static_cast<cuuint64_t>(q.KB),
+                              static_cast<cuuint64_t>(p.E)};
+  const cuuint64_t strides[4] = {row, rows * row, kStep / 2, p.M * row};
+  const cuuint32_t box[5] = {kStep, static_cast<cuuint32_t>(kTileM / parts), static_cast<cuuint32_t>(parts),
+                             kStageSteps, 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 5, const_cast<uint8_t*>(p.w), dims, strides, box, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;

@@ -10,6 +10,32 @@
 
 namespace ep {
 
+// One lane of a converged warp, the same each time. Instructions whose
+// operands must be uniform over the warp (products, copies, their barriers)
+// are issued under this by a warp that runs its loop as a whole: inside a
+// branch on the thread index each of them cost 84 cycles to issue, under this
+// the products' own 51 (at 64 columns and fewer) to 96 (at 192).
+__device__ __forceinline__ bool elect_one() {
+  unsigned r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// A value that every lane holds, known to the compiler as such.
+template <typename T>
+__device__ __forceinline__ T uniform(T v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
+// mbar_wait by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, unsigned parity, int32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+}
+
 // ---- tensor memory ---------------------------------------------------------
 // Whole warp; the column count is a power of two >= 32. The base address
 // appears at *slot (shared memory).
@@ -88,12 +114,12 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 }
 
 // ---- tiled TMA load --------------------------------------------------------------
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z,
-                                            uint64_t* bar) {
+__device__ __forceinline__ void tma_load_5d(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            int c4, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          smem_addr(smem_dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(smem_dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_addr(bar))
       : "memory");
 }
 

@@ -25,9 +25,10 @@ int cache_setup(const ep_kv_cache_t* C, const int32_t* seq_lens, const int32_t* 
   if (static_cast<int64_t>(C->max_pages) * P > INT32_MAX) return EP_ERR_INVALID_ARG;
   if (!cu_tokens && N != C->num_seqs) return EP_ERR_INVALID_ARG;
   if (N > 0) {
-    if (!seq_lens || C->num_seqs < 1) return EP_ERR_INVALID_ARG;
+    if (!seq_lens || C->num_seqs < 1 || C->num_pages < 1) return EP_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(C->num_pages) * C->num_heads > INT32_MAX) return EP_ERR_INVALID_ARG;
     if (C->max_pages > 0 && !C->page_table) return EP_ERR_INVALID_ARG;
-    if (C->num_pages > 0 && (!C->k || !C->v || !C->k_scale || !C->v_scale)) return EP_ERR_INVALID_ARG;
+    if (!C->k || !C->v || !C->k_scale || !C->v_scale) return EP_ERR_INVALID_ARG;
   }
   if (!aligned(C->k, 16) || !aligned(C->v, 16)) return EP_ERR_ALIGNMENT;
   p = KVParams{};

@@ -403,6 +403,19 @@ __device__ void tile_experts(const Params& q, Shared& sh) {
   __syncthreads();
 }
 
+// The epilogue's threads agree on whether they go on, since they meet at barriers.
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  unsigned r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
@@ -638,7 +651,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     int seg = 0;
     while (next_segment(q, sh, run, g)) {
       const int buf = seg & 1;
-      if (!mbar_wait(&sh.acc_full[buf], (seg / 2) & 1, p.status)) break;
+      if (!epilogue_all(mbar_wait(&sh.acc_full[buf], (seg / 2) & 1, p.status))) break;
       ++seg;
       tmem_fence_after();
       const uint32_t acc = tmem + buf * kMaxCols + (static_cast<uint32_t>(warp & 3) << 21);
@@ -767,22 +780,6 @@ Sizes sizes_of(int E, int64_t max_rows, int K, bool fp8) {
   z.image = z.partial + up(sizeof(float) * kMaxBlocks * 2 * z.tile_rows * kTileM);
   z.total = z.image + up(static_cast<size_t>(tiles) * (K / kStep) * sb + static_cast<size_t>(slots) * mult * K);
   return z;
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-  static const EncodeTiled fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12080, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  return fn;
 }
 
 }  // namespace

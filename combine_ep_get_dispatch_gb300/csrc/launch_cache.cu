@@ -14,6 +14,7 @@
 #include <tuple>
 
 #include "kernels.cuh"
+#include "tensor.cuh"
 
 namespace ep {
 
@@ -91,6 +92,18 @@ int blocks_per_sm(const void* fn, int dev, int threads, size_t smem) {
   std::lock_guard<std::mutex> lock(g_mutex);
   g_occupancy[key] = per_sm;
   return per_sm;
+}
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12080, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
 }
 
 }  // namespace ep

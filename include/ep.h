@@ -642,8 +642,8 @@ size_t ep_kv_attention_workspace_bytes(int num_tokens, int num_q_heads, int num_
  * values (code * scale) of head h / (num_q_heads / C->num_heads). The cache
  * already holds the new tokens (ep_kv_append). Products take q as an 11-bit
  * significand scaled by its row's largest magnitude (a BF16 value keeps all
- * its bits down to 2^-14 of it) and softmax weights as 11-bit significands;
- * sums, maxima and normalisers are fp32. A token with nothing to attend
+ * its bits down to 2^-14 of it) and softmax weights as 11-bit significands (down
+ * to 2^-29 of the row's largest); sums, maxima and normalisers are fp32. A token with nothing to attend
  * (seq_lens[b] = 0, a negative position) gets zeros, and lse -inf. Codes at
  * masked positions are never used, NaN among them.
  *

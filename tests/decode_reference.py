@@ -84,12 +84,17 @@ def append(cache: dict, lens, cu, k, v, rope, interleaved) -> None:
 
 
 def attention(cache: dict, lens, cu, q, scale, window):
-    """out, lse and what bounds their errors: for each row sum_j p_j |v_j| and max_j scale sum |q k_j|."""
+    """out, lse and what bounds their errors.
+
+    For each row: sum_j p_j |v_j|; max_j scale sum |q k_j|; and the largest p_j
+    times its value block's scale, times the sum of the value codes'
+    magnitudes, which 2^-40 of is what weights too small for fp16 can lose.
+    """
     T, QH, D = q.shape
     P, KH = cache["k"].shape[2], cache["k"].shape[1]
     G = QH // KH
     out, lse = np.zeros((T, QH, D)), np.full((T, QH), -np.inf)
-    pv, mag = np.zeros((T, QH, D)), np.zeros((T, QH))
+    pv, mag, small = np.zeros((T, QH, D)), np.zeros((T, QH)), np.zeros((T, QH, D))
     pages = cache["k"].shape[0]
     for b, length in enumerate(lens):
         n = cu[b + 1] - cu[b]
@@ -113,8 +118,10 @@ def attention(cache: dict, lens, cu, q, scale, window):
                 out[cu[b] + i, h] = p @ v
                 lse[cu[b] + i, h] = m + np.log(e.sum())
                 pv[cu[b] + i, h] = p @ np.abs(v)
+                vs = cache["v_scale"][page, h // G].astype(np.float64)
+                small[cu[b] + i, h] = (p * vs).max() * (np.abs(v) / vs[:, None]).sum(0)
                 mag[cu[b] + i, h] = abs(scale) * np.max(np.abs(k) @ np.abs(qq) + 2.0 ** -4 * np.abs(k).sum(1) * np.abs(qq).max())
-    return out, lse, pv, mag
+    return out, lse, pv, mag, small
 
 
 def weights(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:

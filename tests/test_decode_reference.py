@@ -39,7 +39,7 @@ def test_attention_of_equal_keys_averages_the_values():
     rng = np.random.default_rng(2)
     cache = dict(k=np.full((2, 1, 16, 64), 0x38, np.uint8), v=rng.integers(0, 127, (2, 1, 16, 64)).astype(np.uint8),
                  k_scale=np.ones((2, 1)), v_scale=np.array([[1.0], [4.0]]), table=np.array([[1, 0]]))
-    out, lse, _, _ = R.attention(cache, [20], [0, 1], np.ones((1, 2, 64)), 0.125, 0)
+    out, lse, *_ = R.attention(cache, [20], [0, 1], np.ones((1, 2, 64)), 0.125, 0)
     v = np.concatenate([R.TABLE[cache["v"][1, 0]] * 4, R.TABLE[cache["v"][0, 0, :4]]])
     assert np.allclose(out[0, 1], v.mean(0)) and np.allclose(lse, np.log(20) + 8)
     assert np.allclose(R.attention(cache, [20], [0, 1], np.ones((1, 2, 64)), 0.125, 4)[0][0, 0], v[16:].mean(0))

@@ -40,6 +40,7 @@ constexpr int kChunk = 32;       // tokens
 constexpr int kWarps = 4;        // computing warps
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kMaxBlocks = 320;  // blocks a workspace has room for
+constexpr int kFan = 8;          // parts of a shared unit that one block joins at once
 constexpr int kUnits = 4;        // units whose descriptors are in flight
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTop = 15.0f;    // the largest weight enters the products as 2^15
@@ -305,93 +306,89 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       ++un;
       // Pages in batches of 32: a lane holds one page's number and scales; the
-      // next batch's are in flight.
+      // next batch's are in flight. (A chunk of two 16-token pages starts at an
+      // even one, so both are in a batch.)
       const int stop = static_cast<int>(min(static_cast<int64_t>(max(s.len, 0)), cap));
-      const int page0 = (d.first + d.c0 * kChunk) >> c.log2P;
       const int pages = stop > 0 ? ((stop - 1) >> c.log2P) + 1 : 0;  // pages the sequence has
       const int32_t* table = c.table + static_cast<int64_t>(b) * c.MP;
       auto page_no = [&](int j) { return j < pages ? __ldg(table + j) : -1; };
       auto scale_of = [&](const float* from, int page) {
         return page >= 0 && page < c.pages ? __ldg(from + static_cast<int64_t>(page) * c.KH + d.h) : 1.0f;
       };
-      int batch = page0;
-      int id[2] = {page_no(page0 + lane), page_no(page0 + 32 + lane)};
-      float ks[2] = {scale_of(c.k_scale, id[0]), 0.0f}, vs[2] = {scale_of(c.v_scale, id[0]), 0.0f};
-      ks[1] = scale_of(c.k_scale, id[1]);
-      vs[1] = scale_of(c.v_scale, id[1]);
-      int id_next = page_no(page0 + 64 + lane);
+      int batch = (d.first + d.c0 * kChunk) >> c.log2P;
+      int id = page_no(batch + lane), id1 = page_no(batch + 32 + lane);
+      float ks = scale_of(c.k_scale, id), vs = scale_of(c.v_scale, id);
+      float ks1 = scale_of(c.k_scale, id1), vs1 = scale_of(c.v_scale, id1);
+      int id2 = page_no(batch + 64 + lane);
       for (int k = d.c0; k < d.c1; ++k, ++it) {
         const int tok = d.first + k * kChunk;
-        int j = tok >> c.log2P;
+        const int j = tok >> c.log2P;
         if (j >= batch + 32) {
           batch += 32;
-          id[0] = id[1];
-          ks[0] = ks[1];
-          vs[0] = vs[1];
-          id[1] = id_next;
-          ks[1] = scale_of(c.k_scale, id[1]);
-          vs[1] = scale_of(c.v_scale, id[1]);
-          id_next = page_no(batch + 64 + lane);
+          id = id1;
+          ks = ks1;
+          vs = vs1;
+          id1 = id2;
+          ks1 = scale_of(c.k_scale, id1);
+          vs1 = scale_of(c.v_scale, id1);
+          id2 = page_no(batch + 64 + lane);
         }
         if (it >= kStages && !mbar_wait_warp(&sh.empty[stage], parity ^ 1, c.status)) {
           ok = false;
           break;
         }
-        // The chunk's pages: one, or two of 16 tokens.
-        const int two = c.P == 16 ? 2 : 1;
-        const int rows = kChunk / two;
-        int pg[2];
+        uint64_t* bar = &sh.full[stage];
+        uint8_t* to = smem + stage * Shape<kD>::kStage;
+        // Tokens that exist from `from` on, `most` at the most, in a page of
+        // the cache; a page outside it is reported and read as masked.
+        auto exist = [&](int page, int from, int most) {
+          const int have = min(most, stop - from);
+          if (have <= 0) return 0u;
+          if (page < 0 || page >= c.pages) {
+            if (lane == 0) flag(c.status, EP_ST_BAD_INDEX);
+            return 0u;
+          }
+          return have >= 32 ? ~0u : (1u << have) - 1u;
+        };
+        auto exponent = [](float v) { return static_cast<int>(__float_as_uint(v) >> 23 & 255) - 127; };
+        const int src = j - batch;
+        const int page = __shfl_sync(0xffffffffu, id, src);
+        const float pk = __shfl_sync(0xffffffffu, ks, src), pv = __shfl_sync(0xffffffffu, vs, src);
         ChunkHeader hd;
-        hd.valid = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int e = (i < two ? j + i : j) - batch;  // at most 32
-          const int src = e & 31;
-          const int x0 = __shfl_sync(0xffffffffu, id[0], src), x1 = __shfl_sync(0xffffffffu, id[1], src);
-          const float k0 = __shfl_sync(0xffffffffu, ks[0], src), k1 = __shfl_sync(0xffffffffu, ks[1], src);
-          const float v0 = __shfl_sync(0xffffffffu, vs[0], src), v1 = __shfl_sync(0xffffffffu, vs[1], src);
-          pg[i] = e < 32 ? x0 : x1;
-          hd.ks[i] = e < 32 ? k0 : k1;
-          hd.ev[i] = static_cast<int>(__float_as_uint(e < 32 ? v0 : v1) >> 23 & 255) - 127;
-          if (i >= two) continue;
-          const int from = tok + i * rows, have = min(rows, stop - from);
-          if (have > 0) {
-            if (pg[i] >= 0 && pg[i] < c.pages) {
-              hd.valid |= (have >= 32 ? ~0u : (1u << have) - 1u) << (i * rows);
-            } else if (lane == 0) {
-              flag(c.status, EP_ST_BAD_INDEX);
+        if (c.P > 16) {
+          hd.valid = exist(page, tok, kChunk);
+          // (Scales of a page that nobody may read stay out of the arithmetic.)
+          hd.ks[0] = hd.ks[1] = hd.valid ? pk : 1.0f;
+          hd.ev[0] = hd.ev[1] = hd.valid ? exponent(pv) : 0;
+          if (elect_one()) {
+            sh.header[stage] = hd;
+            mbar_arrive_expect_tx(bar, hd.valid ? Shape<kD>::kStage : 0);
+            if (hd.valid) {
+              const int block = page * c.KH + d.h, row = tok & (c.P - 1);
+              tma_load_3d(to, &map_k, 0, row, block, bar);
+              tma_load_3d(to + Shape<kD>::kSide, &map_v, 0, row, block, bar);
             }
           }
-        }
-        if (two == 1) {
-          hd.ks[1] = hd.ks[0];
-          hd.ev[1] = hd.ev[0];
-        }
-        // A page nobody may read keeps its scales out of the arithmetic.
-        const unsigned half = two == 2 ? 0xFFFFu : ~0u;
-        if ((hd.valid & half) == 0) {
-          hd.ks[0] = 1.0f;
-          hd.ev[0] = two == 2 && hd.valid ? hd.ev[1] : 0;
-        }
-        if (two == 1) {
-          hd.ks[1] = hd.ks[0];
-          hd.ev[1] = hd.ev[0];
-        } else if ((hd.valid >> 16) == 0) {
-          hd.ks[1] = 1.0f;
-          hd.ev[1] = hd.ev[0];
-        }
-        if (lane == 0) {
-          sh.header[stage] = hd;
-          uint64_t* bar = &sh.full[stage];
-          const int loads = two == 1 ? (hd.valid ? 1 : 0) : ((hd.valid & 0xFFFFu) ? 1 : 0) + (hd.valid >> 16 ? 1 : 0);
-          mbar_arrive_expect_tx(bar, loads * rows * kRowBytes * 2);
-          uint8_t* to = smem + stage * Shape<kD>::kStage;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (i >= two || (hd.valid >> (i * rows) & (two == 2 ? 0xFFFFu : ~0u)) == 0) continue;
-            const int block = pg[i] * c.KH + d.h, row = (tok + i * rows) & (c.P - 1);
-            tma_load_3d(to + i * rows * kRowBytes, &map_k, 0, row, block, bar);
-            tma_load_3d(to + Shape<kD>::kSide + i * rows * kRowBytes, &map_v, 0, row, block, bar);
+        } else {
+          const int page1 = __shfl_sync(0xffffffffu, id, src + 1 & 31);
+          const float pk1 = __shfl_sync(0xffffffffu, ks, src + 1 & 31), pv1 = __shfl_sync(0xffffffffu, vs, src + 1 & 31);
+          const unsigned v0 = exist(page, tok, 16), v1 = exist(page1, tok + 16, 16);
+          hd.valid = v0 | v1 << 16;
+          hd.ks[0] = v0 ? pk : 1.0f;
+          hd.ks[1] = v1 ? pk1 : 1.0f;
+          hd.ev[0] = v0 ? exponent(pv) : v1 ? exponent(pv1) : 0;
+          hd.ev[1] = v1 ? exponent(pv1) : hd.ev[0];
+          if (elect_one()) {
+            sh.header[stage] = hd;
+            mbar_arrive_expect_tx(bar, (v0 ? Shape<kD>::kSide : 0) + (v1 ? Shape<kD>::kSide : 0));
+            if (v0) {
+              tma_load_3d(to, &map_k, 0, 0, page * c.KH + d.h, bar);
+              tma_load_3d(to + Shape<kD>::kSide, &map_v, 0, 0, page * c.KH + d.h, bar);
+            }
+            if (v1) {
+              tma_load_3d(to + 16 * kRowBytes, &map_k, 0, 0, page1 * c.KH + d.h, bar);
+              tma_load_3d(to + Shape<kD>::kSide + 16 * kRowBytes, &map_v, 0, 0, page1 * c.KH + d.h, bar);
+            }
           }
         }
         __syncwarp();
@@ -725,8 +722,86 @@ __global__ void __launch_bounds__(kThreads, 2)
       continue;
     }
     // ---- a unit that other blocks share ----
+    // Parts are joined in groups of kFan blocks, then the groups, each time by
+    // the last to arrive and in order: with one level a long sequence's last
+    // block read 76 parts one after the other (82 us for 131072 tokens x 4
+    // cache heads).
     const int c_first = owner_of(total, blocks, d.at), c_last = owner_of(total, blocks, d.at + d.total - 1);
-    auto part = [&](int block, bool starts) { return partial + (static_cast<int64_t>(block) * 2 + (starts ? 1 : 0)) * kPart; };
+    auto part = [&](int block, bool starts) {
+      return partial + (static_cast<int64_t>(block) * 2 + (starts ? 1 : 0)) * kPart;
+    };
+    // One block's arrival on a counter that expects `n`: whether it is the last.
+    auto arrive = [&](unsigned* counter, int n) {
+      __threadfence();
+      compute_sync();
+      if (tid == 0) {
+        const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(n - 1);
+        if (last) *counter = 0u;
+        sh.last = last;
+      }
+      compute_sync();
+      const bool last = sh.last;
+      if (last) __threadfence();
+      return last;
+    };
+    // Join parts first, first + step, ... below stop (the unit's first one lies in its block's
+    // second slot): into part `to`, or as the result when `to` is null.
+    auto join = [&](int first, int step, int stop, float* to) {
+      for (int i = tid; i < rows * (kD / 4); i += 128) {
+        const int row = i / (kD / 4), ch = i % (kD / 4);
+        const int n = (stop - first + step - 1) / step;
+        float top = -INFINITY, topd = -INFINITY, sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k0 = 0; k0 < n; k0 += kFan) {
+          float4 y[kFan], v[kFan];
+#pragma unroll
+          for (int k = 0; k < kFan; ++k) {
+            const int b = first + (k0 + k) * step;
+            y[k] = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+            v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (b < stop) {
+              const float* from = part(b, b == c_first);
+              y[k] = __ldcg(reinterpret_cast<const float4*>(from + kRows * kD) + row);
+              v[k] = __ldcg(reinterpret_cast<const float4*>(from + row * kD) + ch);
+            }
+          }
+          float t = top, td = topd;
+#pragma unroll
+          for (int k = 0; k < kFan; ++k) {
+            t = fmaxf(t, y[k].x);
+            td = fmaxf(td, y[k].y);
+          }
+          const float rt = t == -INFINITY ? 0.0f : t, rd = td == -INFINITY ? 0.0f : td;
+          const float keep = ex2(top - rt);
+          sum *= ex2(topd - rd);
+          acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+          for (int k = 0; k < kFan; ++k) {
+            const float f = ex2(y[k].x - rt);
+            sum = fmaf(ex2(y[k].y - rd), y[k].z, sum);
+            acc.x = fmaf(f, v[k].x, acc.x);
+            acc.y = fmaf(f, v[k].y, acc.y);
+            acc.z = fmaf(f, v[k].z, acc.z);
+            acc.w = fmaf(f, v[k].w, acc.w);
+          }
+          top = t;
+          topd = td;
+        }
+        if (to) {
+          // (The first part of the group is this thread's own to overwrite,
+          // but for its row's references: all threads of a row read those.)
+          __stcg(reinterpret_cast<float4*>(to + row * kD) + ch, acc);
+          __syncwarp(__activemask());
+          if (ch == 0) __stcg(reinterpret_cast<float4*>(to + kRows * kD) + row, make_float4(top, topd, sum, 0.0f));
+        } else {
+          const float f = sum > 0.0f ? ex2(top - topd) / sum : (sum == 0.0f ? 0.0f : sum);
+          const int64_t at = out_of(row);
+          reinterpret_cast<uint2*>(p.out + at * kD)[ch] =
+              make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+          if (p.lse && ch == 0) p.lse[at] = (topd + log2f(sum)) * kLn2;
+        }
+      }
+    };
     if (tw == 0) {
       float* to = part(blockIdx.x, d.c0 == 0);
 #pragma unroll
@@ -744,46 +819,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           __stcg(reinterpret_cast<float4*>(to + kRows * kD) + row, make_float4(m[r], md[r], l[r], 0.0f));
       }
     }
-    __threadfence();
-    compute_sync();
-    if (tid == 0) {
-      const unsigned old = atomicAdd(&counters[c_first], 1u);
-      const bool last = old == static_cast<unsigned>(c_last - c_first);
-      if (last) counters[c_first] = 0u;
-      sh.last = last;
+    const int parts = c_last - c_first + 1;
+    if (parts <= 2 * kFan) {
+      if (arrive(counters + c_first, parts)) join(c_first, 1, c_last + 1, nullptr);
+      continue;
     }
-    compute_sync();
-    if (!sh.last) continue;
-    __threadfence();
-    // The last block joins all parts, in order: a thread four channels of a row.
-    for (int i = tid; i < rows * (kD / 4); i += 128) {
-      const int row = i / (kD / 4), ch = i % (kD / 4);
-      float top = -INFINITY, topd = -INFINITY;
-      for (int b = c_first; b <= c_last; ++b) {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(part(b, b == c_first) + kRows * kD) + row);
-        top = fmaxf(top, y.x);
-        topd = fmaxf(topd, y.y);
-      }
-      const float rt = top == -INFINITY ? 0.0f : top, rd = topd == -INFINITY ? 0.0f : topd;
-      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float sum = 0.0f;
-      for (int b = c_first; b <= c_last; ++b) {
-        const float* from = part(b, b == c_first);
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(from + kRows * kD) + row);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(from + row * kD) + ch);
-        const float f = ex2(y.x - rt);
-        sum = fmaf(ex2(y.y - rd), y.z, sum);
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
-      }
-      const float f = sum > 0.0f ? ex2(rt - rd) / sum : (sum == 0.0f ? 0.0f : sum);
-      const int64_t at = out_of(row);
-      reinterpret_cast<uint2*>(p.out + at * kD)[ch] =
-          make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-      if (p.lse && ch == 0) p.lse[at] = (topd + log2f(sum)) * kLn2;
-    }
+    // The group's first block's part takes the group's sum.
+    const int group = (static_cast<int>(blockIdx.x) - c_first) / kFan;
+    const int g0 = c_first + group * kFan, g1 = min(g0 + kFan, c_last + 1);
+    // (A block can start a group of one unit and another unit: two counters each.)
+    if (!arrive(counters + kMaxBlocks + 2 * g0 + (g0 == c_first ? 1 : 0), g1 - g0)) continue;
+    join(g0, 1, g1, part(g0, g0 == c_first));
+    if (arrive(counters + c_first, (parts + kFan - 1) / kFan)) join(c_first, kFan, c_last + 1, nullptr);
   }
 }
 

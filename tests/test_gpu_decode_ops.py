@@ -359,6 +359,63 @@ def test_cache_offsets_beyond_32_bits():
     check_attention(c, [n], [0, 2], f64(q), D ** -0.5, 0, out, lse)
 
 
+@pytest.mark.parametrize("D,P,window", [(64, 16, 0), (128, 32, 0), (128, 64, 40)])
+def test_attention_keeps_nan_to_the_tokens_that_see_it(D, P, window):
+    """NaN codes among the newest tokens (and where a window ends) reach the rows that attend to them, no others."""
+    rng = np.random.default_rng(19)
+    n, length = 6, 83
+    c = random_cache(rng, [length], P, 1, D)
+    for at, ch in ((length - 3, 5), (length - 1, 0), (length - n - 38, 17)):
+        c["v"][c["table"][0, at // P], 0, at % P, ch] = 0x7F
+    c["k"][c["table"][0, (length - 2) // P], 0, (length - 2) % P, 9] = 0xFF
+    q = bf16(rng.normal(size=(n, 4, D))).cuda()
+    out, lse = ep.kv_attention(q, device_cache(c), torch.tensor([length], dtype=torch.int32, device="cuda"),
+                               cu_tokens=torch.tensor([0, n], dtype=torch.int32, device="cuda"), window=window,
+                               scale=0.05, return_lse=True)
+    with np.errstate(invalid="ignore"):
+        ref, rl, *_ = R.attention(c, [length], [0, n], f64(q), 0.05, window)
+    assert np.isnan(ref).any() and not np.isnan(ref[0]).all() and np.isnan(rl[-1]).all()
+    assert np.array_equal(np.isnan(f64(out)), np.isnan(ref)) and np.array_equal(np.isnan(f64(lse)), np.isnan(rl))
+    fine = ~np.isnan(ref)
+    assert np.allclose(f64(out)[fine], ref[fine], rtol=2.0 ** -7, atol=2.0 ** -9)
+
+
+@pytest.mark.parametrize("D,KH,G,n", [(128, 1, 8, 1), (64, 3, 5, 1), (128, 2, 8, 4), (64, 1, 16, 5)])
+def test_attention_of_a_long_sequence_over_many_blocks(D, KH, G, n):
+    """One sequence whose parts are joined in two levels, against fp64 torch on its dequantised cache."""
+    rng = np.random.default_rng(20)
+    length, P = 40001, 64
+    pages = -(-length // P)
+    table = torch.from_numpy(rng.permutation(pages).astype(np.int32))[None].cuda()
+    codes = [torch.randint(0, 127, (pages, KH, P, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for t in codes:
+        t |= torch.randint(0, 2, t.shape, dtype=torch.uint8, device="cuda") << 7
+    scales = [torch.exp2(torch.randint(-8, -5, (pages, KH), device="cuda").float()) for _ in range(2)]
+    cache = ep.KVCache(*codes, *scales, table)
+    q = bf16(rng.normal(size=(n, KH * G, D))).cuda()
+    args = dict(cu_tokens=torch.tensor([0, n], dtype=torch.int32, device="cuda"), scale=0.02, return_lse=True,
+                workspace=ep.kv_attention_workspace(q, cache))
+    lens = torch.tensor([length], dtype=torch.int32, device="cuda")
+    out, lse = ep.kv_attention(q, cache, lens, **args)
+    k, v = (t[table[0].long()].view(torch.float8_e4m3fn).double() * s[table[0].long()].double()[..., None, None]
+            for t, s in zip(codes, scales))
+    k, v = (x.permute(1, 0, 2, 3).reshape(KH, -1, D)[:, :length] for x in (k, v))
+    for i in range(n):
+        stop = length - n + i + 1
+        sc = torch.einsum("hgd,hjd->hgj", q[i].double().view(KH, G, D), k[:, :stop]) * 0.02
+        z = torch.logsumexp(sc, -1)
+        w = (sc - z[..., None]).exp()
+        ref = torch.einsum("hgj,hjd->hgd", w, v[:, :stop]).reshape(-1, D)
+        mag = torch.einsum("hgj,hjd->hgd", w, v[:, :stop].abs()).reshape(-1, D)
+        # weights keep 11 bits and scores 2^-19 of at most 64; the result rounds to BF16
+        tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2.0 ** -13) * mag
+        assert ((out[i].double() - ref).abs() <= tol * 1.01).all()
+        assert ((lse[i].double() - z.reshape(-1)).abs() <= 2.0 ** -13).all()
+    for _ in range(3):  # the same bits whichever block comes last
+        again, lse2 = ep.kv_attention(q, cache, lens, **args)
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
+
+
 def test_attention_on_another_stream():
     rng = np.random.default_rng(13)
     c = random_cache(rng, [900], 64, 2, 128)

@@ -13,16 +13,23 @@
 //
 // What bounds it: the cache, read once from HBM. With up to 16 query rows a
 // key/value head (16 G FLOP a byte) the products are far from their limit, so
-// they run as m16n8k16 on registers: a score tile's accumulators are the next
-// product's operand as they are, and K and V fragments come from shared memory
-// in 16-byte loads without conflicts: channels are assigned to a fragment's
-// places so that a lane's are contiguous, and the tiled TMA load swizzles rows.
+// they run as m16n8k16 on registers, the cache on the 16-row side and the query
+// rows as columns: S^T = K Q^T, O^T = V^T P^T. Eight query heads then fill a
+// product (with rows and columns exchanged half of it idled, and decode of 128
+// x 8192 tokens took 400 us), and a converted code serves every column tile.
+// S^T turns into the second product's operand by an 8 x 8 transposition between
+// lanes. K and V fragments come from shared memory in 16-byte loads without
+// conflicts: channels are assigned to a fragment's places so that a lane's are
+// contiguous, and the tiled TMA load swizzles rows.
 //
-// Work: the rows of one (sequence, cache head), up to 16 kRW of them, are a
+// Work: the rows of one (sequence, cache head), up to 8 kNT kRW of them, are a
 // unit of chunks of 32 tokens. The blocks take equal runs of consecutive
-// chunks over all units, whatever the sequences' lengths. In a block, one warp
+// places over all units, whatever the sequences' lengths; a unit has a place
+// for each chunk and kUnitCost more in front, so that a block with many short
+// sequences is not the last to finish (24 sequences of 4 to 30011 tokens, 4
+// drafted each: 75 us without). In a block, one warp
 // loads (pages, scales, descriptors of what comes), four compute: kRW of them
-// hold 16 rows each, 4 / kRW groups take turns with the chunks and are joined
+// hold 8 kNT rows each, 4 / kRW groups take turns with the chunks and are joined
 // at the end of a unit. A unit that several blocks share is joined by the last
 // of them to finish, in the order of its chunks, so results do not depend on
 // which one that was.
@@ -38,16 +45,19 @@ namespace {
 
 constexpr int kChunk = 32;       // tokens
 constexpr int kWarps = 4;        // computing warps
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kThreads = 256;    // the computing warps, a loading one, and three that complete its warpgroup
+constexpr int kComputeRegs = 208, kLoadRegs = 40;  // of the 2 x 128 a thread pair is launched with
 constexpr int kMaxBlocks = 320;  // blocks a workspace has room for
 constexpr int kFan = 8;          // parts of a shared unit that one block joins at once
+constexpr int kUnitCost = 6;     // chunks that a unit costs besides its own: queries, joining, results
 constexpr int kUnits = 4;        // units whose descriptors are in flight
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTop = 15.0f;    // the largest weight enters the products as 2^15
 
-template <int kD>
+template <int kD, int kNT>
 struct Shape {
   static constexpr int kStages = kD == 128 ? 8 : 12;
+  static constexpr int kBlocksPerSM = 2;
   static constexpr int kSide = kChunk * kD;  // bytes of keys (or values) of a chunk
   static constexpr int kStage = 2 * kSide;
 };
@@ -67,24 +77,38 @@ struct Unit {
   int first;         // first token of chunk 0
   int c0, c1, total; // chunks [c0, c1) of `total`
   int it;            // the block's running number of chunk c0
-  int64_t at;        // position of chunk 0 among all chunks
+  int64_t at;        // place of chunk 0 among all units' places
 };
 
-template <int kD, int kRW>
+// A sequence's units.
+struct Sequence {
+  int t0, n, len;
+  int first;   // token that chunk 0 starts with
+  int chunks;  // of each of its units
+  int tiles;   // row tiles
+  bool ok;
+  __device__ __forceinline__ int places() const { return chunks + kUnitCost; }  // of a unit
+  __device__ __forceinline__ int64_t all(int heads) const { return static_cast<int64_t>(places()) * tiles * heads; }
+};
+
+template <int kD, int kNT, int kRW>
 struct Shared {
   static constexpr int kTW = kWarps / kRW;
-  uint64_t full[Shape<kD>::kStages], empty[Shape<kD>::kStages];
+  static constexpr int kStages = Shape<kD, kNT>::kStages;
+  uint64_t full[kStages], empty[kStages];
   uint64_t unit_full[kUnits], unit_empty[kUnits];
-  ChunkHeader header[Shape<kD>::kStages];
+  ChunkHeader header[kStages];
   Unit unit[kUnits];
   int more[kUnits];  // 0: no further unit
   long long sums[kThreads / 32];
   int find_b;
   long long find_at;
+  Sequence find;
   int bad;
   int last;
-  float4 join_o[kTW > 1 ? (kTW - 1) * kRW : 1][kD / 8][kTW > 1 ? 32 : 1];
-  float4 join_ml[kTW > 1 ? (kTW - 1) * kRW : 1][2][kTW > 1 ? 32 : 1];  // m, denominator's reference, l of rows g, g + 8
+  static constexpr int kJoin = kTW > 1 ? (kTW - 1) * kRW : 0;
+  float4 join_o[kJoin ? kJoin : 1][kJoin ? kD / 16 * kNT : 1][32];
+  float4 join_ml[kJoin ? kJoin : 1][2 * kNT][32];  // a row's references and sum
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -118,6 +142,14 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The 8 x 8 transposition of fp16 pairs between lanes: lane (g, j) gives
+// elements (g, 2j), (g, 2j + 1) and gets (2j, g), (2j + 1, g).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
@@ -132,14 +164,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // ---- the division of the work -----------------------------------------------------
-struct Sequence {
-  int t0, n, len;
-  int first;   // token that chunk 0 starts with
-  int chunks;  // of each of its units
-  int tiles;   // row tiles
-  bool ok;
-};
-
 // Sequence b of the call: what its units look like.
 __device__ __forceinline__ Sequence sequence_at(const KVAttentionParams& p, int b, int tile_rows) {
   const KVParams& c = p.c;
@@ -172,25 +196,27 @@ __device__ __forceinline__ int owner_of(int64_t total, int blocks, int64_t i) {
 }
 
 // ---- the kernel ---------------------------------------------------------------------
-template <int kD, int kRW>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int kD, int kNT, int kRW>
+__global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
     kv_attention_kernel(const KVAttentionParams p, float* partial, unsigned* counters,
                         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   constexpr int kTW = kWarps / kRW;
-  constexpr int kRows = 16 * kRW;
-  constexpr int kStages = Shape<kD>::kStages;
-  constexpr int kTiles = kD / 8;        // value channel tiles
+  using S = Shape<kD, kNT>;
+  constexpr int kRows = 8 * kNT * kRW;
+  constexpr int kStages = S::kStages;
+  constexpr int kTiles = kD / 16;       // value channel tiles
   constexpr int kSteps = kD / 16;       // score product steps
   constexpr int kRowBytes = kD;         // of a token of a head
   constexpr int kPart = kRows * (kD + 4);  // floats of a partial result
   extern __shared__ uint8_t dynamic[];
   uint8_t* smem = dynamic + (1024 - (smem_addr(dynamic) & 1023)) % 1024;
-  Shared<kD, kRW>& sh = *reinterpret_cast<Shared<kD, kRW>*>(smem + kStages * Shape<kD>::kStage);
+  using Sh = Shared<kD, kNT, kRW>;
+  Sh& sh = *reinterpret_cast<Sh*>(smem + kStages * S::kStage);
   const KVParams& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.full[i], 2);  // the loads, the header
       mbar_init(&sh.empty[i], kRW);
     }
     for (int i = 0; i < kUnits; ++i) {
@@ -210,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int64_t cap = static_cast<int64_t>(c.MP) * c.P;
   for (int b = b0; b < b1; ++b) {
     const Sequence s = sequence_at(p, b, kRows);
-    mine += static_cast<long long>(s.chunks) * s.tiles * c.KH;
+    mine += s.all(c.KH);
     if (!s.ok) sh.bad = 1;
     if (blockIdx.x == 0) {
       if (!s.ok) flag(c.status, EP_ST_BAD_INDEX);
@@ -241,13 +267,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     long long at = before;
     for (int b = b0; b < b1; ++b) {
       const Sequence s = sequence_at(p, b, kRows);
-      const long long n = static_cast<long long>(s.chunks) * s.tiles * c.KH;
-      if (begin < at + n) {
+      if (begin < at + s.all(c.KH)) {
         sh.find_b = b;
         sh.find_at = at;
+        sh.find = s;
         break;
       }
-      at += n;
+      at += s.all(c.KH);
     }
   }
   if (sh.bad) {
@@ -267,22 +293,29 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   if (begin >= end) return;
 
-  if (warp == kWarps) {
+  if (warp >= kWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    if (warp > kWarps) return;
     // ---- loads ----
     int b = uniform(sh.find_b);
     int64_t seq_at = uniform(sh.find_at);
-    Sequence s = sequence_at(p, b, kRows);
+    Sequence s = sh.find;
     int64_t at = begin;
     int it = 0, un = 0, stage = 0;
     unsigned parity = 0;
     bool ok = true;
     while (ok && at < end) {
-      // The unit that holds position `at`.
-      while (at >= seq_at + static_cast<int64_t>(s.chunks) * s.tiles * c.KH) {
-        seq_at += static_cast<int64_t>(s.chunks) * s.tiles * c.KH;
+      // The unit that holds place `at`.
+      while (at >= seq_at + s.all(c.KH)) {
+        seq_at += s.all(c.KH);
         s = sequence_at(p, ++b, kRows);
       }
-      const int u = static_cast<int>((at - seq_at) / s.chunks);
+      const int u = static_cast<int>((at - seq_at) / s.places());
+      const int64_t unit_at = seq_at + static_cast<int64_t>(u) * s.places();
+      const int from = max(0, static_cast<int>(at - unit_at) - kUnitCost);
+      at = min(end, unit_at + s.places());
+      const int upto = static_cast<int>(at - unit_at) - kUnitCost;
+      if (upto <= from) continue;  // only places in front of its chunks
       Unit d;
       d.b = b;
       d.rt = u % s.tiles;  // row tiles of a head follow one another: its cache comes from L2 after the first
@@ -292,11 +325,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       d.len = s.len;
       d.first = s.first;
       d.total = s.chunks;
-      d.at = seq_at + static_cast<int64_t>(u) * s.chunks;
-      d.c0 = static_cast<int>(at - d.at);
-      d.c1 = static_cast<int>(min(static_cast<int64_t>(s.chunks), d.c0 + (end - at)));
+      d.at = unit_at + kUnitCost;
+      d.c0 = from;
+      d.c1 = upto;
       d.it = it;
-      at += d.c1 - d.c0;
       const int slot = un % kUnits;
       if (un >= kUnits && !mbar_wait_warp(&sh.unit_empty[slot], (un / kUnits - 1) & 1, c.status)) break;
       if (lane == 0) {
@@ -338,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           break;
         }
         uint64_t* bar = &sh.full[stage];
-        uint8_t* to = smem + stage * Shape<kD>::kStage;
+        uint8_t* to = smem + stage * S::kStage;
         // Tokens that exist from `from` on, `most` at the most, in a page of
         // the cache; a page outside it is reported and read as masked.
         auto exist = [&](int page, int from, int most) {
@@ -353,43 +385,48 @@ __global__ void __launch_bounds__(kThreads, 2)
         auto exponent = [](float v) { return static_cast<int>(__float_as_uint(v) >> 23 & 255) - 127; };
         const int src = j - batch;
         const int page = __shfl_sync(0xffffffffu, id, src);
-        const float pk = __shfl_sync(0xffffffffu, ks, src), pv = __shfl_sync(0xffffffffu, vs, src);
         ChunkHeader hd;
+        // Loads first: they need the page's number alone. Scales of a page that
+        // nobody may read stay out of the arithmetic.
         if (c.P > 16) {
           hd.valid = exist(page, tok, kChunk);
-          // (Scales of a page that nobody may read stay out of the arithmetic.)
-          hd.ks[0] = hd.ks[1] = hd.valid ? pk : 1.0f;
-          hd.ev[0] = hd.ev[1] = hd.valid ? exponent(pv) : 0;
           if (elect_one()) {
-            sh.header[stage] = hd;
-            mbar_arrive_expect_tx(bar, hd.valid ? Shape<kD>::kStage : 0);
+            mbar_arrive_expect_tx(bar, hd.valid ? S::kStage : 0);
             if (hd.valid) {
               const int block = page * c.KH + d.h, row = tok & (c.P - 1);
               tma_load_3d(to, &map_k, 0, row, block, bar);
-              tma_load_3d(to + Shape<kD>::kSide, &map_v, 0, row, block, bar);
+              tma_load_3d(to + S::kSide, &map_v, 0, row, block, bar);
             }
           }
+          const float pk = __shfl_sync(0xffffffffu, ks, src), pv = __shfl_sync(0xffffffffu, vs, src);
+          hd.ks[0] = hd.ks[1] = hd.valid ? pk : 1.0f;
+          hd.ev[0] = hd.ev[1] = hd.valid ? exponent(pv) : 0;
         } else {
-          const int page1 = __shfl_sync(0xffffffffu, id, src + 1 & 31);
-          const float pk1 = __shfl_sync(0xffffffffu, ks, src + 1 & 31), pv1 = __shfl_sync(0xffffffffu, vs, src + 1 & 31);
+          const int src1 = src + 1 & 31;
+          const int page1 = __shfl_sync(0xffffffffu, id, src1);
           const unsigned v0 = exist(page, tok, 16), v1 = exist(page1, tok + 16, 16);
           hd.valid = v0 | v1 << 16;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(bar, (v0 ? S::kSide : 0) + (v1 ? S::kSide : 0));
+            if (v0) {
+              tma_load_3d(to, &map_k, 0, 0, page * c.KH + d.h, bar);
+              tma_load_3d(to + S::kSide, &map_v, 0, 0, page * c.KH + d.h, bar);
+            }
+            if (v1) {
+              tma_load_3d(to + 16 * kRowBytes, &map_k, 0, 0, page1 * c.KH + d.h, bar);
+              tma_load_3d(to + S::kSide + 16 * kRowBytes, &map_v, 0, 0, page1 * c.KH + d.h, bar);
+            }
+          }
+          const float pk = __shfl_sync(0xffffffffu, ks, src), pv = __shfl_sync(0xffffffffu, vs, src);
+          const float pk1 = __shfl_sync(0xffffffffu, ks, src1), pv1 = __shfl_sync(0xffffffffu, vs, src1);
           hd.ks[0] = v0 ? pk : 1.0f;
           hd.ks[1] = v1 ? pk1 : 1.0f;
           hd.ev[0] = v0 ? exponent(pv) : v1 ? exponent(pv1) : 0;
           hd.ev[1] = v1 ? exponent(pv1) : hd.ev[0];
-          if (elect_one()) {
-            sh.header[stage] = hd;
-            mbar_arrive_expect_tx(bar, (v0 ? Shape<kD>::kSide : 0) + (v1 ? Shape<kD>::kSide : 0));
-            if (v0) {
-              tma_load_3d(to, &map_k, 0, 0, page * c.KH + d.h, bar);
-              tma_load_3d(to + Shape<kD>::kSide, &map_v, 0, 0, page * c.KH + d.h, bar);
-            }
-            if (v1) {
-              tma_load_3d(to + 16 * kRowBytes, &map_k, 0, 0, page1 * c.KH + d.h, bar);
-              tma_load_3d(to + Shape<kD>::kSide + 16 * kRowBytes, &map_v, 0, 0, page1 * c.KH + d.h, bar);
-            }
-          }
+        }
+        if (elect_one()) {
+          sh.header[stage] = hd;
+          mbar_arrive(bar);
         }
         __syncwarp();
         if (++stage == kStages) {
@@ -409,6 +446,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 
   // ---- computing warps ----
+  // (128 registers a thread at launch; the loading side's share goes to these.)
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
   const int rw = warp % kRW, tw = warp / kRW;
   const int g = lane >> 2, j = lane & 3;
   const uint32_t sbase = smem_addr(smem);
@@ -420,18 +459,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.unit_empty[slot]);
 
-    // This warp's 16 rows: lane (g, j) holds rows g and g + 8, channels of quad j.
+    // This warp's rows. As columns of the score products: lane (g, j) holds
+    // row 8 t + g of column tile t, channels of quad j; of the results it gets
+    // rows 8 t + 2j and 8 t + 2j + 1.
     const int rows = min(kRows, d.n * p.G - d.rt * kRows);  // of the tile
-    uint32_t qa[kSteps][4];
-    float qf[2];   // score factor: scale log2(e) times the power of two taken from q
-    int pos[2];    // position of the row's token; -1: no such row
+    const int row_base = rw * 8 * kNT;
+    auto token_of = [&](int row) { return (d.rt * kRows + row) / p.G; };
+    auto position = [&](int row) { return row < rows ? d.len - d.n + token_of(row) : -1; };  // -1: no such row
+    uint32_t qb[kNT][kSteps][2];
+    float qf[kNT][2];   // score factors: scale log2(e) times the power of two taken from q
+    int pos[kNT][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = rw * 16 + g + 8 * r;
+    for (int t = 0; t < kNT; ++t) {
+      const int row = row_base + 8 * t + g;
       const int gr = d.rt * kRows + row;
       const int i = gr / p.G, head = d.h * p.G + gr % p.G;
       const bool live = row < rows;
-      pos[r] = live ? d.len - d.n + i : -1;
       constexpr int kMineCh = kD / 4;  // channels of a lane
       uint4 raw[kMineCh / 8];
       const uint4* src = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(d.t0 + i) * p.q_stride +
@@ -449,26 +492,36 @@ __global__ void __launch_bounds__(kThreads, 2)
       // Exponent of the largest magnitude (a BF16's bits order like its value).
       const int e = min(253, max(1, static_cast<int>(top >> 7)));
       const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-      qf[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(e) << 23);
+      const float f = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(e) << 23);
 #pragma unroll
       for (int x = 0; x < kMineCh / 8; ++x) {
         const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          qa[2 * x + y][r] = pack_f16x2(bf16_lo(w[2 * y]) * down, bf16_hi(w[2 * y]) * down);
-          qa[2 * x + y][2 + r] = pack_f16x2(bf16_lo(w[2 * y + 1]) * down, bf16_hi(w[2 * y + 1]) * down);
-        }
+        for (int y = 0; y < 4; ++y)
+          qb[t][2 * x + y / 2][y & 1] = pack_f16x2(bf16_lo(w[y]) * down, bf16_hi(w[y]) * down);
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        qf[t][r] = __shfl_sync(0xffffffffu, f, 8 * j + 4 * r);
+        pos[t][r] = position(row_base + 8 * t + 2 * j + r);
       }
     }
-    // Positions of the tile's first and last row: what every row sees of a chunk.
-    const int first_pos = d.len - d.n + (d.rt * kRows + rw * 16) / p.G;
-    const int last_row = min(rows, rw * 16 + 16) - 1;
-    const int last_pos = last_row >= rw * 16 ? d.len - d.n + (d.rt * kRows + last_row) / p.G : -1;
+    // Positions of the warp's first and last row: what every row sees of a chunk.
+    const int first_pos = d.len - d.n + token_of(row_base);
+    const int last_row = min(rows, row_base + 8 * kNT) - 1;
+    const int last_pos = last_row >= row_base ? d.len - d.n + token_of(last_row) : -1;
 
-    float o[kTiles][4];
+    float o[kTiles][kNT][4];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int t = 0; t < kNT; ++t) o[i][t][0] = o[i][t][1] = o[i][t][2] = o[i][t][3] = 0.0f;
+    float m[kNT][2], l[kNT][2];
+#pragma unroll
+    for (int t = 0; t < kNT; ++t) {
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.0f;
+    }
     int e0 = 0;
     bool started = false;
 
@@ -479,80 +532,93 @@ __global__ void __launch_bounds__(kThreads, 2)
       // for the barriers below, and the loading warp ends the work.)
       if (!mbar_wait_warp(&sh.full[stage], (it / kStages) & 1, c.status)) break;
       const ChunkHeader hd = sh.header[stage];
-      const uint32_t kbuf = sbase + stage * Shape<kD>::kStage, vbuf = kbuf + Shape<kD>::kSide;
+      const uint32_t kbuf = sbase + stage * S::kStage, vbuf = kbuf + S::kSide;
       const int tok = d.first + (d.c0 + it - d.it) * kChunk;
       if (!started) {
         e0 = hd.ev[0];
         started = true;
       }
-      // Scores.
-      float s[4][4];
+      // Scores: tokens 16 h + g (and + 8) of the chunk, rows 8 t + 2j, + 1.
+      float s[2][kNT][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
-        const uint32_t row = kbuf + (t * 8 + g) * kRowBytes;
-        if (kD == 128) {
-          const uint4 x = lds128(row + (((2 * j) ^ g) << 4)), y = lds128(row + (((2 * j + 1) ^ g) << 4));
-          const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k) mma16816(s[t], qa[k], codes_lo(w[k]), codes_hi(w[k]));
-        } else {
-          const uint4 x = lds128(row + ((j ^ (g >> 1)) << 4));
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        for (int t = 0; t < kNT; ++t) s[h][t][0] = s[h][t][1] = s[h][t][2] = s[h][t][3] = 0.0f;
+        const uint32_t row = kbuf + (h * 16 + g) * kRowBytes;
+        uint32_t w[2][kSteps];
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k) mma16816(s[t], qa[k], codes_lo(w[k]), codes_hi(w[k]));
+        for (int x = 0; x < 2; ++x) {
+          if (kD == 128) {
+            const uint4 a = lds128(row + 8 * x * kRowBytes + (((2 * j) ^ g) << 4));
+            const uint4 b = lds128(row + 8 * x * kRowBytes + (((2 * j + 1) ^ g) << 4));
+            w[x][0] = a.x; w[x][1] = a.y; w[x][2] = a.z; w[x][3] = a.w;
+            w[x][kSteps - 4] = b.x; w[x][kSteps - 3] = b.y; w[x][kSteps - 2] = b.z; w[x][kSteps - 1] = b.w;
+          } else {
+            const uint4 a = lds128(row + 8 * x * kRowBytes + ((j ^ (g >> 1)) << 4));
+            w[x][0] = a.x; w[x][1] = a.y; w[x][2] = a.z; w[x][3] = a.w;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          const uint32_t a[4] = {codes_lo(w[0][k]), codes_lo(w[1][k]), codes_hi(w[0][k]), codes_hi(w[1][k])};
+#pragma unroll
+          for (int t = 0; t < kNT; ++t) mma16816(s[h][t], a, qb[t][k][0], qb[t][k][1]);
         }
       }
       // In units of log2, the value block's exponent added.
       const bool masked = hd.valid != ~0u || tok + kChunk - 1 > first_pos ||
                           (p.window > 0 && tok <= last_pos - p.window) || last_pos < first_pos;
       const float el[2] = {static_cast<float>(hd.ev[0] - e0), static_cast<float>(hd.ev[1] - e0)};
-      float mx[2] = {-INFINITY, -INFINITY};
+      auto sees = [&](int at, int ps) {
+        return (hd.valid >> at & 1) && tok + at <= ps && !(p.window > 0 && tok + at <= ps - p.window);
+      };
+      float alpha[kNT][2], shift[kNT][2];
+      bool moved = false;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < kNT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[t][i] = fmaf(s[t][i], hd.ks[t >> 1] * qf[i >> 1], el[t >> 1]);
-          if (masked) {
-            const int at = t * 8 + 2 * j + (i & 1), ps = pos[i >> 1];
-            if (!(hd.valid >> at & 1) || tok + at > ps || (p.window > 0 && tok + at <= ps - p.window))
-              s[t][i] = -INFINITY;
-          }
-          mx[i >> 1] = fmaxf(mx[i >> 1], s[t][i]);
+        for (int r = 0; r < 2; ++r) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float& v = s[h][t][2 * x + r];
+              v = fmaf(v, hd.ks[h] * qf[t][r], el[h]);
+              if (masked && !sees(h * 16 + g + 8 * x, pos[t][r])) v = -INFINITY;
+              mx = fmaxf(mx, v);
+            }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float top = fmaxf(m[t][r], mx);
+          const float ref = top == -INFINITY ? 0.0f : top;
+          alpha[t][r] = ex2(m[t][r] - ref);
+          moved |= top > m[t][r];
+          m[t][r] = top;
+          l[t][r] *= alpha[t][r];
+          shift[t][r] = ref - kTop;
         }
-      }
-      float alpha[2], ref[2];
+      const float w0 = ex2(-el[0]), w1 = ex2(-el[1]);
+      uint32_t pb[2][kNT][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        const float top = fmaxf(m[r], mx[r]);
-        ref[r] = top == -INFINITY ? 0.0f : top;
-        alpha[r] = ex2(m[r] - ref[r]);
-        m[r] = top;
-        l[r] *= alpha[r];
-      }
-      const float el0 = ex2(-el[0]), el1 = ex2(-el[1]);
-      const float shift[2] = {ref[0] - kTop, ref[1] - kTop};
-      uint32_t pa[2][4];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < kNT; ++t) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] = ex2(s[t][i] - shift[i >> 1]);
-        const float w = t < 2 ? el0 : el1;
-        l[0] = fmaf(s[t][0] + s[t][1], w, l[0]);
-        l[1] = fmaf(s[t][2] + s[t][3], w, l[1]);
-        pa[t >> 1][(t & 1) * 2] = pack_f16x2(s[t][0], s[t][1]);
-        pa[t >> 1][(t & 1) * 2 + 1] = pack_f16x2(s[t][2], s[t][3]);
-      }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          o[i][0] *= alpha[0];
-          o[i][1] *= alpha[0];
-          o[i][2] *= alpha[1];
-          o[i][3] *= alpha[1];
+          for (int x = 0; x < 4; ++x) s[h][t][x] = ex2(s[h][t][x] - shift[t][x & 1]);
+          l[t][0] = fmaf(s[h][t][0] + s[h][t][2], h ? w1 : w0, l[t][0]);
+          l[t][1] = fmaf(s[h][t][1] + s[h][t][3], h ? w1 : w0, l[t][1]);
+          pb[h][t][0] = transpose8(pack_f16x2(s[h][t][0], s[h][t][1]));
+          pb[h][t][1] = transpose8(pack_f16x2(s[h][t][2], s[h][t][3]));
         }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+          for (int t = 0; t < kNT; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[i][t][x] *= alpha[t][x & 1];
       }
       // Values: lane (g, j) takes tokens 2j, 2j + 1, 2j + 8, 2j + 9 of each 16.
 #pragma unroll
@@ -584,109 +650,111 @@ __global__ void __launch_bounds__(kThreads, 2)
               v[x][w] &= ~(nan[x][w] * 0xFFu);
             }
           if (__any_sync(0xffffffffu, some != 0)) {
-            uint32_t sees[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              // Rows g (x even) and g + 8, tokens of score tile 2q + x / 2: 1 where the row sees the token.
-              uint32_t word = 0;
+            for (int t = 0; t < kNT; ++t) {
+              // 1 where row 8 t + g sees the token.
+              const int ps = position(row_base + 8 * t + g);
+              uint32_t in[2];
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const int at = q * 16 + (x >> 1) * 8 + 2 * j + y, ps = pos[x & 1];
-                const bool in = (hd.valid >> at & 1) && tok + at <= ps && !(p.window > 0 && tok + at <= ps - p.window);
-                if (in) word |= 0x3C00u << (16 * y);
+              for (int x = 0; x < 2; ++x) {
+                const int at = q * 16 + 8 * x + 2 * j;
+                in[x] = (sees(at, ps) ? 0x3C00u : 0u) | (sees(at + 1, ps) ? 0x3C000000u : 0u);
               }
-              sees[x] = word;
-            }
 #pragma unroll
-            for (int w = 0; w < kWords; ++w)
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
+              for (int i = 0; i < kTiles; ++i) {
                 float cnt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                auto one = [&](int x) { return nan[x][w] >> (8 * y) & 1u ? 0x3C00u : 0u; };
-                mma16816(cnt, sees, one(0) | one(1) << 16, one(2) | one(3) << 16);
+                auto one = [&](int x, int ch) { return nan[x][ch >> 2] >> (8 * (ch & 3)) & 1u ? 0x3C00u : 0u; };
+                const uint32_t a[4] = {one(0, 2 * i) | one(1, 2 * i) << 16, one(0, 2 * i + 1) | one(1, 2 * i + 1) << 16,
+                                       one(2, 2 * i) | one(3, 2 * i) << 16, one(2, 2 * i + 1) | one(3, 2 * i + 1) << 16};
+                mma16816(cnt, a, in[0], in[1]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (cnt[i] > 0.0f) o[4 * w + y][i] = __int_as_float(0x7FC00000);
+                for (int x = 0; x < 4; ++x)
+                  if (cnt[x] > 0.0f) o[i][t][x] = __int_as_float(0x7FC00000);
               }
+            }
           }
         }
 #pragma unroll
-        for (int w = 0; w < kWords; ++w) {
-          const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-          const uint32_t c0 = __byte_perm(v[2][w], v[3][w], 0x5140), c1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-          mma16816(o[4 * w], pa[q], codes_lo(a0), codes_lo(c0));
-          mma16816(o[4 * w + 1], pa[q], codes_hi(a0), codes_hi(c0));
-          mma16816(o[4 * w + 2], pa[q], codes_lo(a1), codes_lo(c1));
-          mma16816(o[4 * w + 3], pa[q], codes_hi(a1), codes_hi(c1));
-        }
+        for (int w = 0; w < kWords; ++w)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {  // channels 4 w + 2 y and the next
+            const uint32_t a = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
+            const uint32_t b = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
+            const uint32_t f[4] = {codes_lo(a), codes_hi(a), codes_lo(b), codes_hi(b)};
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) mma16816(o[2 * w + y][t], f, pb[q][t][0], pb[q][t][1]);
+          }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.empty[stage]);
     }
 
     // ---- end of the run of chunks: join the groups ----
+    float md[kNT][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    }
-    // m is the numerator's reference with the values' exponents: 2^(m + e0) o;
-    // the normaliser is 2^m l.
-    float md[2] = {m[0] - kTop, m[1] - kTop};
-    m[0] = md[0] + static_cast<float>(e0);
-    m[1] = md[1] + static_cast<float>(e0);
+    for (int t = 0; t < kNT; ++t)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], 4);
+        l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], 8);
+        l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], 16);
+        // The numerator is 2^m o, the values' exponents in m; the normaliser 2^md l.
+        md[t][r] = m[t][r] - kTop;
+        m[t][r] = md[t][r] + static_cast<float>(e0);
+      }
     if (kTW > 1) {
       compute_sync();  // the first group is done with the last unit's
       if (tw > 0) {
         const int w = (tw - 1) * kRW + rw;
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) sh.join_o[w][i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-        sh.join_ml[w][0][lane] = make_float4(m[0], md[0], l[0], 0.0f);
-        sh.join_ml[w][1][lane] = make_float4(m[1], md[1], l[1], 0.0f);
+        for (int t = 0; t < kNT; ++t) {
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+            sh.join_o[w][i * kNT + t][lane] = make_float4(o[i][t][0], o[i][t][1], o[i][t][2], o[i][t][3]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            sh.join_ml[w][2 * t + r][lane] = make_float4(m[t][r], md[t][r], l[t][r], 0.0f);
+        }
       }
       compute_sync();
       if (tw == 0) {
-        float4 x[kTW][2];  // each group's references and sum
-        x[0][0] = make_float4(m[0], md[0], l[0], 0.0f);
-        x[0][1] = make_float4(m[1], md[1], l[1], 0.0f);
 #pragma unroll
-        for (int w = 1; w < kTW; ++w) {
-          x[w][0] = sh.join_ml[(w - 1) * kRW + rw][0][lane];
-          x[w][1] = sh.join_ml[(w - 1) * kRW + rw][1][lane];
-        }
-        float f[kTW][2];
+        for (int t = 0; t < kNT; ++t) {
+          float f[kTW][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float top = -INFINITY, topd = -INFINITY;
+          for (int r = 0; r < 2; ++r) {
+            float4 x[kTW];  // each group's references and sum
+            x[0] = make_float4(m[t][r], md[t][r], l[t][r], 0.0f);
+            float top = m[t][r], topd = md[t][r];
 #pragma unroll
-          for (int w = 0; w < kTW; ++w) {
-            top = fmaxf(top, x[w][r].x);
-            topd = fmaxf(topd, x[w][r].y);
+            for (int w = 1; w < kTW; ++w) {
+              x[w] = sh.join_ml[(w - 1) * kRW + rw][2 * t + r][lane];
+              top = fmaxf(top, x[w].x);
+              topd = fmaxf(topd, x[w].y);
+            }
+            const float rt = top == -INFINITY ? 0.0f : top, rd = topd == -INFINITY ? 0.0f : topd;
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kTW; ++w) {
+              f[w][r] = ex2(x[w].x - rt);
+              sum = fmaf(ex2(x[w].y - rd), x[w].z, sum);
+            }
+            m[t][r] = top;
+            md[t][r] = topd;
+            l[t][r] = sum;
           }
-          const float rt = top == -INFINITY ? 0.0f : top, rd = topd == -INFINITY ? 0.0f : topd;
-          float sum = 0.0f;
 #pragma unroll
-          for (int w = 0; w < kTW; ++w) {
-            f[w][r] = ex2(x[w][r].x - rt);
-            sum = fmaf(ex2(x[w][r].y - rd), x[w][r].z, sum);
-          }
-          m[r] = top;
-          md[r] = topd;
-          l[r] = sum;
-        }
+          for (int i = 0; i < kTiles; ++i) {
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          o[i][0] *= f[0][0];
-          o[i][1] *= f[0][0];
-          o[i][2] *= f[0][1];
-          o[i][3] *= f[0][1];
+            for (int x = 0; x < 4; ++x) o[i][t][x] *= f[0][x & 1];
 #pragma unroll
-          for (int w = 1; w < kTW; ++w) {
-            const float4 y = sh.join_o[(w - 1) * kRW + rw][i][lane];
-            o[i][0] = fmaf(f[w][0], y.x, o[i][0]);
-            o[i][1] = fmaf(f[w][0], y.y, o[i][1]);
-            o[i][2] = fmaf(f[w][1], y.z, o[i][2]);
-            o[i][3] = fmaf(f[w][1], y.w, o[i][3]);
+            for (int w = 1; w < kTW; ++w) {
+              const float4 y = sh.join_o[(w - 1) * kRW + rw][i * kNT + t][lane];
+              o[i][t][0] = fmaf(f[w][0], y.x, o[i][t][0]);
+              o[i][t][1] = fmaf(f[w][1], y.y, o[i][t][1]);
+              o[i][t][2] = fmaf(f[w][0], y.z, o[i][t][2]);
+              o[i][t][3] = fmaf(f[w][1], y.w, o[i][t][3]);
+            }
           }
         }
       }
@@ -696,28 +764,26 @@ __global__ void __launch_bounds__(kThreads, 2)
       return static_cast<int64_t>(d.t0 + gr / p.G) * p.QH + d.h * p.G + gr % p.G;
     };
     const bool whole = d.c0 == 0 && d.c1 == d.total;
-    // Lane (g, j) holds row g (and g + 8), channels [j kD / 4, (j + 1) kD / 4):
-    // the first half from c0 (c2), the second from c1 (c3) of the tiles in turn.
+    // Lane (g, j) holds rows 8 t + 2j and + 1, channels [g kD / 8, (g + 1) kD / 8).
     if (whole) {
       if (tw == 0) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = rw * 16 + g + 8 * r;
-          if (row >= rows) continue;
-          const float f = l[r] > 0.0f ? ex2(m[r] - md[r]) / l[r] : (l[r] == 0.0f ? 0.0f : l[r]);
-          const int64_t at = out_of(row);
-          uint4* to = reinterpret_cast<uint4*>(p.out + at * kD + j * (kD / 4));
+        for (int t = 0; t < kNT; ++t)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int r = 0; r < 2; ++r) {
+            const int row = row_base + 8 * t + 2 * j + r;
+            if (row >= rows) continue;
+            const float f = l[t][r] > 0.0f ? ex2(m[t][r] - md[t][r]) / l[t][r] : (l[t][r] == 0.0f ? 0.0f : l[t][r]);
+            const int64_t at = out_of(row);
+            uint4* to = reinterpret_cast<uint4*>(p.out + at * kD + g * (kD / 8));
 #pragma unroll
-            for (int i = 0; i < kTiles; i += 8)
-              to[(x * kTiles + i) / 8] =
-                  make_uint4(pack_bf16x2(o[i][2 * r + x] * f, o[i + 1][2 * r + x] * f),
-                             pack_bf16x2(o[i + 2][2 * r + x] * f, o[i + 3][2 * r + x] * f),
-                             pack_bf16x2(o[i + 4][2 * r + x] * f, o[i + 5][2 * r + x] * f),
-                             pack_bf16x2(o[i + 6][2 * r + x] * f, o[i + 7][2 * r + x] * f));
-          if (p.lse && j == 0) p.lse[at] = (md[r] + log2f(l[r])) * kLn2;
-        }
+            for (int i = 0; i < kTiles; i += 4)
+              to[i / 4] = make_uint4(pack_bf16x2(o[i][t][r] * f, o[i][t][2 + r] * f),
+                                     pack_bf16x2(o[i + 1][t][r] * f, o[i + 1][t][2 + r] * f),
+                                     pack_bf16x2(o[i + 2][t][r] * f, o[i + 2][t][2 + r] * f),
+                                     pack_bf16x2(o[i + 3][t][r] * f, o[i + 3][t][2 + r] * f));
+            if (p.lse && g == 0) p.lse[at] = (md[t][r] + log2f(l[t][r])) * kLn2;
+          }
       }
       continue;
     }
@@ -805,19 +871,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (tw == 0) {
       float* to = part(blockIdx.x, d.c0 == 0);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = rw * 16 + g + 8 * r;
-        if (row >= rows) continue;
-        float4* v = reinterpret_cast<float4*>(to + row * kD + j * (kD / 4));
+      for (int t = 0; t < kNT; ++t)
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int r = 0; r < 2; ++r) {
+          const int row = row_base + 8 * t + 2 * j + r;
+          if (row >= rows) continue;
+          float4* v = reinterpret_cast<float4*>(to + row * kD + g * (kD / 8));
 #pragma unroll
-          for (int i = 0; i < kTiles; i += 4)
-            __stcg(v + (x * kTiles + i) / 4, make_float4(o[i][2 * r + x], o[i + 1][2 * r + x], o[i + 2][2 * r + x],
-                                                         o[i + 3][2 * r + x]));
-        if (j == 0)
-          __stcg(reinterpret_cast<float4*>(to + kRows * kD) + row, make_float4(m[r], md[r], l[r], 0.0f));
-      }
+          for (int i = 0; i < kTiles; i += 2)
+            __stcg(v + i / 2, make_float4(o[i][t][r], o[i][t][2 + r], o[i + 1][t][r], o[i + 1][t][2 + r]));
+          if (g == 0)
+            __stcg(reinterpret_cast<float4*>(to + kRows * kD) + row, make_float4(m[t][r], md[t][r], l[t][r], 0.0f));
+        }
     }
     const int parts = c_last - c_first + 1;
     if (parts <= 2 * kFan) {
@@ -847,40 +912,47 @@ bool cache_map(CUtensorMap* map, uint8_t* base, const KVParams& c) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kD, int kRW>
+template <int kD, int kNT, int kRW>
 cudaError_t launch(const KVAttentionParams& p, cudaStream_t s) {
   CUtensorMap mk, mv;
   if (!cache_map(&mk, p.c.k, p.c) || !cache_map(&mv, p.c.v, p.c)) return cudaErrorInvalidValue;
-  const size_t smem = Shape<kD>::kStages * Shape<kD>::kStage + sizeof(Shared<kD, kRW>) + 1024;
-  const auto fn = kv_attention_kernel<kD, kRW>;
+  using S = Shape<kD, kNT>;
+  const size_t smem = S::kStages * S::kStage + sizeof(Shared<kD, kNT, kRW>) + 1024;
+  const auto fn = kv_attention_kernel<kD, kNT, kRW>;
   const int dev = current_device();
   const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(fn), dev, smem);
   if (err != cudaSuccess) return err;
   const int sms = device_sms(dev);
   if (sms < 1) return cudaErrorInvalidDevice;
-  const int grid = 2 * sms < kMaxBlocks ? 2 * sms : kMaxBlocks;
+  const int grid = S::kBlocksPerSM * sms < kMaxBlocks ? S::kBlocksPerSM * sms : kMaxBlocks;
   return launch_kernel(fn, dim3(grid), dim3(kThreads), smem, s, /*dependent=*/true, p,
                        reinterpret_cast<float*>(p.ws + 4096), reinterpret_cast<unsigned*>(p.ws), mk, mv);
 }
 
-// Row tiles of 16, 32 or 64: the smallest that holds a sequence's rows of one
+// Row tiles of 8, 16, 32 or 64: the smallest that holds a sequence's rows of one
 // cache head, so that its cache is read once.
-int row_warps(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+int tile_rows_for(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+template <int kD>
+cudaError_t launch_rows(const KVAttentionParams& p, int rows, cudaStream_t s) {
+  return rows == 8    ? launch<kD, 1, 1>(p, s)
+         : rows == 16 ? launch<kD, 2, 1>(p, s)
+         : rows == 32 ? launch<kD, 2, 2>(p, s)
+                      : launch<kD, 2, 4>(p, s);
+}
 
 }  // namespace
 
 size_t kv_attention_ws_bytes(int N, int QH, int KH, int D) {
-  const int rows = 16 * row_warps(static_cast<int64_t>(N) * (QH / KH));
+  const int rows = tile_rows_for(static_cast<int64_t>(N) * (QH / KH));
   return 4096 + sizeof(float) * kMaxBlocks * 2 * rows * static_cast<size_t>(D + 4);
 }
 
 cudaError_t launch_kv_attention(const KVAttentionParams& p, cudaStream_t s) {
   if (p.c.N <= 0) return cudaSuccess;
   const int64_t each = (static_cast<int64_t>(p.c.N) + p.c.B - 1) / p.c.B;  // new tokens a sequence
-  const int rw = row_warps(each * p.G);
-  if (p.c.pages == 0) return cudaErrorInvalidValue;
-  if (p.c.D == 64) return rw == 1 ? launch<64, 1>(p, s) : rw == 2 ? launch<64, 2>(p, s) : launch<64, 4>(p, s);
-  return rw == 1 ? launch<128, 1>(p, s) : rw == 2 ? launch<128, 2>(p, s) : launch<128, 4>(p, s);
+  const int rows = tile_rows_for(each * p.G);
+  return p.c.D == 64 ? launch_rows<64>(p, rows, s) : launch_rows<128>(p, rows, s);
 }
 
 }  // namespace ep

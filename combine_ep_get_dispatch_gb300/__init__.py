@@ -384,35 +384,68 @@ def ep_fp8_quantize(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, fp8:
            "ep_fp8_quantize")
 
 
-def _heads(t: Optional[torch.Tensor], what: str, dtype=torch.bfloat16):
-    """Pointer and token stride of a [tokens, heads, dim] tensor whose heads are contiguous."""
-    if t is None:
-        return None, 0
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 3:
-        raise ValueError(f"{what}: expected a CUDA tensor [tokens, heads, dim] of {dtype}")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+# A decode step's calls are as short on the GPU as their marshalling is on the
+# host (a torch call costs this host 0.1 us for each attribute that it asks a
+# tensor for), so these ask for each once and hand plain integers to ctypes.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _heads(t: torch.Tensor, what: str) -> Tuple[int, int, int, int, int]:
+    """(address, token stride, tokens, heads, dim) of a [tokens, heads, dim] bf16 tensor with contiguous heads."""
+    if t.dtype is not _BF16 or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{what}: expected a CUDA tensor [tokens, heads, dim] of {_BF16}")
+    n, heads, dim = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 or (s1 != dim and heads > 1)) and t.numel():
         raise ValueError(f"{what}: heads must be contiguous")
     # One token (or none) has no stride of its own.
-    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-    return ctypes.c_void_p(t.data_ptr()), stride
+    return t.data_ptr(), s0 if n > 1 else heads * dim, n, heads, dim
 
 
-def _typed(t: Optional[torch.Tensor], what: str, dtype, shape=None) -> Optional[torch.Tensor]:
-    if t is not None and (t.dtype != dtype or (shape is not None and tuple(t.shape) != tuple(shape))):
+def _address(t: Optional[torch.Tensor], what: str, dtype, shape=None) -> Optional[int]:
+    """Address of a contiguous CUDA tensor of the dtype (and shape)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or (shape is not None and t.shape != shape):
         raise ValueError(f"{what}: expected {dtype}" + (f" of shape {tuple(shape)}" if shape is not None else ""))
-    return t
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _raw(stream) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(_get_device())
+    return _stream(stream).value or 0
 
 
 def ep_kv_append(cache: "KVCache", seq_lens, cu_tokens, k, v, q, q_out, rope, interleaved, status=None,
                  stream=None) -> None:
-    kp, ks = _heads(k, "k")
-    vp, vs = _heads(v, "v")
-    qp, qs = _heads(q, "q")
-    op, os_ = _heads(q_out, "q_out")
-    rows, dim = rope.shape if rope is not None else (0, 0)
-    _check(lib().ep_kv_append(ctypes.byref(cache.c_struct()), _p(seq_lens), _p(cu_tokens), k.shape[0], kp, ks, vp, vs,
-                              qp, qs, op, os_, q.shape[1] if q is not None else 0, _p(rope), rows, dim,
-                              int(bool(interleaved)), _p(status), _stream(stream)), "ep_kv_append")
+    if cache._c is None:
+        cache.c_struct()
+    kp, ks, tokens, heads, dim = _heads(k, "k")
+    vp, vs, vt, vh, vd = _heads(v, "v")
+    if heads != cache.heads or dim != cache.dim or vt != tokens or vh != heads or vd != dim:
+        raise ValueError("k, v: expected [tokens, heads, dim] of the cache's heads")
+    qp = op = None
+    qs = os_ = qh = rows = rot = 0
+    if q is not None:
+        qp, qs, qt, qh, qd = _heads(q, "q")
+        op, os_, ot, oh, od = (qp, qs, qt, qh, qd) if q_out is q else _heads(q_out, "q_out")
+        if qt != tokens or qd != dim or ot != tokens or oh != qh or od != dim:
+            raise ValueError("q, q_out: expected [tokens, q_heads, dim]")
+    rp = _address(rope, "rope", _F32)
+    if rp is not None:
+        rows, rot = rope.shape
+    rc = lib().ep_kv_append(cache.c_ref, _address(seq_lens, "seq_lens", _I32, cache.seqs),
+                            cu_tokens if cu_tokens is None else _address(cu_tokens, "cu_tokens", _I32, cache.cu_shape),
+                            tokens, kp, ks, vp, vs, qp, qs, op, os_, qh, rp, rows, rot, 1 if interleaved else 0,
+                            status if status is None else _address(status, "status", _I32), _raw(stream))
+    if rc != EP_OK:
+        raise EPError("ep_kv_append", rc)
 
 
 def ep_kv_attention_workspace_bytes(num_tokens: int, num_q_heads: int, num_heads: int, head_dim: int) -> int:
@@ -421,10 +454,20 @@ def ep_kv_attention_workspace_bytes(num_tokens: int, num_q_heads: int, num_heads
 
 def ep_kv_attention(cache: "KVCache", seq_lens, cu_tokens, q, scale, window, out, lse, workspace, status=None,
                     stream=None) -> None:
-    qp, qs = _heads(q, "q")
-    _check(lib().ep_kv_attention(ctypes.byref(cache.c_struct()), _p(seq_lens), _p(cu_tokens), q.shape[0], qp, qs,
-                                 q.shape[1], float(scale), int(window), _p(out), _p(lse), _p(workspace),
-                                 workspace.numel(), _p(status), _stream(stream)), "ep_kv_attention")
+    if cache._c is None:
+        cache.c_struct()
+    qp, qs, tokens, heads, dim = _heads(q, "q")
+    if dim != cache.dim:
+        raise ValueError("q: expected [tokens, q_heads, dim] of the cache's dim")
+    rc = lib().ep_kv_attention(cache.c_ref, _address(seq_lens, "seq_lens", _I32, cache.seqs),
+                               cu_tokens if cu_tokens is None else
+                               _address(cu_tokens, "cu_tokens", _I32, cache.cu_shape),
+                               tokens, qp, qs, heads, scale, window, _address(out, "out", _BF16, q.shape),
+                               lse if lse is None else _address(lse, "lse", _F32, (tokens, heads)),
+                               _address(workspace, "workspace", _U8), workspace.numel(),
+                               status if status is None else _address(status, "status", _I32), _raw(stream))
+    if rc != EP_OK:
+        raise EPError("ep_kv_attention", rc)
 
 
 def ep_expert_linear_workspace_bytes(num_experts: int, max_rows: int, in_features: int, x_is_fp8: bool) -> int:
@@ -433,10 +476,16 @@ def ep_expert_linear_workspace_bytes(num_experts: int, max_rows: int, in_feature
 
 def ep_expert_linear(x, x_scale, x_rows, in_features, row_count, row_offset, rows_per_expert, max_rows, w, w_scale,
                      flags, y, workspace, status=None, stream=None) -> None:
-    _check(lib().ep_expert_linear(_p(x), _p(x_scale), x_rows, in_features, _p(row_count), _p(row_offset),
-                                  rows_per_expert, w.shape[0], max_rows, _p(w), _p(w_scale), w.shape[1], int(flags),
-                                  _p(y), _p(workspace), workspace.numel(), _p(status), _stream(stream)),
-           "ep_expert_linear")
+    E, M, half = w.shape
+    rc = lib().ep_expert_linear(_address(x, "x", _BF16 if x_scale is None else _U8),
+                                _address(x_scale, "x_scale", _U8), x_rows, in_features,
+                                _address(row_count, "row_count", _I32),
+                                _address(row_offset, "row_offset", _I32), rows_per_expert, E, max_rows,
+                                _address(w, "weight", _U8), _address(w_scale, "weight_scale", _U8), M,
+                                flags, _address(y, "out", _BF16), _address(workspace, "workspace", _U8),
+                                workspace.numel(), _address(status, "status", _I32), _raw(stream))
+    if rc != EP_OK:
+        raise EPError("ep_expert_linear", rc)
 
 
 # -------------------------------------------------------------- page-level ----
@@ -750,13 +799,15 @@ class KVCache:
             if self.k.dim() != 4 or self.page_table.dim() != 2:
                 raise ValueError("KVCache: k is [pages, heads, page_size, head_dim], page_table [seqs, max_pages]")
             pages, heads, size, dim = self.k.shape
-            _typed(self.k, "k", torch.uint8)
-            _typed(self.v, "v", torch.uint8, self.k.shape)
-            _typed(self.k_scale, "k_scale", torch.float32, (pages, heads))
-            _typed(self.v_scale, "v_scale", torch.float32, (pages, heads))
-            _typed(self.page_table, "page_table", torch.int32)
-            self._c = ep_kv_cache_t(_p(self.k), _p(self.v), _p(self.k_scale), _p(self.v_scale), _p(self.page_table),
-                                    pages, heads, size, dim, *self.page_table.shape)
+            seqs, most = self.page_table.shape
+            addresses = (_address(self.k, "k", torch.uint8), _address(self.v, "v", torch.uint8, self.k.shape),
+                         _address(self.k_scale, "k_scale", torch.float32, (pages, heads)),
+                         _address(self.v_scale, "v_scale", torch.float32, (pages, heads)),
+                         _address(self.page_table, "page_table", torch.int32))
+            self._c = ep_kv_cache_t(*addresses, pages, heads, size, dim, seqs, most)
+            self.c_ref = ctypes.byref(self._c)
+            self.heads, self.dim = heads, dim
+            self.seqs, self.cu_shape = torch.Size((seqs,)), torch.Size((seqs + 1,))
         return self._c
 
 
@@ -782,16 +833,6 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, seq_lens: torch.
     """
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _, heads, _, dim = cache.k.shape
-    _typed(k, "k", torch.bfloat16, (k.shape[0], heads, dim))
-    _typed(v, "v", torch.bfloat16, k.shape)
-    if q is not None:
-        _typed(q, "q", torch.bfloat16, (k.shape[0], q.shape[1], dim))
-        _typed(q_out, "q_out", torch.bfloat16, q.shape)
-    seqs = cache.page_table.shape[0]
-    _typed(seq_lens, "seq_lens", torch.int32, (seqs,))
-    _typed(cu_tokens, "cu_tokens", torch.int32, (seqs + 1,))
-    _typed(rope, "rope", torch.float32)
     ep_kv_append(cache, seq_lens, cu_tokens, k, v, q, q_out, rope, interleaved, status, stream)
     return q_out
 
@@ -815,19 +856,13 @@ def kv_attention(q: torch.Tensor, cache: KVCache, seq_lens: torch.Tensor, cu_tok
     workspace passed in must have been zero-filled once (kv_attention_workspace
     makes one); without it, one is made. Returns out, or (out, lse).
     """
-    T, QH, dim = q.shape
-    _typed(q, "q", torch.bfloat16, (T, QH, cache.k.shape[3]))
-    seqs = cache.page_table.shape[0]
-    _typed(seq_lens, "seq_lens", torch.int32, (seqs,))
-    _typed(cu_tokens, "cu_tokens", torch.int32, (seqs + 1,))
     if out is None:
-        out = torch.empty((T, QH, dim), dtype=torch.bfloat16, device=q.device)
-    _typed(out, "out", torch.bfloat16, q.shape)
-    lse = torch.empty((T, QH), dtype=torch.float32, device=q.device) if return_lse else None
+        out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
     if workspace is None:
         workspace = kv_attention_workspace(q, cache)
-    ep_kv_attention(cache, seq_lens, cu_tokens, q, dim ** -0.5 if scale is None else scale, window, out, lse, workspace,
-                    status, stream)
+    ep_kv_attention(cache, seq_lens, cu_tokens, q, q.shape[2] ** -0.5 if scale is None else scale, window, out, lse,
+                    workspace, status, stream)
     return (out, lse) if return_lse else out
 
 
@@ -859,21 +894,22 @@ def expert_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Ten
     """
     E, M, half = weight.shape
     K = x.shape[-1]
-    _typed(weight, "weight", torch.uint8, (E, M, K // 2))
-    _typed(weight_scale, "weight_scale", torch.uint8, (E, M, K // 32))
-    _typed(row_count, "row_count", torch.int32, (E,))
-    _typed(row_offset, "row_offset", torch.int32)
-    _typed(x, "x", torch.bfloat16 if x_scale is None else torch.uint8)
-    _typed(x_scale, "x_scale", torch.uint8, (*x.shape[:-1], K // 128))
-    if row_offset is None and (x.dim() != 3 or x.shape[0] != E):
-        raise ValueError("x: expected [num_experts, cap, in] without row_offset")
-    if row_offset is not None and row_offset.numel() < E:
-        raise ValueError("row_offset: expected an offset for each expert")
     rows = x.numel() // K
-    shape = (*x.shape[:-1], M // 2 if glu else M)
+    lead = x.shape[:-1]
+    if weight_scale.shape != (E, M, K // 32) or 2 * half != K or row_count.shape != (E,):
+        raise ValueError("weight, weight_scale, row_count: expected [E, out, in/2], [E, out, in/32] and [E]")
+    if x_scale is not None and x_scale.shape != (*lead, K // 128):
+        raise ValueError("x_scale: expected a byte for each 128 channels of x")
+    if row_offset is None:
+        if x.dim() != 3 or x.shape[0] != E:
+            raise ValueError("x: expected [num_experts, cap, in] without row_offset")
+    elif row_offset.numel() < E:
+        raise ValueError("row_offset: expected an offset for each expert")
+    shape = (*lead, M // 2 if glu else M)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-    _typed(out, "out", torch.bfloat16, shape)
+        out = torch.empty(shape, dtype=_BF16, device=x.device)
+    elif out.shape != shape:
+        raise ValueError(f"out: expected shape {shape}")
     limit = rows if max_rows is None else int(max_rows)
     if workspace is None:
         workspace = expert_linear_workspace(x, weight, limit)

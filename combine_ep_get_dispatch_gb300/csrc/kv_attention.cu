@@ -46,7 +46,7 @@ namespace {
 constexpr int kChunk = 32;       // tokens
 constexpr int kWarps = 4;        // computing warps
 constexpr int kThreads = 256;    // the computing warps, a loading one, and three that complete its warpgroup
-constexpr int kComputeRegs = 208, kLoadRegs = 40;  // of the 2 x 128 a thread pair is launched with
+constexpr int kComputeRegs = 216, kLoadRegs = 40;  // of the 2 x 128 a thread pair is launched with
 constexpr int kMaxBlocks = 320;  // blocks a workspace has room for
 constexpr int kFan = 8;          // parts of a shared unit that one block joins at once
 constexpr int kUnitCost = 6;     // chunks that a unit costs besides its own: queries, joining, results
@@ -106,7 +106,7 @@ struct Shared {
   Sequence find;
   int bad;
   int last;
-  static constexpr int kJoin = kTW > 1 ? (kTW - 1) * kRW : 0;
+  static constexpr int kJoin = kTW / 2 * kRW;  // warps that hand their sums over at once
   float4 join_o[kJoin ? kJoin : 1][kJoin ? kD / 16 * kNT : 1][32];
   float4 join_ml[kJoin ? kJoin : 1][2 * kNT][32];  // a row's references and sum
 };
@@ -541,28 +541,28 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
       // Scores: tokens 16 h + g (and + 8) of the chunk, rows 8 t + 2j, + 1.
       float s[2][kNT][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int t = 0; t < kNT; ++t) s[h][t][0] = s[h][t][1] = s[h][t][2] = s[h][t][3] = 0.0f;
-        const uint32_t row = kbuf + (h * 16 + g) * kRowBytes;
-        uint32_t w[2][kSteps];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (kD == 128) {
-            const uint4 a = lds128(row + 8 * x * kRowBytes + (((2 * j) ^ g) << 4));
-            const uint4 b = lds128(row + 8 * x * kRowBytes + (((2 * j + 1) ^ g) << 4));
-            w[x][0] = a.x; w[x][1] = a.y; w[x][2] = a.z; w[x][3] = a.w;
-            w[x][kSteps - 4] = b.x; w[x][kSteps - 3] = b.y; w[x][kSteps - 2] = b.z; w[x][kSteps - 1] = b.w;
-          } else {
-            const uint4 a = lds128(row + 8 * x * kRowBytes + ((j ^ (g >> 1)) << 4));
-            w[x][0] = a.x; w[x][1] = a.y; w[x][2] = a.z; w[x][3] = a.w;
+      for (int k0 = 0; k0 < kSteps; k0 += 4) {  // four steps: 16 bytes of a token's keys a lane
+        uint32_t w[2][2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t row = kbuf + (h * 16 + 8 * x + g) * kRowBytes;
+            const uint4 a = lds128(row + (kD == 128 ? ((2 * j + k0 / 4) ^ g) << 4 : (j ^ (g >> 1)) << 4));
+            w[h][x][0] = a.x; w[h][x][1] = a.y; w[h][x][2] = a.z; w[h][x][3] = a.w;
           }
-        }
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          const uint32_t a[4] = {codes_lo(w[0][k]), codes_lo(w[1][k]), codes_hi(w[0][k]), codes_hi(w[1][k])};
+        for (int k = 0; k < 4; ++k) {
 #pragma unroll
-          for (int t = 0; t < kNT; ++t) mma16816(s[h][t], a, qb[t][k][0], qb[t][k][1]);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {codes_lo(w[h][0][k]), codes_lo(w[h][1][k]), codes_hi(w[h][0][k]), codes_hi(w[h][1][k])};
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) mma16816(s[h][t], a, qb[t][k0 + k][0], qb[t][k0 + k][1]);
+          }
         }
       }
       // In units of log2, the value block's exponent added.
@@ -702,10 +702,12 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
         md[t][r] = m[t][r] - kTop;
         m[t][r] = md[t][r] + static_cast<float>(e0);
       }
-    if (kTW > 1) {
-      compute_sync();  // the first group is done with the last unit's
-      if (tw > 0) {
-        const int w = (tw - 1) * kRW + rw;
+    // Half of the groups hands over to the other half, until one is left.
+#pragma unroll
+    for (int half = kTW / 2; half >= 1; half /= 2) {
+      compute_sync();  // what was handed over before has been read
+      if (tw >= half && tw < 2 * half) {
+        const int w = (tw - half) * kRW + rw;
 #pragma unroll
         for (int t = 0; t < kNT; ++t) {
 #pragma unroll
@@ -717,44 +719,29 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
         }
       }
       compute_sync();
-      if (tw == 0) {
+      if (tw < half) {
+        const int w = tw * kRW + rw;
 #pragma unroll
         for (int t = 0; t < kNT; ++t) {
-          float f[kTW][2];
+          float f[2], fo[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float4 x[kTW];  // each group's references and sum
-            x[0] = make_float4(m[t][r], md[t][r], l[t][r], 0.0f);
-            float top = m[t][r], topd = md[t][r];
-#pragma unroll
-            for (int w = 1; w < kTW; ++w) {
-              x[w] = sh.join_ml[(w - 1) * kRW + rw][2 * t + r][lane];
-              top = fmaxf(top, x[w].x);
-              topd = fmaxf(topd, x[w].y);
-            }
+            const float4 x = sh.join_ml[w][2 * t + r][lane];
+            const float top = fmaxf(m[t][r], x.x), topd = fmaxf(md[t][r], x.y);
             const float rt = top == -INFINITY ? 0.0f : top, rd = topd == -INFINITY ? 0.0f : topd;
-            float sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kTW; ++w) {
-              f[w][r] = ex2(x[w].x - rt);
-              sum = fmaf(ex2(x[w].y - rd), x[w].z, sum);
-            }
+            f[r] = ex2(m[t][r] - rt);
+            fo[r] = ex2(x.x - rt);
+            l[t][r] = fmaf(ex2(x.y - rd), x.z, l[t][r] * ex2(md[t][r] - rd));
             m[t][r] = top;
             md[t][r] = topd;
-            l[t][r] = sum;
           }
 #pragma unroll
           for (int i = 0; i < kTiles; ++i) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[i][t][x] *= f[0][x & 1];
-#pragma unroll
-            for (int w = 1; w < kTW; ++w) {
-              const float4 y = sh.join_o[(w - 1) * kRW + rw][i * kNT + t][lane];
-              o[i][t][0] = fmaf(f[w][0], y.x, o[i][t][0]);
-              o[i][t][1] = fmaf(f[w][1], y.y, o[i][t][1]);
-              o[i][t][2] = fmaf(f[w][0], y.z, o[i][t][2]);
-              o[i][t][3] = fmaf(f[w][1], y.w, o[i][t][3]);
-            }
+            const float4 y = sh.join_o[w][i * kNT + t][lane];
+            o[i][t][0] = fmaf(fo[0], y.x, o[i][t][0] * f[0]);
+            o[i][t][1] = fmaf(fo[1], y.y, o[i][t][1] * f[1]);
+            o[i][t][2] = fmaf(fo[0], y.z, o[i][t][2] * f[0]);
+            o[i][t][3] = fmaf(fo[1], y.w, o[i][t][3] * f[1]);
           }
         }
       }
@@ -813,58 +800,79 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
     // Join parts first, first + step, ... below stop (the unit's first one lies in its block's
     // second slot): into part `to`, or as the result when `to` is null.
     auto join = [&](int first, int step, int stop, float* to) {
-      for (int i = tid; i < rows * (kD / 4); i += 128) {
-        const int row = i / (kD / 4), ch = i % (kD / 4);
-        const int n = (stop - first + step - 1) / step;
-        float top = -INFINITY, topd = -INFINITY, sum = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int k0 = 0; k0 < n; k0 += kFan) {
-          float4 y[kFan], v[kFan];
+      const int n = (stop - first + step - 1) / step;
+      constexpr int kVec = kD / 4;            // float4 of a row
+      constexpr int kAtOnce = 2;              // rows a thread works on side by side
+      constexpr int kStride = 128 / kVec;     // rows of the block's threads
+      const int ch = tid % kVec;
+      for (int r0 = tid / kVec; r0 < rows; r0 += kAtOnce * kStride) {
+        float top[kAtOnce], topd[kAtOnce], sum[kAtOnce];
+        float4 acc[kAtOnce];
 #pragma unroll
-          for (int k = 0; k < kFan; ++k) {
-            const int b = first + (k0 + k) * step;
-            y[k] = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
-            v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (b < stop) {
-              const float* from = part(b, b == c_first);
-              y[k] = __ldcg(reinterpret_cast<const float4*>(from + kRows * kD) + row);
-              v[k] = __ldcg(reinterpret_cast<const float4*>(from + row * kD) + ch);
-            }
-          }
-          float t = top, td = topd;
-#pragma unroll
-          for (int k = 0; k < kFan; ++k) {
-            t = fmaxf(t, y[k].x);
-            td = fmaxf(td, y[k].y);
-          }
-          const float rt = t == -INFINITY ? 0.0f : t, rd = td == -INFINITY ? 0.0f : td;
-          const float keep = ex2(top - rt);
-          sum *= ex2(topd - rd);
-          acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
-#pragma unroll
-          for (int k = 0; k < kFan; ++k) {
-            const float f = ex2(y[k].x - rt);
-            sum = fmaf(ex2(y[k].y - rd), y[k].z, sum);
-            acc.x = fmaf(f, v[k].x, acc.x);
-            acc.y = fmaf(f, v[k].y, acc.y);
-            acc.z = fmaf(f, v[k].z, acc.z);
-            acc.w = fmaf(f, v[k].w, acc.w);
-          }
-          top = t;
-          topd = td;
+        for (int a = 0; a < kAtOnce; ++a) {
+          top[a] = topd[a] = -INFINITY;
+          sum[a] = 0.0f;
+          acc[a] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
-        if (to) {
-          // (The first part of the group is this thread's own to overwrite,
-          // but for its row's references: all threads of a row read those.)
-          __stcg(reinterpret_cast<float4*>(to + row * kD) + ch, acc);
-          __syncwarp(__activemask());
-          if (ch == 0) __stcg(reinterpret_cast<float4*>(to + kRows * kD) + row, make_float4(top, topd, sum, 0.0f));
-        } else {
-          const float f = sum > 0.0f ? ex2(top - topd) / sum : (sum == 0.0f ? 0.0f : sum);
-          const int64_t at = out_of(row);
-          reinterpret_cast<uint2*>(p.out + at * kD)[ch] =
-              make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-          if (p.lse && ch == 0) p.lse[at] = (topd + log2f(sum)) * kLn2;
+        for (int k0 = 0; k0 < n; k0 += kFan) {
+          float4 y[kAtOnce][kFan], v[kAtOnce][kFan];
+#pragma unroll
+          for (int k = 0; k < kFan; ++k)
+#pragma unroll
+            for (int a = 0; a < kAtOnce; ++a) {
+              const int b = first + (k0 + k) * step, row = r0 + a * kStride;
+              y[a][k] = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+              v[a][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (b < stop && row < rows) {
+                const float* from = part(b, b == c_first);
+                y[a][k] = __ldcg(reinterpret_cast<const float4*>(from + kRows * kD) + row);
+                v[a][k] = __ldcg(reinterpret_cast<const float4*>(from + row * kD) + ch);
+              }
+            }
+#pragma unroll
+          for (int a = 0; a < kAtOnce; ++a) {
+            float t = top[a], td = topd[a];
+#pragma unroll
+            for (int k = 0; k < kFan; ++k) {
+              t = fmaxf(t, y[a][k].x);
+              td = fmaxf(td, y[a][k].y);
+            }
+            const float rt = t == -INFINITY ? 0.0f : t, rd = td == -INFINITY ? 0.0f : td;
+            const float keep = ex2(top[a] - rt);
+            sum[a] *= ex2(topd[a] - rd);
+            acc[a] = make_float4(acc[a].x * keep, acc[a].y * keep, acc[a].z * keep, acc[a].w * keep);
+#pragma unroll
+            for (int k = 0; k < kFan; ++k) {
+              const float f = ex2(y[a][k].x - rt);
+              sum[a] = fmaf(ex2(y[a][k].y - rd), y[a][k].z, sum[a]);
+              acc[a].x = fmaf(f, v[a][k].x, acc[a].x);
+              acc[a].y = fmaf(f, v[a][k].y, acc[a].y);
+              acc[a].z = fmaf(f, v[a][k].z, acc[a].z);
+              acc[a].w = fmaf(f, v[a][k].w, acc[a].w);
+            }
+            top[a] = t;
+            topd[a] = td;
+          }
+        }
+        // (A group's sum goes where its first part lay: a thread overwrites what
+        // it alone has read, but for a row's references, which all threads of
+        // the row, in one warp, have read before.)
+        __syncwarp(__activemask());
+#pragma unroll
+        for (int a = 0; a < kAtOnce; ++a) {
+          const int row = r0 + a * kStride;
+          if (row >= rows) break;
+          if (to) {
+            __stcg(reinterpret_cast<float4*>(to + row * kD) + ch, acc[a]);
+            if (ch == 0)
+              __stcg(reinterpret_cast<float4*>(to + kRows * kD) + row, make_float4(top[a], topd[a], sum[a], 0.0f));
+          } else {
+            const float f = sum[a] > 0.0f ? ex2(top[a] - topd[a]) / sum[a] : (sum[a] == 0.0f ? 0.0f : sum[a]);
+            const int64_t at = out_of(row);
+            reinterpret_cast<uint2*>(p.out + at * kD)[ch] =
+                make_uint2(pack_bf16x2(acc[a].x * f, acc[a].y * f), pack_bf16x2(acc[a].z * f, acc[a].w * f));
+            if (p.lse && ch == 0) p.lse[at] = (topd[a] + log2f(sum[a])) * kLn2;
+          }
         }
       }
     };

@@ -144,6 +144,7 @@ int ep_expert_linear(const void* x, const uint8_t* x_scale, int64_t x_rows, int 
                      void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
   if (!linear_sizes_ok(num_experts, max_rows, in_features) || x_rows < 0) return EP_ERR_INVALID_ARG;
   if (flags & ~EP_LINEAR_GLU) return EP_ERR_INVALID_ARG;
+  if (x_scale && x_rows > INT32_MAX) return EP_ERR_INVALID_ARG;
   const int glu = flags & EP_LINEAR_GLU;
   if (out_features < 8 || out_features > (1 << 20) || out_features % (glu ? 16 : 8) != 0) return EP_ERR_INVALID_ARG;
   if (!row_offset && (rows_per_expert < 0 || rows_per_expert > INT32_MAX)) return EP_ERR_INVALID_ARG;

@@ -19,9 +19,10 @@
 // adds them in the order of the steps, so that the result does not depend on
 // which one that was.
 //
-// Two launches: expert_rows_kernel writes x in the tensor cores' shared-memory
-// layout (and splits BF16), expert_linear_kernel is its programmatic dependent
-// and starts reading weights meanwhile.
+// Two launches: expert_rows_kernel splits BF16 rows into the tensor cores'
+// shared-memory layout (of E4M3 rows it lays out the scales; their codes come
+// by tiled loads as they are), expert_linear_kernel is its programmatic
+// dependent and starts reading weights meanwhile.
 #include <algorithm>
 
 #include "common.cuh"
@@ -66,9 +67,14 @@ struct Params {
 
 __device__ __forceinline__ int round8(int v) { return (v + 7) & ~7; }
 
+// Expert e's first row of x.
+__device__ __forceinline__ int64_t first_row(const ExpertLinearParams& p, int e) {
+  return p.offset ? static_cast<int64_t>(__ldg(p.offset + e)) : e * p.region;
+}
+
 // The rows expert e can have: within its region, and x.
 __device__ __forceinline__ int rows_of(const ExpertLinearParams& p, int e, int32_t count, int64_t& first) {
-  first = p.offset ? static_cast<int64_t>(__ldg(p.offset + e)) : e * p.region;
+  first = first_row(p, e);
   if (count <= 0) return 0;
   int64_t n = count;
   int64_t room = p.x_rows - first;
@@ -81,191 +87,212 @@ __device__ __forceinline__ int rows_of(const ExpertLinearParams& p, int e, int32
   return static_cast<int>(n);
 }
 
-// ---- rows of x -------------------------------------------------------------------
-// The place of a group of eight rows: warp-wide search over the experts' counts.
-struct RowGroup {
-  int e, n;        // expert (-1: no such group) and its rows
-  int64_t first;   // its first row in x
-  int row0;        // the group's first row within the expert
-  int slot0;       // rows (rounded up to 8) of the experts before
-  int tile0;       // row tiles of the experts before
+// ---- tiles of rows -----------------------------------------------------------------
+// Of each expert e, E entries each: row tiles and rows (rounded up to 8) of the
+// experts before it (and of all, at E), and its rows. In shared memory.
+struct Tables {
+  int* tile0;  // [E + 1]
+  int* slot0;  // [E + 1]
+  int* rows;   // [E]
+  __device__ Tables(int* at, int E) : tile0(at), slot0(at + E + 1), rows(at + 2 * E + 2) {}
+};
+constexpr size_t table_bytes(int E) { return sizeof(int) * (3 * static_cast<size_t>(E) + 2); }
+
+struct Scan {
+  long long row_sum[kThreads / 32];
+  int slot_sum[kThreads / 32], tile_sum[kThreads / 32];
 };
 
-__device__ RowGroup find_group(const Params& q, int group) {
+// Counts -> tiles, by a whole block of kThreads; ends with a block barrier.
+__device__ void tile_experts(const Params& q, Scan& sc, const Tables& tb) {
   const ExpertLinearParams& p = q.p;
-  const int lane = threadIdx.x & 31;
-  const int per = (p.E + 31) / 32;
-  const int e0 = lane * per, e1 = min(p.E, e0 + per);
-  // This lane's experts: rows without the bound of max_rows.
-  int64_t rows = 0;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int per = (p.E + kThreads - 1) / kThreads;
+  const int e0 = min(p.E, tid * per), e1 = min(p.E, e0 + per);
+  int mine[EP_MAX_EXPERTS / kThreads];
   int64_t first;
-  for (int e = e0; e < e1; ++e) rows += rows_of(p, e, __ldg(p.count + e), first);
-  int64_t before = rows;
+  long long rows = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += v;
+  for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i) {
+    mine[i] = e0 + i < e1 ? rows_of(p, e0 + i, __ldg(p.count + e0 + i), first) : 0;
+    rows += mine[i];
   }
-  before -= rows;
+  auto scan = [&](auto v, auto* sums) {  // exclusive over the block
+    auto s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const auto u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane == 31) sums[w] = s;
+    __syncthreads();
+    auto before = s - v;
+    for (int i = 0; i < w; ++i) before += sums[i];
+    return before;
+  };
+  // Rows are counted in 64 bits up to max_rows; what is left of them fits 27.
+  long long used = scan(rows, sc.row_sum);
   int slots = 0, tiles = 0;
-  int64_t used = before;
-  for (int e = e0; e < e1; ++e) {
-    int n = rows_of(p, e, __ldg(p.count + e), first);
-    const int64_t left = p.max_rows - used;
-    used += n;
-    if (n > left) {
-      n = left > 0 ? static_cast<int>(left) : 0;
+#pragma unroll
+  for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i) {
+    const long long left = used < p.max_rows ? p.max_rows - used : 0;
+    used += mine[i];
+    if (mine[i] > left) {
+      mine[i] = static_cast<int>(left);
       flag(p.status, EP_ST_CAPACITY);
     }
-    slots += round8(n);
-    tiles += (n + q.tile_rows - 1) / q.tile_rows;
+    slots += round8(mine[i]);
+    tiles += (mine[i] + q.tile_rows - 1) / q.tile_rows;
   }
-  int slot0 = slots, tile0 = tiles;
+  int s0 = scan(slots, sc.slot_sum), t0 = scan(tiles, sc.tile_sum);
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(0xffffffffu, slot0, o), b = __shfl_up_sync(0xffffffffu, tile0, o);
-    if (lane >= o) {
-      slot0 += a;
-      tile0 += b;
+  for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i) {
+    if (e0 + i < e1) {
+      tb.rows[e0 + i] = mine[i];
+      tb.slot0[e0 + i] = s0;
+      tb.tile0[e0 + i] = t0;
     }
+    s0 += round8(mine[i]);
+    t0 += (mine[i] + q.tile_rows - 1) / q.tile_rows;
   }
-  slot0 -= slots;
-  tile0 -= tiles;
-  RowGroup g{-1, 0, 0, 0, 0, 0};
-  if (group * 8 >= slot0 && group * 8 < slot0 + slots) {
-    used = before;
-    for (int e = e0; e < e1; ++e) {
-      int n = rows_of(p, e, __ldg(p.count + e), first);
-      const int64_t left = p.max_rows - used;
-      used += n;
-      if (n > left) n = left > 0 ? static_cast<int>(left) : 0;
-      if (group * 8 < slot0 + round8(n)) {
-        g = RowGroup{e, n, first, group * 8 - slot0, slot0, tile0};
-        break;
-      }
-      slot0 += round8(n);
-      tile0 += (n + q.tile_rows - 1) / q.tile_rows;
-    }
+  if (tid == kThreads - 1) {
+    tb.tile0[p.E] = t0;
+    tb.slot0[p.E] = s0;
   }
-  const unsigned who = __ballot_sync(0xffffffffu, g.e >= 0);
-  const int src = who ? __ffs(who) - 1 : 0;
-  g.e = __shfl_sync(0xffffffffu, g.e, src);
-  g.n = __shfl_sync(0xffffffffu, g.n, src);
-  g.first = __shfl_sync(0xffffffffu, g.first, src);
-  g.row0 = __shfl_sync(0xffffffffu, g.row0, src);
-  g.slot0 = __shfl_sync(0xffffffffu, g.slot0, src);
-  g.tile0 = __shfl_sync(0xffffffffu, g.tile0, src);
-  return g;
+  __syncthreads();
 }
 
-// Bytes of the image in front of a tile, and the columns of the tile.
+// The last expert whose entry is <= v.
+__device__ __forceinline__ int expert_of(const int* table, int E, int v) {
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (table[mid] <= v) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// ---- rows of x -------------------------------------------------------------------
+// Columns of a tile, and the bytes of the image in front of it.
 __device__ __forceinline__ int tile_cols(const Params& q, int n, int tile) {
   return round8(min(q.tile_rows, n - tile * q.tile_rows)) * q.mult;
 }
 __device__ __forceinline__ int64_t image_at(const Params& q, int slot0, int tile0, int tile) {
-  return (static_cast<int64_t>(slot0) + static_cast<int64_t>(tile) * q.tile_rows) * q.mult * q.p.K +
-         static_cast<int64_t>(tile0 + tile) * q.KB * q.scale_bytes;
+  const int64_t scales = static_cast<int64_t>(tile0 + tile) * q.KB * q.scale_bytes;
+  if (q.mult == 1) return scales;  // the codes of E4M3 rows are not in it
+  return scales + (static_cast<int64_t>(slot0) + static_cast<int64_t>(tile) * q.tile_rows) * q.mult * q.p.K;
 }
 
 __device__ __forceinline__ unsigned scale_place(int col) {
   return static_cast<unsigned>((col >> 7) * kScaleBytes + (col & 31) * 16 + ((col >> 5) & 3) * 4);
 }
 
-constexpr int kRowThreads = 256;  // a warp for each of a group's eight rows
-constexpr int kRowSpan = 1024;    // inputs a block takes
+constexpr int kRowSpan = 1024;  // inputs of an item
 
-// Grid: (groups of eight rows, spans of inputs).
-__global__ void __launch_bounds__(kRowThreads) expert_rows_kernel(const Params q) {
+// Items: groups of eight rows, and spans of inputs of BF16 rows; a warp takes a
+// row. (One scan of the counts a block; with a scan and a search for each item
+// this kernel took 40 us of the 756 for 128 tokens x 256 experts.)
+__global__ void __launch_bounds__(kThreads) expert_rows_kernel(const Params q) {
+  extern __shared__ int tables[];
+  __shared__ Scan sc;
   const ExpertLinearParams& p = q.p;
+  const Tables tb(tables, p.E);
   grid_dependency_wait();
   launch_dependents();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const RowGroup g = find_group(q, blockIdx.x);
-  if (g.e < 0) return;
-  const int j = g.row0 + w;  // row within the expert
-  const int tile = g.row0 / q.tile_rows, r = j - tile * q.tile_rows;
-  const int cols = tile_cols(q, g.n, tile), rows8 = cols / q.mult;
-  uint8_t* image = q.image + image_at(q, g.slot0, g.tile0, tile);
-  // Of a stage's two steps (or the last one alone): their codes, then their scales.
-  auto stage = [&](int kb) {
-    return image + static_cast<int64_t>(kb / kStageSteps) * kStageSteps * (cols * kStep + q.scale_bytes);
-  };
-  auto scales = [&](int kb) {
-    return stage(kb) + ((kb | 1) < q.KB ? kStageSteps : 1) * cols * kStep + kb % kStageSteps * q.scale_bytes;
-  };
-  const bool live = j < g.n;
-  const int64_t row = g.first + j;
-  const int k1 = min(p.K, (static_cast<int>(blockIdx.y) + 1) * kRowSpan);
-  // Column c of step kb, 16-byte piece `piece`.
-  auto place = [&](int kb, int c, int piece) {
-    return stage(kb) + kb % kStageSteps * cols * kStep + (c >> 3) * 1024 + (c & 7) * 128 + ((piece ^ (c & 7)) << 4);
-  };
-  if (p.x_scale) {
-    // E4M3: a lane moves 16 inputs, a step's scale byte serves its four groups.
-    for (int k = blockIdx.y * kRowSpan + lane * 16; k < k1; k += 512) {
-      const int kb = k / kStep;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (live) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + row * p.K + k));
-      *reinterpret_cast<uint4*>(place(kb, r, (k % kStep) >> 4)) = v;
-      if (k % kStep == 0) {
+  tile_experts(q, sc, tb);
+  const int spans = q.mult == 2 ? (p.K + kRowSpan - 1) / kRowSpan : 1;
+  const int64_t items = static_cast<int64_t>(tb.slot0[p.E] / 8) * spans;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int group = static_cast<int>(item / spans), part = static_cast<int>(item % spans);
+    const int e = expert_of(tb.slot0, p.E, group * 8);
+    const int n = tb.rows[e], slot0 = tb.slot0[e], tile0 = tb.tile0[e];
+    const int row0 = group * 8 - slot0, j = row0 + w;  // row within the expert
+    const int tile = row0 / q.tile_rows, r = j - tile * q.tile_rows;
+    const int cols = tile_cols(q, n, tile), rows8 = cols / q.mult;
+    uint8_t* image = q.image + image_at(q, slot0, tile0, tile);
+    const bool live = j < n;
+    const int64_t row = first_row(p, e) + j;
+    if (q.mult == 1) {
+      // E4M3: a scale byte serves a step's four groups of 32.
+      for (int kb = lane; kb < q.KB; kb += 32) {
         const uint32_t s = live ? __ldg(p.x_scale + row * q.KB + kb) : 127u;
-        *reinterpret_cast<uint32_t*>(scales(kb) + scale_place(r)) = s * 0x01010101u;
+        *reinterpret_cast<uint32_t*>(image + static_cast<int64_t>(kb) * q.scale_bytes + scale_place(r)) = s * 0x01010101u;
       }
+      continue;
     }
-    return;
-  }
-  // BF16: a lane splits 8 inputs, four lanes share a scale. Both columns of a
-  // row: its high terms at r, its low terms at rows8 + r.
-  const int span = (k1 - static_cast<int>(blockIdx.y) * kRowSpan + 255) / 256;
-  for (int i = 0; i < span; ++i) {
-    const int k = blockIdx.y * kRowSpan + i * 256 + lane * 8;
-    const bool in = k < k1;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (live && in) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.K + k));
-    float x[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
-                  bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
-    float m = 0.0f;
-    bool finite[8];
+    // Of a stage's two steps (or the last one alone): their codes, then their scales.
+    auto stage = [&](int kb) {
+      return image + static_cast<int64_t>(kb / kStageSteps) * kStageSteps * (cols * kStep + q.scale_bytes);
+    };
+    auto scales = [&](int kb) {
+      return stage(kb) + ((kb | 1) < q.KB ? kStageSteps : 1) * cols * kStep + kb % kStageSteps * q.scale_bytes;
+    };
+    // Column c of step kb, 16-byte piece `piece`.
+    auto place = [&](int kb, int c, int piece) {
+      return stage(kb) + kb % kStageSteps * cols * kStep + (c >> 3) * 1024 + (c & 7) * 128 + ((piece ^ (c & 7)) << 4);
+    };
+    // A lane splits 8 inputs, four lanes share a scale. Both columns of a row:
+    // its high terms at r, its low terms at rows8 + r.
+    const int k1 = min(p.K, (part + 1) * kRowSpan);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.K);
+    uint4 raw[kRowSpan / 256];
 #pragma unroll
-    for (int a = 0; a < 8; ++a) {
-      finite[a] = fabsf(x[a]) <= 3.4028234663852886e38f;
-      if (finite[a]) m = fmaxf(m, fabsf(x[a]));
+    for (int i = 0; i < kRowSpan / 256; ++i) {
+      const int k = part * kRowSpan + i * 256 + lane * 8;
+      raw[i] = live && k < k1 ? __ldg(src + k / 8) : make_uint4(0, 0, 0, 0);
     }
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    // The exponent of the smallest power of two >= m / 448, kept so that the
-    // low terms' scale, 2^-4 of it, is a normal number.
-    const uint32_t up = (__float_as_uint(__fdiv_rn(m, 448.0f)) + 0x007FFFFFu) >> 23;
-    const uint32_t b = up < 5u ? 5u : up;
-    const float inv = __uint_as_float((254u - b) << 23);
-    uint32_t hi[2], lo[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      hi[h] = lo[h] = 0;
+    for (int i = 0; i < kRowSpan / 256; ++i) {
+      const int k = part * kRowSpan + i * 256 + lane * 8;
+      const uint4 v = raw[i];
+      float x[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
+                    bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
+      float m = 0.0f;
+      bool finite[8];
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const int at = 4 * h + 2 * a;
-        const float x0 = x[at] * inv, x1 = x[at + 1] * inv;
-        const uint32_t c = pack_e4m3x2(finite[at] ? x0 : __int_as_float(0x7FC00000), finite[at + 1] ? x1 : __int_as_float(0x7FC00000));
-        uint32_t f2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f2) : "h"(static_cast<uint16_t>(c)));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f2));
-        hi[h] |= c << (16 * a);
-        lo[h] |= pack_e4m3x2((x0 - f.x) * 16.0f, (x1 - f.y) * 16.0f) << (16 * a);
+      for (int a = 0; a < 8; ++a) {
+        finite[a] = fabsf(x[a]) <= 3.4028234663852886e38f;
+        if (finite[a]) m = fmaxf(m, fabsf(x[a]));
       }
-    }
-    // A step's four scale bytes, gathered into its first lane.
-    uint32_t s = b;
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      // The exponent of the smallest power of two >= m / 448, kept so that the
+      // low terms' scale, 2^-4 of it, is a normal number.
+      const uint32_t up = (__float_as_uint(__fdiv_rn(m, 448.0f)) + 0x007FFFFFu) >> 23;
+      const uint32_t b = up < 5u ? 5u : up;
+      const float inv = __uint_as_float((254u - b) << 23);
+      uint32_t hi[2], lo[2];
 #pragma unroll
-    for (int a = 1; a < 4; ++a) s |= __shfl_down_sync(0xffffffffu, b, 4 * a) << (8 * a);
-    if (!in) continue;
-    const int kb = k / kStep, piece = (k % kStep) >> 4, half = (k >> 3 & 1) * 8;
-    *reinterpret_cast<uint2*>(place(kb, r, piece) + half) = make_uint2(hi[0], hi[1]);
-    *reinterpret_cast<uint2*>(place(kb, rows8 + r, piece) + half) = make_uint2(lo[0], lo[1]);
-    if ((lane & 15) == 0) {
-      uint8_t* at = scales(kb);
-      *reinterpret_cast<uint32_t*>(at + scale_place(r)) = s;
-      *reinterpret_cast<uint32_t*>(at + scale_place(rows8 + r)) = s - 0x04040404u;
+      for (int h = 0; h < 2; ++h) {
+        hi[h] = lo[h] = 0;
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const int at = 4 * h + 2 * a;
+          const float nan = __int_as_float(0x7FC00000);
+          const float x0 = x[at] * inv, x1 = x[at + 1] * inv;
+          const uint32_t c = pack_e4m3x2(finite[at] ? x0 : nan, finite[at + 1] ? x1 : nan);
+          uint32_t f2;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f2) : "h"(static_cast<uint16_t>(c)));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f2));
+          hi[h] |= c << (16 * a);
+          lo[h] |= pack_e4m3x2((x0 - f.x) * 16.0f, (x1 - f.y) * 16.0f) << (16 * a);
+        }
+      }
+      // A step's four scale bytes, gathered into its first lane.
+      uint32_t s = b;
+#pragma unroll
+      for (int a = 1; a < 4; ++a) s |= __shfl_down_sync(0xffffffffu, b, 4 * a) << (8 * a);
+      if (k >= k1) continue;
+      const int kb = k / kStep, piece = (k % kStep) >> 4, half = (k >> 3 & 1) * 8;
+      *reinterpret_cast<uint2*>(place(kb, r, piece) + half) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(place(kb, rows8 + r, piece) + half) = make_uint2(lo[0], lo[1]);
+      if ((lane & 15) == 0) {
+        uint8_t* at = scales(kb);
+        *reinterpret_cast<uint32_t*>(at + scale_place(r)) = s;
+        *reinterpret_cast<uint32_t*>(at + scale_place(rows8 + r)) = s - 0x04040404u;
+      }
     }
   }
 }
@@ -277,12 +304,7 @@ struct Shared {
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem;
   int last;                       // this block is the last to finish its shared unit
-  long long row_sum[kThreads / 32];
-  int slot_sum[kThreads / 32], tile_sum[kThreads / 32];
-  int tiles;                      // row tiles of all experts
-  int tile0[EP_MAX_EXPERTS + 1];  // row tiles of the experts before
-  int slot0[EP_MAX_EXPERTS];      // rows, rounded up to 8, of the experts before
-  int rows[EP_MAX_EXPERTS];
+  Scan scan;
   float swap[2][8][64];           // GLU: ups on their way to the gates' threads
 };
 
@@ -323,84 +345,25 @@ __device__ __forceinline__ int owner_of(int64_t total, int blocks, int64_t i) {
 }
 
 // The next run of steps of one unit, by a whole warp.
-__device__ __forceinline__ bool next_segment(const Params& q, const Shared& sh, Run& run, Segment& s) {
+__device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, Run& run, Segment& s) {
   if (run.at >= run.end) return false;
   s.unit = run.at / q.KS;
   s.s0 = static_cast<int>(run.at - s.unit * q.KS);
   s.s1 = static_cast<int>(min(static_cast<int64_t>(q.KS), s.s0 + (run.end - run.at)));
   run.at += s.s1 - s.s0;
-  const int t = static_cast<int>(s.unit / q.MT);
-  int lo = 0, hi = q.p.E;  // the last expert with tile0 <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (sh.tile0[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  s.e = lo = uniform(lo);
-  s.slot0 = uniform(sh.slot0[lo]);
-  s.tile0 = uniform(sh.tile0[lo]);
-  const int tiles = uniform(sh.tile0[lo + 1]) - s.tile0;
+  const int lo = uniform(expert_of(tb.tile0, q.p.E, static_cast<int>(s.unit / q.MT)));
+  s.e = lo;
+  s.slot0 = uniform(tb.slot0[lo]);
+  s.tile0 = uniform(tb.tile0[lo]);
+  const int tiles = uniform(tb.tile0[lo + 1]) - s.tile0;
   // Tiles of one (expert, outputs) follow one another, so that its weights
   // come from L2 after the first.
   const int u = static_cast<int>(s.unit - static_cast<int64_t>(s.tile0) * q.MT);
   s.mt = u / tiles;
   s.tile = u - s.mt * tiles;
-  s.rows = min(q.tile_rows, uniform(sh.rows[lo]) - s.tile * q.tile_rows);
+  s.rows = min(q.tile_rows, uniform(tb.rows[lo]) - s.tile * q.tile_rows);
   s.cols = round8(s.rows) * q.mult;
   return true;
-}
-
-// Counts -> tiles, by the whole block.
-__device__ void tile_experts(const Params& q, Shared& sh) {
-  const ExpertLinearParams& p = q.p;
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int per = (p.E + kThreads - 1) / kThreads;
-  const int e0 = min(p.E, tid * per), e1 = min(p.E, e0 + per);
-  int mine[EP_MAX_EXPERTS / kThreads];
-  int64_t first;
-  long long rows = 0;
-#pragma unroll
-  for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i) {
-    mine[i] = e0 + i < e1 ? rows_of(p, e0 + i, __ldg(p.count + e0 + i), first) : 0;
-    rows += mine[i];
-  }
-  auto scan = [&](auto v, auto* sums) {  // exclusive over the block
-    auto s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const auto u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
-    }
-    if (lane == 31) sums[w] = s;
-    __syncthreads();
-    auto before = s - v;
-    for (int i = 0; i < w; ++i) before += sums[i];
-    return before;
-  };
-  // Rows are counted in 64 bits up to max_rows; what is left of them fits 27.
-  long long used = scan(rows, sh.row_sum);
-  int slots = 0, tiles = 0;
-#pragma unroll
-  for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i) {
-    const long long left = used < p.max_rows ? p.max_rows - used : 0;
-    used += mine[i];
-    if (mine[i] > left) mine[i] = static_cast<int>(left);
-    slots += round8(mine[i]);
-    tiles += (mine[i] + q.tile_rows - 1) / q.tile_rows;
-  }
-  int s0 = scan(slots, sh.slot_sum), t0 = scan(tiles, sh.tile_sum);
-#pragma unroll
-  for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i) {
-    if (e0 + i < e1) {
-      sh.rows[e0 + i] = mine[i];
-      sh.slot0[e0 + i] = s0;
-      sh.tile0[e0 + i] = t0;
-    }
-    s0 += round8(mine[i]);
-    t0 += (mine[i] + q.tile_rows - 1) / q.tile_rows;
-  }
-  if (tid == kThreads - 1) sh.tile0[p.E] = sh.tiles = t0;
-  __syncthreads();
 }
 
 // The epilogue's threads agree on whether they go on, since they meet at barriers.
@@ -418,14 +381,21 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
 }
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
+// Of E4M3 rows, `rows8` come as boxes of 128, 32 and 8.
+struct RowMaps {
+  CUtensorMap box128, box32, box8;
+};
+
 __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
-                                                                 const __grid_constant__ CUtensorMap map) {
+                                                                 const __grid_constant__ CUtensorMap map,
+                                                                 const __grid_constant__ RowMaps maps) {
   extern __shared__ uint8_t dynamic[];
   // The stages start on a 1024-byte boundary (the swizzle's period).
   uint8_t* smem = dynamic + (1024 - (smem_addr(dynamic) & 1023)) % 1024;
   __shared__ Shared sh;
   const ExpertLinearParams& p = q.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
+  const Tables tb(reinterpret_cast<int*>(smem + q.stages * q.stage_bytes + kScaleGroups * 4 * kScaleBytes), p.E);
   if (tid == 0) {
     for (int i = 0; i < q.stages; ++i) {
       mbar_init(&sh.full[i], 1);
@@ -444,12 +414,12 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
   if (warp == 3) tmem_alloc(&sh.tmem, kTmemCols);
   // The counts are older than the rows kernel, which released this one only
   // once everything before it had completed.
-  tile_experts(q, sh);  // (ends with a block barrier)
+  tile_experts(q, sh.scan, tb);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = uniform(sh.tmem);
-  const int64_t total = static_cast<int64_t>(uniform(sh.tiles)) * q.MT * q.KS;
+  const int64_t total = static_cast<int64_t>(uniform(tb.tile0[p.E])) * q.MT * q.KS;
   const int outs = p.glu ? p.M / 2 : p.M;
   // Every block that takes part has steps: the join counts on it.
   const int blocks = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(total / kMinStages, int64_t{1})));
@@ -473,11 +443,12 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     };
     // Bytes of rows in a stage: the last one of an odd number of steps holds one.
     auto x_bytes = [&](int st, unsigned step) { return st * kStageSteps + 1 < q.KB ? 2 * step : step; };
+    const bool fp8 = q.mult == 1;
     const Run start = run;
     Segment g;
     Ring r;
     int ahead = 0;
-    while (ahead < q.stages && next_segment(q, sh, run, g)) {
+    while (ahead < q.stages && next_segment(q, tb, run, g)) {
       const unsigned step = g.cols * kStep + q.scale_bytes;
       for (int st = g.s0; st < g.s1 && ahead < q.stages; ++st, ++ahead) {
         if (elect_one()) load_w(g, st, kStageSteps * kTileTx + x_bytes(st, step), r);
@@ -489,10 +460,12 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     r = Ring{};
     unsigned round = 0;  // passes over the ring
     bool ok = true;
-    while (ok && next_segment(q, sh, run, g)) {
-      const unsigned step = g.cols * kStep + q.scale_bytes;
+    while (ok && next_segment(q, tb, run, g)) {
+      const unsigned xcodes = g.cols * kStep, step = xcodes + q.scale_bytes;
+      const unsigned image_step = fp8 ? q.scale_bytes : step;
       const uint8_t* x =
-          q.image + image_at(q, g.slot0, g.tile0, g.tile) + static_cast<int64_t>(g.s0) * kStageSteps * step;
+          q.image + image_at(q, g.slot0, g.tile0, g.tile) + static_cast<int64_t>(g.s0) * kStageSteps * image_step;
+      const int row0 = static_cast<int>(first_row(p, g.e)) + g.tile * q.tile_rows;
       for (int st = g.s0; st < g.s1; ++st) {
         const bool loaded = ahead > 0;
         if (loaded) {
@@ -502,11 +475,25 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
           break;
         }
         if (elect_one()) {
-          const unsigned bytes = x_bytes(st, step);
-          if (!loaded) load_w(g, st, kStageSteps * kTileTx + bytes, r);
-          bulk_g2s(smem + r.offset + x_at, x, bytes, &sh.full[r.stage]);
+          uint64_t* bar = &sh.full[r.stage];
+          const unsigned steps = st * kStageSteps + 1 < q.KB ? kStageSteps : 1;
+          if (!loaded) load_w(g, st, kStageSteps * kTileTx + steps * step, r);
+          uint8_t* to = smem + r.offset + x_at;
+          if (!fp8) {
+            bulk_g2s(to, x, steps * step, bar);
+          } else {
+            bulk_g2s(to + steps * xcodes, x, steps * q.scale_bytes, bar);
+            for (unsigned h = 0; h < steps; ++h) {
+              const int k = (st * kStageSteps + h) * kStep;
+              int at = 0;
+              uint8_t* d = to + h * xcodes;
+              for (; at + 128 <= g.cols; at += 128) tma_load_2d(d + at * kStep, &maps.box128, k, row0 + at, bar);
+              for (; at + 32 <= g.cols; at += 32) tma_load_2d(d + at * kStep, &maps.box32, k, row0 + at, bar);
+              for (; at < g.cols; at += 8) tma_load_2d(d + at * kStep, &maps.box8, k, row0 + at, bar);
+            }
+          }
         }
-        x += kStageSteps * step;
+        x += kStageSteps * image_step;
         r.advance(q);
         if (r.stage == 0) round = 1;
       }
@@ -522,7 +509,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     const uint64_t ws0 = desc_rows16(base + ws_at), xs0 = desc_rows16(base + x_at);
     int group = 0;             // place in the ring of the weights' scales
     unsigned group_parity = 0;
-    while (ok && next_segment(q, sh, run, g)) {
+    while (ok && next_segment(q, tb, run, g)) {
       const int buf = seg & 1;
       if (seg >= 2 && !mbar_wait_warp(&sh.acc_empty[buf], (seg / 2 - 1) & 1, p.status)) break;
       tmem_fence_after();
@@ -586,7 +573,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     int lo[kAhead], hi[kAhead];
     Segment g;
     int next = 0;
-    bool more = next_segment(q, sh, run, g);
+    bool more = next_segment(q, tb, run, g);
     if (more) next = g.s0 * kStageSteps;
     // Steps [lo, hi) of one aligned group of four; lo == hi: none left.
     auto fetch = [&](uint32_t(&to)[4][4], int& from, int& upto) {
@@ -614,7 +601,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
       }
       next = group + 4;
       if (next >= end) {
-        more = next_segment(q, sh, run, g);
+        more = next_segment(q, tb, run, g);
         if (more) next = g.s0 * kStageSteps;
       }
     };
@@ -649,7 +636,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     grid_dependency_wait();
     Segment g;
     int seg = 0;
-    while (next_segment(q, sh, run, g)) {
+    while (next_segment(q, tb, run, g)) {
       const int buf = seg & 1;
       if (!epilogue_all(mbar_wait(&sh.acc_full[buf], (seg / 2) & 1, p.status))) break;
       ++seg;
@@ -657,8 +644,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
       const uint32_t acc = tmem + buf * kMaxCols + (static_cast<uint32_t>(warp & 3) << 21);
       const int rows8 = round8(g.rows);
       const bool whole = g.s0 == 0 && g.s1 == q.KS;
-      const int64_t base = p.offset ? static_cast<int64_t>(__ldg(p.offset + g.e)) : g.e * p.region;
-      const int64_t row0 = base + g.tile * q.tile_rows;
+      const int64_t row0 = first_row(p, g.e) + g.tile * q.tile_rows;
       const int o = p.glu ? g.mt * 64 + (m & 63) : g.mt * kTileM + m;
       auto slot = [&](int block, bool starts) {
         return q.partial + (static_cast<int64_t>(block) * 2 + (starts ? 1 : 0)) * q.tile_rows * kTileM;
@@ -778,7 +764,7 @@ Sizes sizes_of(int E, int64_t max_rows, int K, bool fp8) {
   z.counters = 0;
   z.partial = 1024;
   z.image = z.partial + up(sizeof(float) * kMaxBlocks * 2 * z.tile_rows * kTileM);
-  z.total = z.image + up(static_cast<size_t>(tiles) * (K / kStep) * sb + static_cast<size_t>(slots) * mult * K);
+  z.total = z.image + up(static_cast<size_t>(tiles) * (K / kStep) * sb + (fp8 ? 0 : static_cast<size_t>(slots) * mult * K));
   return z;
 }
 
@@ -804,9 +790,10 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   q.scale_bytes = q.cols_cap > 128 ? 2 * kScaleBytes : kScaleBytes;
   q.stage_bytes = (kStageSteps * (kTileBytes + q.cols_cap * kStep + q.scale_bytes) + 1023) / 1024 * 1024;
   constexpr unsigned kRing = kScaleGroups * 4 * kScaleBytes;
-  constexpr unsigned kSmem = 227 * 1024 - sizeof(Shared) - 2048 - kRing;
-  q.stages = std::min<int>(kMaxStages, kSmem / q.stage_bytes);
-  const size_t smem = static_cast<size_t>(q.stages) * q.stage_bytes + kRing + 1024;
+  const unsigned tables = static_cast<unsigned>(table_bytes(p.E));
+  const unsigned most = 227 * 1024 - sizeof(Shared) - 2048 - kRing - tables;
+  q.stages = std::min<int>(kMaxStages, most / q.stage_bytes);
+  const size_t smem = static_cast<size_t>(q.stages) * q.stage_bytes + kRing + tables + 1024;
 
   const EncodeTiled encode = encode_tiled();
   if (!encode) return cudaErrorNotSupported;
@@ -832,12 +819,29 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   if (err != cudaSuccess) return err;
   const int sms = device_sms(dev);
   if (sms < 1) return cudaErrorInvalidDevice;
+  RowMaps maps;
+  maps.box128 = maps.box32 = maps.box8 = map;
+  if (fp8) {
+    const cuuint64_t xd[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.x_rows)};
+    const cuuint64_t xs[1] = {static_cast<cuuint64_t>(p.K)};
+    CUtensorMap* const to[3] = {&maps.box128, &maps.box32, &maps.box8};
+    const cuuint32_t heights[3] = {128, 32, 8};
+    for (int i = 0; i < 3; ++i) {
+      const cuuint32_t b[2] = {kStep, heights[i]};
+      if (encode(to[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p.x), xd, xs, b, ones,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    }
+  }
+  // Items of the rows kernel: at most these.
   const int64_t groups = (p.max_rows + 7 * std::min<int64_t>(p.E, p.max_rows)) / 8;
-  err = launch_kernel(expert_rows_kernel, dim3(static_cast<unsigned>(groups), (p.K + kRowSpan - 1) / kRowSpan),
-                      dim3(kRowThreads), 0, s, /*dependent=*/true, q);
+  const int64_t items = groups * (fp8 ? 1 : (p.K + kRowSpan - 1) / kRowSpan);
+  err = launch_kernel(expert_rows_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(items, 2 * sms))),
+                      dim3(kThreads), tables, s, /*dependent=*/true, q);
   if (err != cudaSuccess) return err;
   return launch_kernel(expert_linear_kernel, dim3(std::min(sms, kMaxBlocks)), dim3(kThreads), smem, s,
-                       /*dependent=*/true, q, map);
+                       /*dependent=*/true, q, map, maps);
 }
 
 }  // namespace ep

@@ -19,6 +19,10 @@
 // adds them in the order of the steps, so that the result does not depend on
 // which one that was.
 //
+// With many rows the blocks' reads of x, not HBM, set the pace: each of an
+// expert's 32 or more output tiles needs all of its rows. Blocks then work in
+// clusters of neighbouring output tiles, each loads a share of the rows for all.
+//
 // Two launches: expert_rows_kernel splits BF16 rows into the tensor cores'
 // shared-memory layout (of E4M3 rows it lays out the scales; their codes come
 // by tiled loads as they are), expert_linear_kernel is its programmatic
@@ -37,7 +41,7 @@ constexpr int kStep = 128;                  // inputs a step
 constexpr int kTileM = 128;                 // outputs a unit (with GLU: 64 gates, 64 ups)
 constexpr int kTileBytes = kTileM * kStep;  // weights of a step in shared memory (8-bit containers)
 constexpr int kTileTx = kTileBytes / 2;     // ... and as TMA counts them
-constexpr int kStageSteps = 2;              // steps a stage holds
+constexpr int kMaxSteps = 2;                // most steps a stage holds
 constexpr int kScaleBytes = 512;            // scale bytes of 128 rows for one step
 constexpr int kMaxCols = 192;
 constexpr int kMaxBlocks = 160;             // blocks a workspace has room for
@@ -55,8 +59,10 @@ struct Params {
   int tile_rows;    // rows of a full tile
   int cols_cap;     // its columns
   int KB;           // steps of a unit: K / 128
-  int KS;           // stages of a unit: two steps each, the last one perhaps one
-  int MT;           // units of a tile: output tiles of an expert
+  int steps;        // steps of a stage, 1 or 2
+  int KS;           // stages of a unit; the last one may hold one step of two
+  int MT;           // units of a tile: an expert's output tiles, a cluster's blocks taking one each
+  int cluster;      // blocks of a cluster
   int stages;
   unsigned stage_bytes;
   int scale_bytes;     // of a step's rows: 512 for each 128 columns that a tile can have
@@ -222,16 +228,19 @@ __global__ void __launch_bounds__(kThreads) expert_rows_kernel(const Params q) {
       }
       continue;
     }
-    // Of a stage's two steps (or the last one alone): their codes, then their scales.
-    auto stage = [&](int kb) {
-      return image + static_cast<int64_t>(kb / kStageSteps) * kStageSteps * (cols * kStep + q.scale_bytes);
+    // Of a stage's steps (the last one may hold one of two): their codes, then their scales.
+    const int step = cols * kStep + q.scale_bytes;
+    auto codes = [&](int kb) {
+      const int h = kb % q.steps;
+      return image + static_cast<int64_t>(kb - h) * step + h * cols * kStep;
     };
     auto scales = [&](int kb) {
-      return stage(kb) + ((kb | 1) < q.KB ? kStageSteps : 1) * cols * kStep + kb % kStageSteps * q.scale_bytes;
+      const int h = kb % q.steps, n = min(q.steps, q.KB - (kb - h));
+      return image + static_cast<int64_t>(kb - h) * step + n * cols * kStep + h * q.scale_bytes;
     };
     // Column c of step kb, 16-byte piece `piece`.
     auto place = [&](int kb, int c, int piece) {
-      return stage(kb) + kb % kStageSteps * cols * kStep + (c >> 3) * 1024 + (c & 7) * 128 + ((piece ^ (c & 7)) << 4);
+      return codes(kb) + (c >> 3) * 1024 + (c & 7) * 128 + ((piece ^ (c & 7)) << 4);
     };
     // A lane splits 8 inputs, four lanes share a scale. Both columns of a row:
     // its high terms at r, its low terms at rows8 + r.
@@ -310,7 +319,7 @@ struct Shared {
 
 // A run of steps of one unit.
 struct Segment {
-  int e, tile, mt;
+  int e, tile, mt;  // mt: of this block
   int s0, s1;     // stages
   int cols;       // columns of its tile
   int rows;       // rows of its tile
@@ -345,7 +354,7 @@ __device__ __forceinline__ int owner_of(int64_t total, int blocks, int64_t i) {
 }
 
 // The next run of steps of one unit, by a whole warp.
-__device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, Run& run, Segment& s) {
+__device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, int rank, Run& run, Segment& s) {
   if (run.at >= run.end) return false;
   s.unit = run.at / q.KS;
   s.s0 = static_cast<int>(run.at - s.unit * q.KS);
@@ -359,8 +368,9 @@ __device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, 
   // Tiles of one (expert, outputs) follow one another, so that its weights
   // come from L2 after the first.
   const int u = static_cast<int>(s.unit - static_cast<int64_t>(s.tile0) * q.MT);
-  s.mt = u / tiles;
-  s.tile = u - s.mt * tiles;
+  const int mt = u / tiles;
+  s.tile = u - mt * tiles;
+  s.mt = mt * q.cluster + rank;
   s.rows = min(q.tile_rows, uniform(tb.rows[lo]) - s.tile * q.tile_rows);
   s.cols = round8(s.rows) * q.mult;
   return true;
@@ -399,7 +409,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
   if (tid == 0) {
     for (int i = 0; i < q.stages; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.empty[i], q.cluster);  // every block has used what its peers load for it
     }
     for (int i = 0; i < kScaleGroups; ++i) {
       mbar_init(&sh.scale_full[i], 1);
@@ -422,12 +432,17 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
   const int64_t total = static_cast<int64_t>(uniform(tb.tile0[p.E])) * q.MT * q.KS;
   const int outs = p.glu ? p.M / 2 : p.M;
   // Every block that takes part has steps: the join counts on it.
-  const int blocks = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(total / kMinStages, int64_t{1})));
+  const int rank = q.cluster > 1 ? static_cast<int>(uniform(cluster_rank())) : 0;
+  const int me = static_cast<int>(blockIdx.x) / q.cluster;  // the cluster's number
+  const int blocks =  // clusters
+      static_cast<int>(min(static_cast<int64_t>(gridDim.x / q.cluster), max(total / kMinStages, int64_t{1})));
+  const uint16_t all = static_cast<uint16_t>((1u << q.cluster) - 1u);
   Run run{0, 0};
-  if (blockIdx.x < blocks) run = Run{run_begin(total, blocks, blockIdx.x), run_begin(total, blocks, blockIdx.x + 1)};
+  if (me < blocks) run = Run{run_begin(total, blocks, me), run_begin(total, blocks, me + 1)};
+  if (q.cluster > 1) cluster_sync();  // barriers are set up before a peer's load arrives
   // A stage: weights, rows, the rows' scales. Behind the stages: the ring of
   // the weights' scales.
-  constexpr unsigned x_at = kStageSteps * kTileBytes;
+  const unsigned x_at = q.steps * kTileBytes;
   const unsigned ws_at = q.stages * q.stage_bytes;
   // First output row of half h (64 rows) of a unit's weights.
   auto out_row = [&](int mt, int h) { return p.glu ? mt * 64 + h * outs : mt * kTileM + h * 64; };
@@ -439,19 +454,18 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     auto load_w = [&](const Segment& g, int st, unsigned bytes, const Ring& r) {
       uint64_t* bar = &sh.full[r.stage];
       mbar_arrive_expect_tx(bar, bytes);
-      tma_load_5d(smem + r.offset, &map, 0, out_row(g.mt, 0), 0, st * kStageSteps, g.e, bar);
+      tma_load_5d(smem + r.offset, &map, 0, out_row(g.mt, 0), 0, st * q.steps, g.e, bar);
     };
-    // Bytes of rows in a stage: the last one of an odd number of steps holds one.
-    auto x_bytes = [&](int st, unsigned step) { return st * kStageSteps + 1 < q.KB ? 2 * step : step; };
+    auto steps_of = [&](int st) { return static_cast<unsigned>(min(q.steps, q.KB - st * q.steps)); };
     const bool fp8 = q.mult == 1;
     const Run start = run;
     Segment g;
     Ring r;
     int ahead = 0;
-    while (ahead < q.stages && next_segment(q, tb, run, g)) {
+    while (ahead < q.stages && next_segment(q, tb, rank, run, g)) {
       const unsigned step = g.cols * kStep + q.scale_bytes;
       for (int st = g.s0; st < g.s1 && ahead < q.stages; ++st, ++ahead) {
-        if (elect_one()) load_w(g, st, kStageSteps * kTileTx + x_bytes(st, step), r);
+        if (elect_one()) load_w(g, st, q.steps * kTileTx + steps_of(st) * step, r);
         r.advance(q);
       }
     }
@@ -459,43 +473,57 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     run = start;
     r = Ring{};
     unsigned round = 0;  // passes over the ring
+    unsigned empty = 0;  // asked a stage ahead
     bool ok = true;
-    while (ok && next_segment(q, tb, run, g)) {
+    while (ok && next_segment(q, tb, rank, run, g)) {
       const unsigned xcodes = g.cols * kStep, step = xcodes + q.scale_bytes;
       const unsigned image_step = fp8 ? q.scale_bytes : step;
       const uint8_t* x =
-          q.image + image_at(q, g.slot0, g.tile0, g.tile) + static_cast<int64_t>(g.s0) * kStageSteps * image_step;
+          q.image + image_at(q, g.slot0, g.tile0, g.tile) + static_cast<int64_t>(g.s0) * q.steps * image_step;
       const int row0 = static_cast<int>(first_row(p, g.e)) + g.tile * q.tile_rows;
       for (int st = g.s0; st < g.s1; ++st) {
         const bool loaded = ahead > 0;
         if (loaded) {
           --ahead;
-        } else if (round > 0 && !mbar_wait_warp(&sh.empty[r.stage], r.parity ^ 1, p.status)) {
+        } else if (round > 0 && !mbar_wait_asked(empty, &sh.empty[r.stage], r.parity ^ 1, p.status)) {
           ok = false;
           break;
         }
+        const Ring at_r = r;
+        r.advance(q);
+        if (r.stage == 0) round = 1;
+        empty = mbar_ask(&sh.empty[r.stage], r.parity ^ 1);
         if (elect_one()) {
-          uint64_t* bar = &sh.full[r.stage];
-          const unsigned steps = st * kStageSteps + 1 < q.KB ? kStageSteps : 1;
-          if (!loaded) load_w(g, st, kStageSteps * kTileTx + steps * step, r);
-          uint8_t* to = smem + r.offset + x_at;
+          uint64_t* bar = &sh.full[at_r.stage];
+          const unsigned steps = steps_of(st);
+          if (!loaded) load_w(g, st, q.steps * kTileTx + steps * step, at_r);
+          uint8_t* to = smem + at_r.offset + x_at;
           if (!fp8) {
-            bulk_g2s(to, x, steps * step, bar);
+            const unsigned bytes = steps * step;
+            if (q.cluster == 1) {
+              bulk_g2s(to, x, bytes, bar);
+            } else {
+              const unsigned share = (bytes / q.cluster + 127) & ~127u, from = min(bytes, rank * share);
+              const unsigned n = min(share, bytes - from);
+              if (n > 0) bulk_g2s_cluster(to + from, x + from, n, bar, all);
+            }
           } else {
             bulk_g2s(to + steps * xcodes, x, steps * q.scale_bytes, bar);
+            const int share = round8((g.cols + q.cluster - 1) / q.cluster), stop = min(g.cols, (rank + 1) * share);
             for (unsigned h = 0; h < steps; ++h) {
-              const int k = (st * kStageSteps + h) * kStep;
-              int at = 0;
+              const int k = (st * q.steps + h) * kStep;
               uint8_t* d = to + h * xcodes;
-              for (; at + 128 <= g.cols; at += 128) tma_load_2d(d + at * kStep, &maps.box128, k, row0 + at, bar);
-              for (; at + 32 <= g.cols; at += 32) tma_load_2d(d + at * kStep, &maps.box32, k, row0 + at, bar);
-              for (; at < g.cols; at += 8) tma_load_2d(d + at * kStep, &maps.box8, k, row0 + at, bar);
+              for (int at = rank * share; at < stop;) {
+                const int n = at + 128 <= stop ? 128 : at + 32 <= stop ? 32 : 8;
+                const CUtensorMap* box = n == 128 ? &maps.box128 : n == 32 ? &maps.box32 : &maps.box8;
+                if (q.cluster == 1) tma_load_2d(d + at * kStep, box, k, row0 + at, bar);
+                else tma_load_2d_cluster(d + at * kStep, box, k, row0 + at, bar, all);
+                at += n;
+              }
             }
           }
         }
-        x += kStageSteps * image_step;
-        r.advance(q);
-        if (r.stage == 0) round = 1;
+        x += q.steps * image_step;
       }
     }
   } else if (warp == 1) {
@@ -509,7 +537,10 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     const uint64_t ws0 = desc_rows16(base + ws_at), xs0 = desc_rows16(base + x_at);
     int group = 0;             // place in the ring of the weights' scales
     unsigned group_parity = 0;
-    while (ok && next_segment(q, tb, run, g)) {
+    // What the next stage needs is looked for before this one's products are
+    // issued, so that the look costs no time between them.
+    unsigned full = 0, scales = 0;
+    while (ok && next_segment(q, tb, rank, run, g)) {
       const int buf = seg & 1;
       if (seg >= 2 && !mbar_wait_warp(&sh.acc_empty[buf], (seg / 2 - 1) & 1, p.status)) break;
       tmem_fence_after();
@@ -518,26 +549,33 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
       const bool wide = g.cols > 128;
       const unsigned x_step = g.cols * kStep >> 4, xs_step = q.scale_bytes >> 4;
       for (int st = g.s0; st < g.s1; ++st) {
-        if ((st == g.s0 || (st & 1) == 0) && !mbar_wait_warp(&sh.scale_full[group], group_parity, p.status)) {
-          ok = false;
-          break;
-        }
-        if (!mbar_wait_warp(&sh.full[r.stage], r.parity, p.status)) {
+        const int kb = st * q.steps;
+        const bool group_start = st == g.s0 || (kb & 3) == 0;
+        if ((group_start && !mbar_wait_asked(scales, &sh.scale_full[group], group_parity, p.status)) ||
+            !mbar_wait_asked(full, &sh.full[r.stage], r.parity, p.status)) {
           ok = false;
           break;
         }
         tmem_fence_after();
-        const bool last = st + 1 == g.s1, group_end = (st & 1) == 1 || last;
+        const bool last = st + 1 == g.s1, group_end = (kb + q.steps & 3) == 0 || last;
         const unsigned at = r.offset >> 4;  // in the descriptors' units
-        const uint64_t ws = ws0 + (group * 4 + (st & 1) * 2) * (kScaleBytes / 16);
-        const uint32_t sc = tmem + kTmemScales + slot * 2 * kScaleCols;
-        const bool both = st * kStageSteps + 1 < q.KB;
+        const int stage = r.stage, this_group = group;
+        r.advance(q);
+        if (group_end && ++group == kScaleGroups) {
+          group = 0;
+          group_parity ^= 1;
+        }
+        full = mbar_ask(&sh.full[r.stage], r.parity);
+        scales = mbar_ask(&sh.scale_full[group], group_parity);
+        const uint64_t ws = ws0 + (this_group * 4 + (kb & 3)) * (kScaleBytes / 16);
+        const uint32_t sc = tmem + kTmemScales + slot * kMaxSteps * kScaleCols;
+        const int steps = min(q.steps, q.KB - kb);
         if (elect_one()) {
 #pragma unroll
-          for (int h = 0; h < kStageSteps; ++h) {
-            if (h > 0 && !both) break;
+          for (int h = 0; h < kMaxSteps; ++h) {
+            if (h == steps) break;
             const uint32_t c = sc + h * kScaleCols;
-            const uint64_t xs = xs0 + at + (both ? kStageSteps : 1) * x_step + h * xs_step;
+            const uint64_t xs = xs0 + at + steps * x_step + h * xs_step;
             tmem_copy_scales(c, ws + h * (kScaleBytes / 16));
             tmem_copy_scales(c + 4, xs);
             if (wide) tmem_copy_scales(c + 8, xs + kScaleBytes / 16);
@@ -546,17 +584,13 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
               mma_scaled(d, a0 + at + h * (kTileBytes / 16) + 2 * i, b0 + at + h * x_step + 2 * i,
                          idesc_scale_byte(idesc, i), c, c + 4, st > g.s0 || h > 0 || i > 0);
           }
-          mma_commit(&sh.empty[r.stage]);
-          if (group_end) mma_commit(&sh.scale_empty[group]);
+          if (q.cluster == 1) mma_commit(&sh.empty[stage]);
+          else mma_commit_cluster(&sh.empty[stage], all);
+          if (group_end) mma_commit(&sh.scale_empty[this_group]);
           if (last) mma_commit(&sh.acc_full[buf]);
         }
         __syncwarp();
         slot ^= 1;
-        if (group_end && ++group == kScaleGroups) {
-          group = 0;
-          group_parity ^= 1;
-        }
-        r.advance(q);
       }
       ++seg;
     }
@@ -573,15 +607,15 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     int lo[kAhead], hi[kAhead];
     Segment g;
     int next = 0;
-    bool more = next_segment(q, tb, run, g);
-    if (more) next = g.s0 * kStageSteps;
+    bool more = next_segment(q, tb, rank, run, g);
+    if (more) next = g.s0 * q.steps;
     // Steps [lo, hi) of one aligned group of four; lo == hi: none left.
     auto fetch = [&](uint32_t(&to)[4][4], int& from, int& upto) {
       from = upto = 0;
       if (!more) return;
       const int group = next & ~3;
       from = next - group;
-      const int end = min(q.KB, g.s1 * kStageSteps);
+      const int end = min(q.KB, g.s1 * q.steps);
       upto = min(4, end - group);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -601,8 +635,8 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
       }
       next = group + 4;
       if (next >= end) {
-        more = next_segment(q, tb, run, g);
-        if (more) next = g.s0 * kStageSteps;
+        more = next_segment(q, tb, rank, run, g);
+        if (more) next = g.s0 * q.steps;
       }
     };
 #pragma unroll
@@ -636,7 +670,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     grid_dependency_wait();
     Segment g;
     int seg = 0;
-    while (next_segment(q, tb, run, g)) {
+    while (next_segment(q, tb, rank, run, g)) {
       const int buf = seg & 1;
       if (!epilogue_all(mbar_wait(&sh.acc_full[buf], (seg / 2) & 1, p.status))) break;
       ++seg;
@@ -647,7 +681,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
       const int64_t row0 = first_row(p, g.e) + g.tile * q.tile_rows;
       const int o = p.glu ? g.mt * 64 + (m & 63) : g.mt * kTileM + m;
       auto slot = [&](int block, bool starts) {
-        return q.partial + (static_cast<int64_t>(block) * 2 + (starts ? 1 : 0)) * q.tile_rows * kTileM;
+        return q.partial + ((static_cast<int64_t>(block) * q.cluster + rank) * 2 + (starts ? 1 : 0)) * q.tile_rows * kTileM;
       };
       // Eight finished sums of this thread's output row: to y.
       auto finish = [&](float* v, int c0) {
@@ -668,7 +702,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
           if (c0 + i < g.rows)
             reinterpret_cast<__nv_bfloat16*>(p.y)[(row0 + c0 + i) * outs + o] = __float2bfloat16(v[i]);
       };
-      float* mine = slot(blockIdx.x, g.s0 == 0);
+      float* mine = slot(me, g.s0 == 0);
       for (int c0 = 0; c0 < rows8; c0 += 8) {
         float v[8];
         tmem_load8(v, acc + c0);
@@ -700,9 +734,9 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
       __threadfence();
       epilogue_sync();
       if (m == 0) {
-        const unsigned old = atomicAdd(&q.counters[c_first], 1u);
-        const bool last = old == static_cast<unsigned>(c_last - c_first);
-        if (last) q.counters[c_first] = 0u;
+        unsigned* counter = q.counters + c_first * q.cluster + rank;
+        const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(c_last - c_first);
+        if (last) *counter = 0u;
         sh.last = last;
       }
       epilogue_sync();
@@ -730,6 +764,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     tmem_fence_after();
     tmem_free(tmem, kTmemCols);
   }
+  if (q.cluster > 1) cluster_sync();  // no block leaves while a peer may still arrive on its barriers
 }
 
 // Rows of a full tile: enough for nearly every expert's rows in one tile (the
@@ -746,6 +781,9 @@ int tile_rows_for(int E, int64_t max_rows, int mult) {
     if (cap / mult >= mean + sd4) return cap / mult;
   return kMaxCols / mult;
 }
+
+// Blocks of a cluster.
+int cluster_for(int cols) { return cols >= 128 ? 2 : 1; }
 
 struct Sizes {
   int tile_rows;
@@ -782,13 +820,16 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   q.tile_rows = z.tile_rows;
   q.cols_cap = z.tile_rows * q.mult;
   q.KB = p.K / kStep;
-  q.KS = (q.KB + kStageSteps - 1) / kStageSteps;
+  q.steps = 2;
+  q.KS = (q.KB + q.steps - 1) / q.steps;
+  q.cluster = cluster_for(q.cols_cap);
   q.MT = p.glu ? (p.M / 2 + 63) / 64 : (p.M + kTileM - 1) / kTileM;
+  q.MT = (q.MT + q.cluster - 1) / q.cluster;
   q.counters = reinterpret_cast<unsigned*>(p.ws + z.counters);
   q.partial = reinterpret_cast<float*>(p.ws + z.partial);
   q.image = p.ws + z.image;
   q.scale_bytes = q.cols_cap > 128 ? 2 * kScaleBytes : kScaleBytes;
-  q.stage_bytes = (kStageSteps * (kTileBytes + q.cols_cap * kStep + q.scale_bytes) + 1023) / 1024 * 1024;
+  q.stage_bytes = (q.steps * (kTileBytes + q.cols_cap * kStep + q.scale_bytes) + 1023) / 1024 * 1024;
   constexpr unsigned kRing = kScaleGroups * 4 * kScaleBytes;
   const unsigned tables = static_cast<unsigned>(table_bytes(p.E));
   const unsigned most = 227 * 1024 - sizeof(Shared) - 2048 - kRing - tables;
@@ -806,7 +847,7 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
                               static_cast<cuuint64_t>(p.E)};
   const cuuint64_t strides[4] = {row, rows * row, kStep / 2, p.M * row};
   const cuuint32_t box[5] = {kStep, static_cast<cuuint32_t>(kTileM / parts), static_cast<cuuint32_t>(parts),
-                             kStageSteps, 1};
+                             static_cast<cuuint32_t>(q.steps), 1};
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 5, const_cast<uint8_t*>(p.w), dims, strides, box, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -840,8 +881,11 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   err = launch_kernel(expert_rows_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(items, 2 * sms))),
                       dim3(kThreads), tables, s, /*dependent=*/true, q);
   if (err != cudaSuccess) return err;
-  return launch_kernel(expert_linear_kernel, dim3(std::min(sms, kMaxBlocks)), dim3(kThreads), smem, s,
-                       /*dependent=*/true, q, map, maps);
+  // One block an SM; of clusters, as many as are resident at once.
+  int grid = std::min(sms, kMaxBlocks);
+  if (q.cluster > 1) grid = std::min(grid, clusters_resident(fn, dev, kThreads, smem, q.cluster, grid) * q.cluster);
+  if (grid < 1) return cudaErrorInvalidConfiguration;
+  return launch_kernel_cluster(expert_linear_kernel, dim3(grid), dim3(kThreads), smem, s, q.cluster, q, map, maps);
 }
 
 }  // namespace ep

@@ -173,6 +173,8 @@ int device_sms(int dev);
 bool device_cooperative(int dev);
 cudaError_t ensure_dynamic_smem(const void* fn, int dev, size_t smem);  // raise the kernel's limit to >= smem
 int blocks_per_sm(const void* fn, int dev, int threads, size_t smem);   // occupancy, 0 on failure
+// Clusters of `cluster` blocks that are resident at once, of a grid of at most `blocks`; 0 on failure.
+int clusters_resident(const void* fn, int dev, int threads, size_t smem, int cluster, int blocks);
 
 // The routing layout of ep_get_dispatch_layout: every check first (an error
 // code, with nothing enqueued), then, when reset_barrier is set, a zero fill

@@ -41,7 +41,9 @@ constexpr int kStep = 128;                  // inputs a step
 constexpr int kTileM = 128;                 // outputs a unit (with GLU: 64 gates, 64 ups)
 constexpr int kTileBytes = kTileM * kStep;  // weights of a step in shared memory (8-bit containers)
 constexpr int kTileTx = kTileBytes / 2;     // ... and as TMA counts them
-constexpr int kMaxSteps = 2;                // most steps a stage holds
+constexpr int kSteps = 2;                   // steps a stage holds
+constexpr int kCluster = 4;                 // blocks of a cluster, where there are clusters
+constexpr int kRowMaps = 8;                 // boxes of 8, 16 .. 64 rows
 constexpr int kScaleBytes = 512;            // scale bytes of 128 rows for one step
 constexpr int kMaxCols = 192;
 constexpr int kMaxBlocks = 160;             // blocks a workspace has room for
@@ -59,10 +61,8 @@ struct Params {
   int tile_rows;    // rows of a full tile
   int cols_cap;     // its columns
   int KB;           // steps of a unit: K / 128
-  int steps;        // steps of a stage, 1 or 2
-  int KS;           // stages of a unit; the last one may hold one step of two
+  int KS;           // stages of a unit: two steps each, the last one perhaps one
   int MT;           // units of a tile: an expert's output tiles, a cluster's blocks taking one each
-  int cluster;      // blocks of a cluster
   int stages;
   unsigned stage_bytes;
   int scale_bytes;     // of a step's rows: 512 for each 128 columns that a tile can have
@@ -231,11 +231,11 @@ __global__ void __launch_bounds__(kThreads) expert_rows_kernel(const Params q) {
     // Of a stage's steps (the last one may hold one of two): their codes, then their scales.
     const int step = cols * kStep + q.scale_bytes;
     auto codes = [&](int kb) {
-      const int h = kb % q.steps;
+      const int h = kb % kSteps;
       return image + static_cast<int64_t>(kb - h) * step + h * cols * kStep;
     };
     auto scales = [&](int kb) {
-      const int h = kb % q.steps, n = min(q.steps, q.KB - (kb - h));
+      const int h = kb % kSteps, n = min(kSteps, q.KB - (kb - h));
       return image + static_cast<int64_t>(kb - h) * step + n * cols * kStep + h * q.scale_bytes;
     };
     // Column c of step kb, 16-byte piece `piece`.
@@ -307,6 +307,19 @@ __global__ void __launch_bounds__(kThreads) expert_rows_kernel(const Params q) {
 }
 
 // ---- the products ------------------------------------------------------------------
+// E4M3 rows come straight from x, each block of the cluster loading a box of
+// this many, so a stage holds up to 8 kC - 8 columns more than the tile's.
+template <int kC>
+__device__ __forceinline__ int row_share(int cols) {
+  return round8((cols + kC - 1) / kC);
+}
+template <bool kFp8, int kC>
+__device__ __forceinline__ unsigned loaded_cols(int cols) {
+  if (!kFp8) return cols;
+  const int share = row_share<kC>(cols);
+  return (cols + share - 1) / share * share;
+}
+
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t scale_full[kScaleGroups], scale_empty[kScaleGroups];
@@ -354,7 +367,7 @@ __device__ __forceinline__ int owner_of(int64_t total, int blocks, int64_t i) {
 }
 
 // The next run of steps of one unit, by a whole warp.
-__device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, int rank, Run& run, Segment& s) {
+__device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, int cluster, int rank, Run& run, Segment& s) {
   if (run.at >= run.end) return false;
   s.unit = run.at / q.KS;
   s.s0 = static_cast<int>(run.at - s.unit * q.KS);
@@ -370,7 +383,7 @@ __device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, 
   const int u = static_cast<int>(s.unit - static_cast<int64_t>(s.tile0) * q.MT);
   const int mt = u / tiles;
   s.tile = u - mt * tiles;
-  s.mt = mt * q.cluster + rank;
+  s.mt = mt * cluster + rank;
   s.rows = min(q.tile_rows, uniform(tb.rows[lo]) - s.tile * q.tile_rows);
   s.cols = round8(s.rows) * q.mult;
   return true;
@@ -391,14 +404,17 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
 }
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// Of E4M3 rows, `rows8` come as boxes of 128, 32 and 8.
+// E4M3 rows: maps for boxes of 8, 16, .. rows.
 struct RowMaps {
-  CUtensorMap box128, box32, box8;
+  CUtensorMap box[kRowMaps];
 };
 
-__global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
-                                                                 const __grid_constant__ CUtensorMap map,
-                                                                 const __grid_constant__ RowMaps maps) {
+// kFp8: x in E4M3. kC: blocks of a cluster; more than one where tiles have 128
+// columns or more.
+template <bool kFp8, int kC>
+__global__ void __launch_bounds__(kThreads)
+    expert_linear_kernel(const Params q, const __grid_constant__ CUtensorMap map,
+                         const __grid_constant__ RowMaps maps) {
   extern __shared__ uint8_t dynamic[];
   // The stages start on a 1024-byte boundary (the swizzle's period).
   uint8_t* smem = dynamic + (1024 - (smem_addr(dynamic) & 1023)) % 1024;
@@ -409,7 +425,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
   if (tid == 0) {
     for (int i = 0; i < q.stages; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], q.cluster);  // every block has used what its peers load for it
+      mbar_init(&sh.empty[i], kC);  // every block has used what its peers load for it
     }
     for (int i = 0; i < kScaleGroups; ++i) {
       mbar_init(&sh.scale_full[i], 1);
@@ -432,17 +448,17 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
   const int64_t total = static_cast<int64_t>(uniform(tb.tile0[p.E])) * q.MT * q.KS;
   const int outs = p.glu ? p.M / 2 : p.M;
   // Every block that takes part has steps: the join counts on it.
-  const int rank = q.cluster > 1 ? static_cast<int>(uniform(cluster_rank())) : 0;
-  const int me = static_cast<int>(blockIdx.x) / q.cluster;  // the cluster's number
+  const int rank = kC > 1 ? static_cast<int>(uniform(cluster_rank())) : 0;
+  const int me = static_cast<int>(blockIdx.x) / kC;  // the cluster's number
   const int blocks =  // clusters
-      static_cast<int>(min(static_cast<int64_t>(gridDim.x / q.cluster), max(total / kMinStages, int64_t{1})));
-  const uint16_t all = static_cast<uint16_t>((1u << q.cluster) - 1u);
+      static_cast<int>(min(static_cast<int64_t>(gridDim.x / kC), max(total / kMinStages, int64_t{1})));
+  constexpr uint16_t kAll = static_cast<uint16_t>((1u << kC) - 1u);
   Run run{0, 0};
   if (me < blocks) run = Run{run_begin(total, blocks, me), run_begin(total, blocks, me + 1)};
-  if (q.cluster > 1) cluster_sync();  // barriers are set up before a peer's load arrives
+  if (kC > 1) cluster_sync();  // barriers are set up before a peer's load arrives
   // A stage: weights, rows, the rows' scales. Behind the stages: the ring of
   // the weights' scales.
-  const unsigned x_at = q.steps * kTileBytes;
+  constexpr unsigned x_at = kSteps * kTileBytes;
   const unsigned ws_at = q.stages * q.stage_bytes;
   // First output row of half h (64 rows) of a unit's weights.
   auto out_row = [&](int mt, int h) { return p.glu ? mt * 64 + h * outs : mt * kTileM + h * 64; };
@@ -454,18 +470,18 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     auto load_w = [&](const Segment& g, int st, unsigned bytes, const Ring& r) {
       uint64_t* bar = &sh.full[r.stage];
       mbar_arrive_expect_tx(bar, bytes);
-      tma_load_5d(smem + r.offset, &map, 0, out_row(g.mt, 0), 0, st * q.steps, g.e, bar);
+      tma_load_5d(smem + r.offset, &map, 0, out_row(g.mt, 0), 0, st * kSteps, g.e, bar);
     };
-    auto steps_of = [&](int st) { return static_cast<unsigned>(min(q.steps, q.KB - st * q.steps)); };
-    const bool fp8 = q.mult == 1;
+    auto steps_of = [&](int st) { return static_cast<unsigned>(min(kSteps, q.KB - st * kSteps)); };
+    // Bytes of a step's rows, and of what this cluster's blocks load of them.
+    auto step_bytes = [&](const Segment& g) { return loaded_cols<kFp8, kC>(g.cols) * kStep + q.scale_bytes; };
     const Run start = run;
     Segment g;
     Ring r;
     int ahead = 0;
-    while (ahead < q.stages && next_segment(q, tb, rank, run, g)) {
-      const unsigned step = g.cols * kStep + q.scale_bytes;
+    while (ahead < q.stages && next_segment(q, tb, kC, rank, run, g)) {
       for (int st = g.s0; st < g.s1 && ahead < q.stages; ++st, ++ahead) {
-        if (elect_one()) load_w(g, st, q.steps * kTileTx + steps_of(st) * step, r);
+        if (elect_one()) load_w(g, st, kSteps * kTileTx + steps_of(st) * step_bytes(g), r);
         r.advance(q);
       }
     }
@@ -475,12 +491,17 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     unsigned round = 0;  // passes over the ring
     unsigned empty = 0;  // asked a stage ahead
     bool ok = true;
-    while (ok && next_segment(q, tb, rank, run, g)) {
-      const unsigned xcodes = g.cols * kStep, step = xcodes + q.scale_bytes;
-      const unsigned image_step = fp8 ? q.scale_bytes : step;
+    while (ok && next_segment(q, tb, kC, rank, run, g)) {
+      const unsigned step = step_bytes(g), xcodes = step - q.scale_bytes;
+      const unsigned image_step = kFp8 ? q.scale_bytes : step;
       const uint8_t* x =
-          q.image + image_at(q, g.slot0, g.tile0, g.tile) + static_cast<int64_t>(g.s0) * q.steps * image_step;
-      const int row0 = static_cast<int>(first_row(p, g.e)) + g.tile * q.tile_rows;
+          q.image + image_at(q, g.slot0, g.tile0, g.tile) + static_cast<int64_t>(g.s0) * kSteps * image_step;
+      // E4M3: this block's share of the rows, one box a step.
+      const int share = row_share<kC>(g.cols);
+      const int row = static_cast<int>(uniform(first_row(p, g.e))) + g.tile * q.tile_rows + rank * share;
+      const bool mine = rank * share < g.cols;
+      const CUtensorMap* box = &maps.box[share / 8 - 1];
+      const unsigned share_at = x_at + rank * share * kStep;
       for (int st = g.s0; st < g.s1; ++st) {
         const bool loaded = ahead > 0;
         if (loaded) {
@@ -489,41 +510,36 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
           ok = false;
           break;
         }
-        const Ring at_r = r;
+        const Ring at = r;
         r.advance(q);
         if (r.stage == 0) round = 1;
         empty = mbar_ask(&sh.empty[r.stage], r.parity ^ 1);
+        const unsigned steps = steps_of(st);
         if (elect_one()) {
-          uint64_t* bar = &sh.full[at_r.stage];
-          const unsigned steps = steps_of(st);
-          if (!loaded) load_w(g, st, q.steps * kTileTx + steps * step, at_r);
-          uint8_t* to = smem + at_r.offset + x_at;
-          if (!fp8) {
-            const unsigned bytes = steps * step;
-            if (q.cluster == 1) {
-              bulk_g2s(to, x, bytes, bar);
-            } else {
-              const unsigned share = (bytes / q.cluster + 127) & ~127u, from = min(bytes, rank * share);
-              const unsigned n = min(share, bytes - from);
-              if (n > 0) bulk_g2s_cluster(to + from, x + from, n, bar, all);
-            }
-          } else {
-            bulk_g2s(to + steps * xcodes, x, steps * q.scale_bytes, bar);
-            const int share = round8((g.cols + q.cluster - 1) / q.cluster), stop = min(g.cols, (rank + 1) * share);
-            for (unsigned h = 0; h < steps; ++h) {
-              const int k = (st * q.steps + h) * kStep;
-              uint8_t* d = to + h * xcodes;
-              for (int at = rank * share; at < stop;) {
-                const int n = at + 128 <= stop ? 128 : at + 32 <= stop ? 32 : 8;
-                const CUtensorMap* box = n == 128 ? &maps.box128 : n == 32 ? &maps.box32 : &maps.box8;
-                if (q.cluster == 1) tma_load_2d(d + at * kStep, box, k, row0 + at, bar);
-                else tma_load_2d_cluster(d + at * kStep, box, k, row0 + at, bar, all);
-                at += n;
+          uint64_t* bar = &sh.full[at.stage];
+          if (!loaded) load_w(g, st, kSteps * kTileTx + steps * step, at);
+          uint8_t* to = smem + at.offset;
+          if (kFp8) {
+            bulk_g2s(to + x_at + steps * xcodes, x, steps * q.scale_bytes, bar);
+            if (mine) {
+#pragma unroll
+              for (int h = 0; h < kSteps; ++h) {
+                if (h == steps) break;
+                const int k = (st * kSteps + h) * kStep;
+                if (kC == 1) tma_load_2d(to + share_at + h * xcodes, box, k, row, bar);
+                else tma_load_2d_cluster(to + share_at + h * xcodes, box, k, row, bar, kAll);
               }
             }
+          } else if (kC == 1) {
+            bulk_g2s(to + x_at, x, steps * step, bar);
+          } else {
+            const unsigned bytes = steps * step, part = (bytes / kC + 127) & ~127u, from = min(bytes, rank * part);
+            const unsigned n = min(part, bytes - from);
+            if (n > 0) bulk_g2s_cluster(to + x_at + from, x + from, n, bar, kAll);
           }
         }
-        x += q.steps * image_step;
+        __syncwarp();
+        x += kSteps * image_step;
       }
     }
   } else if (warp == 1) {
@@ -540,16 +556,16 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     // What the next stage needs is looked for before this one's products are
     // issued, so that the look costs no time between them.
     unsigned full = 0, scales = 0;
-    while (ok && next_segment(q, tb, rank, run, g)) {
+    while (ok && next_segment(q, tb, kC, rank, run, g)) {
       const int buf = seg & 1;
       if (seg >= 2 && !mbar_wait_warp(&sh.acc_empty[buf], (seg / 2 - 1) & 1, p.status)) break;
       tmem_fence_after();
       const uint32_t d = tmem + buf * kMaxCols;
       const uint32_t idesc = idesc_e2m1_e4m3(g.cols);
-      const bool wide = g.cols > 128;
-      const unsigned x_step = g.cols * kStep >> 4, xs_step = q.scale_bytes >> 4;
+      const bool wide = kC > 1 && g.cols > 128;
+      const unsigned x_step = loaded_cols<kFp8, kC>(g.cols) * kStep >> 4, xs_step = q.scale_bytes >> 4;
       for (int st = g.s0; st < g.s1; ++st) {
-        const int kb = st * q.steps;
+        const int kb = st * kSteps;
         const bool group_start = st == g.s0 || (kb & 3) == 0;
         if ((group_start && !mbar_wait_asked(scales, &sh.scale_full[group], group_parity, p.status)) ||
             !mbar_wait_asked(full, &sh.full[r.stage], r.parity, p.status)) {
@@ -557,7 +573,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
           break;
         }
         tmem_fence_after();
-        const bool last = st + 1 == g.s1, group_end = (kb + q.steps & 3) == 0 || last;
+        const bool last = st + 1 == g.s1, group_end = (kb + kSteps & 3) == 0 || last;
         const unsigned at = r.offset >> 4;  // in the descriptors' units
         const int stage = r.stage, this_group = group;
         r.advance(q);
@@ -568,24 +584,26 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
         full = mbar_ask(&sh.full[r.stage], r.parity);
         scales = mbar_ask(&sh.scale_full[group], group_parity);
         const uint64_t ws = ws0 + (this_group * 4 + (kb & 3)) * (kScaleBytes / 16);
-        const uint32_t sc = tmem + kTmemScales + slot * kMaxSteps * kScaleCols;
-        const int steps = min(q.steps, q.KB - kb);
+        const uint32_t sc = tmem + kTmemScales + slot * kSteps * kScaleCols;
+        const bool both = kb + 1 < q.KB;
+        const uint64_t xs = xs0 + at + (both ? 2 : 1) * x_step;
+        // 32 inputs a product: 32 bytes on.
+        auto step = [&](int h, bool accumulate) {
+          const uint32_t c = sc + h * kScaleCols;
+          tmem_copy_scales(c, ws + h * (kScaleBytes / 16));
+          tmem_copy_scales(c + 4, xs + h * xs_step);
+          if (wide) tmem_copy_scales(c + 8, xs + h * xs_step + kScaleBytes / 16);
+          const uint64_t a = a0 + at + h * (kTileBytes / 16), b = b0 + at + h * x_step;
+          mma_scaled(d, a, b, idesc, c, c + 4, accumulate);
+#pragma unroll
+          for (int i = 1; i < 4; ++i)
+            mma_scaled(d, a + 2 * i, b + 2 * i, idesc_scale_byte(idesc, i), c, c + 4, true);
+        };
         if (elect_one()) {
-#pragma unroll
-          for (int h = 0; h < kMaxSteps; ++h) {
-            if (h == steps) break;
-            const uint32_t c = sc + h * kScaleCols;
-            const uint64_t xs = xs0 + at + steps * x_step + h * xs_step;
-            tmem_copy_scales(c, ws + h * (kScaleBytes / 16));
-            tmem_copy_scales(c + 4, xs);
-            if (wide) tmem_copy_scales(c + 8, xs + kScaleBytes / 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)  // 32 inputs: 32 bytes on
-              mma_scaled(d, a0 + at + h * (kTileBytes / 16) + 2 * i, b0 + at + h * x_step + 2 * i,
-                         idesc_scale_byte(idesc, i), c, c + 4, st > g.s0 || h > 0 || i > 0);
-          }
-          if (q.cluster == 1) mma_commit(&sh.empty[stage]);
-          else mma_commit_cluster(&sh.empty[stage], all);
+          step(0, st > g.s0);
+          if (both) step(1, true);
+          if (kC == 1) mma_commit(&sh.empty[stage]);
+          else mma_commit_cluster(&sh.empty[stage], kAll);
           if (group_end) mma_commit(&sh.scale_empty[this_group]);
           if (last) mma_commit(&sh.acc_full[buf]);
         }
@@ -594,28 +612,37 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
       }
       ++seg;
     }
-  } else if (warp == 2) {
+  } else if (warp < 4) {
     // The weights' scales: four bytes a row and step, laid out for the copy to
     // tensor memory (row r: place r % 32, word r / 32). A lane reads 16 bytes
     // of a row, four steps, at once, and keeps kAhead such groups in flight,
     // across units: with four steps ahead the loads' latency alone set the
-    // pace (experts_up 1513 us).
-    constexpr int kAhead = 5;
+    // pace (128 tokens x 256 experts: 1513 us). Two warps take turns: one spent
+    // 870 cycles a stage on it, as long as the products take.
+    constexpr int kAhead = 3;
     const int64_t pitch = p.K / 32;
     const bool vec = q.KB % 4 == 0;
     uint32_t v[kAhead][4][4];  // [group][row][step]
     int lo[kAhead], hi[kAhead];
     Segment g;
     int next = 0;
-    bool more = next_segment(q, tb, rank, run, g);
-    if (more) next = g.s0 * q.steps;
+    bool more = next_segment(q, tb, kC, rank, run, g);
+    if (more) next = g.s0 * kSteps;
+    auto advance = [&]() {  // to the next group
+      if (!more) return;
+      next = (next & ~3) + 4;
+      if (next >= min(q.KB, g.s1 * kSteps)) {
+        more = next_segment(q, tb, kC, rank, run, g);
+        if (more) next = g.s0 * kSteps;
+      }
+    };
     // Steps [lo, hi) of one aligned group of four; lo == hi: none left.
     auto fetch = [&](uint32_t(&to)[4][4], int& from, int& upto) {
       from = upto = 0;
       if (!more) return;
       const int group = next & ~3;
       from = next - group;
-      const int end = min(q.KB, g.s1 * q.steps);
+      const int end = min(q.KB, g.s1 * kSteps);
       upto = min(4, end - group);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -633,15 +660,13 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
             to[i][j] = j >= from && j < upto ? __ldg(reinterpret_cast<const uint32_t*>(src) + j) : 0;
         }
       }
-      next = group + 4;
-      if (next >= end) {
-        more = next_segment(q, tb, rank, run, g);
-        if (more) next = g.s0 * q.steps;
-      }
+      advance();
+      advance();  // the other warp's
     };
+    if (warp == 3) advance();
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch(v[i], lo[i], hi[i]);
-    int at = 0;
+    int at = warp - 2;
     unsigned parity = 0, round = 0;
     bool ok = true;
     while (ok && hi[0] > lo[0]) {
@@ -656,8 +681,9 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.scale_full[at]);
-        if (++at == kScaleGroups) {
-          at = 0;
+        at += 2;
+        if (at >= kScaleGroups) {
+          at -= kScaleGroups;
           parity ^= 1;
           round = 1;
         }
@@ -670,7 +696,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     grid_dependency_wait();
     Segment g;
     int seg = 0;
-    while (next_segment(q, tb, rank, run, g)) {
+    while (next_segment(q, tb, kC, rank, run, g)) {
       const int buf = seg & 1;
       if (!epilogue_all(mbar_wait(&sh.acc_full[buf], (seg / 2) & 1, p.status))) break;
       ++seg;
@@ -681,7 +707,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
       const int64_t row0 = first_row(p, g.e) + g.tile * q.tile_rows;
       const int o = p.glu ? g.mt * 64 + (m & 63) : g.mt * kTileM + m;
       auto slot = [&](int block, bool starts) {
-        return q.partial + ((static_cast<int64_t>(block) * q.cluster + rank) * 2 + (starts ? 1 : 0)) * q.tile_rows * kTileM;
+        return q.partial + ((static_cast<int64_t>(block) * kC + rank) * 2 + (starts ? 1 : 0)) * q.tile_rows * kTileM;
       };
       // Eight finished sums of this thread's output row: to y.
       auto finish = [&](float* v, int c0) {
@@ -734,7 +760,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
       __threadfence();
       epilogue_sync();
       if (m == 0) {
-        unsigned* counter = q.counters + c_first * q.cluster + rank;
+        unsigned* counter = q.counters + c_first * kC + rank;
         const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(c_last - c_first);
         if (last) *counter = 0u;
         sh.last = last;
@@ -764,7 +790,7 @@ __global__ void __launch_bounds__(kThreads) expert_linear_kernel(const Params q,
     tmem_fence_after();
     tmem_free(tmem, kTmemCols);
   }
-  if (q.cluster > 1) cluster_sync();  // no block leaves while a peer may still arrive on its barriers
+  if (kC > 1) cluster_sync();  // no block leaves while a peer may still arrive on its barriers
 }
 
 // Rows of a full tile: enough for nearly every expert's rows in one tile (the
@@ -783,7 +809,7 @@ int tile_rows_for(int E, int64_t max_rows, int mult) {
 }
 
 // Blocks of a cluster.
-int cluster_for(int cols) { return cols >= 128 ? 2 : 1; }
+int cluster_for(int cols) { return cols >= 128 ? kCluster : 1; }
 
 struct Sizes {
   int tile_rows;
@@ -808,6 +834,24 @@ Sizes sizes_of(int E, int64_t max_rows, int K, bool fp8) {
 
 }  // namespace
 
+namespace {
+
+template <bool kFp8, int kC>
+cudaError_t launch_products(const Params& q, const CUtensorMap& map, const RowMaps& maps, size_t smem, int dev, int sms,
+                            cudaStream_t s) {
+  const auto kernel = expert_linear_kernel<kFp8, kC>;
+  const void* fn = reinterpret_cast<const void*>(kernel);
+  const cudaError_t err = ensure_dynamic_smem(fn, dev, smem);
+  if (err != cudaSuccess) return err;
+  // One block an SM; of clusters, as many as are resident at once.
+  int grid = std::min(sms, kMaxBlocks);
+  if (kC > 1) grid = std::min(grid / kC, clusters_resident(fn, dev, kThreads, smem, kC, grid)) * kC;
+  if (grid < 1) return cudaErrorInvalidConfiguration;
+  return launch_kernel_cluster(kernel, dim3(grid), dim3(kThreads), smem, s, kC, q, map, maps);
+}
+
+}  // namespace
+
 size_t expert_linear_ws_bytes(int E, int64_t max_rows, int K, bool fp8) { return sizes_of(E, max_rows, K, fp8).total; }
 
 cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
@@ -820,16 +864,15 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   q.tile_rows = z.tile_rows;
   q.cols_cap = z.tile_rows * q.mult;
   q.KB = p.K / kStep;
-  q.steps = 2;
-  q.KS = (q.KB + q.steps - 1) / q.steps;
-  q.cluster = cluster_for(q.cols_cap);
+  q.KS = (q.KB + kSteps - 1) / kSteps;
+  const int cluster = cluster_for(q.cols_cap);
   q.MT = p.glu ? (p.M / 2 + 63) / 64 : (p.M + kTileM - 1) / kTileM;
-  q.MT = (q.MT + q.cluster - 1) / q.cluster;
+  q.MT = (q.MT + cluster - 1) / cluster;
   q.counters = reinterpret_cast<unsigned*>(p.ws + z.counters);
   q.partial = reinterpret_cast<float*>(p.ws + z.partial);
   q.image = p.ws + z.image;
   q.scale_bytes = q.cols_cap > 128 ? 2 * kScaleBytes : kScaleBytes;
-  q.stage_bytes = (q.steps * (kTileBytes + q.cols_cap * kStep + q.scale_bytes) + 1023) / 1024 * 1024;
+  q.stage_bytes = (kSteps * (kTileBytes + q.cols_cap * kStep + q.scale_bytes) + 1023) / 1024 * 1024;
   constexpr unsigned kRing = kScaleGroups * 4 * kScaleBytes;
   const unsigned tables = static_cast<unsigned>(table_bytes(p.E));
   const unsigned most = 227 * 1024 - sizeof(Shared) - 2048 - kRing - tables;
@@ -847,45 +890,40 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
                               static_cast<cuuint64_t>(p.E)};
   const cuuint64_t strides[4] = {row, rows * row, kStep / 2, p.M * row};
   const cuuint32_t box[5] = {kStep, static_cast<cuuint32_t>(kTileM / parts), static_cast<cuuint32_t>(parts),
-                             static_cast<cuuint32_t>(q.steps), 1};
+                             static_cast<cuuint32_t>(kSteps), 1};
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 5, const_cast<uint8_t*>(p.w), dims, strides, box, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
 
-  const int dev = current_device();
-  const void* fn = reinterpret_cast<const void*>(expert_linear_kernel);
-  cudaError_t err = ensure_dynamic_smem(fn, dev, smem);
-  if (err != cudaSuccess) return err;
-  const int sms = device_sms(dev);
-  if (sms < 1) return cudaErrorInvalidDevice;
   RowMaps maps;
-  maps.box128 = maps.box32 = maps.box8 = map;
   if (fp8) {
     const cuuint64_t xd[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.x_rows)};
     const cuuint64_t xs[1] = {static_cast<cuuint64_t>(p.K)};
-    CUtensorMap* const to[3] = {&maps.box128, &maps.box32, &maps.box8};
-    const cuuint32_t heights[3] = {128, 32, 8};
-    for (int i = 0; i < 3; ++i) {
-      const cuuint32_t b[2] = {kStep, heights[i]};
-      if (encode(to[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p.x), xd, xs, b, ones,
+    for (int i = 0; i < q.cols_cap / cluster / 8; ++i) {
+      const cuuint32_t b[2] = {kStep, static_cast<cuuint32_t>(8 * (i + 1))};
+      if (encode(&maps.box[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p.x), xd, xs, b, ones,
                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     }
   }
+  const int dev = current_device();
+  const int sms = device_sms(dev);
+  if (sms < 1) return cudaErrorInvalidDevice;
   // Items of the rows kernel: at most these.
   const int64_t groups = (p.max_rows + 7 * std::min<int64_t>(p.E, p.max_rows)) / 8;
   const int64_t items = groups * (fp8 ? 1 : (p.K + kRowSpan - 1) / kRowSpan);
-  err = launch_kernel(expert_rows_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(items, 2 * sms))),
-                      dim3(kThreads), tables, s, /*dependent=*/true, q);
+  const cudaError_t err =
+      launch_kernel(expert_rows_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(items, 6 * sms))), dim3(kThreads),
+                    tables, s, /*dependent=*/true, q);
   if (err != cudaSuccess) return err;
-  // One block an SM; of clusters, as many as are resident at once.
-  int grid = std::min(sms, kMaxBlocks);
-  if (q.cluster > 1) grid = std::min(grid, clusters_resident(fn, dev, kThreads, smem, q.cluster, grid) * q.cluster);
-  if (grid < 1) return cudaErrorInvalidConfiguration;
-  return launch_kernel_cluster(expert_linear_kernel, dim3(grid), dim3(kThreads), smem, s, q.cluster, q, map, maps);
+  if (cluster == 1)
+    return fp8 ? launch_products<true, 1>(q, map, maps, smem, dev, sms, s)
+               : launch_products<false, 1>(q, map, maps, smem, dev, sms, s);
+  return fp8 ? launch_products<true, kCluster>(q, map, maps, smem, dev, sms, s)
+             : launch_products<false, kCluster>(q, map, maps, smem, dev, sms, s);
 }
 
 }  // namespace ep

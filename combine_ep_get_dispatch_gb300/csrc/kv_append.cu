@@ -23,6 +23,8 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kMaxPage = 128;    // tokens
+constexpr int kQueryHeads = 4;   // query heads a thread rotates
 constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100
 
 // The smallest power of two >= fl(amax / 448), at least 2^-100 (amax finite).
@@ -189,7 +191,7 @@ __device__ int sequence_of_place(const KVParams& c, int u, int* s_b) {
 
 // kLanes threads a (unit, head, key or value): D / 16 of them hold a row.
 template <int kD, int kLanes>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KVAppendParams p) {
+__global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const KVAppendParams p) {
   constexpr int kRowLanes = kD / 16;
   constexpr int kRows = kLanes / kRowLanes;   // rows side by side
   constexpr int kGroups = kThreads / kLanes;  // (head, key or value) pairs a block
@@ -233,11 +235,33 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KVAppendParam
     float m = 0.0f;
     const int rows = live ? last - first : 0;
     float x[8], y[8];
-    for (int r = r0; r < rows; r += kRows) {
-      const uint4* g = reinterpret_cast<const uint4*>(base + static_cast<int64_t>(first + r) * stride);
-      unpack8(x, __ldg(g + va));
-      unpack8(y, __ldg(g + vb));
+    // The rows are read once and stay in registers between the maximum and the
+    // encoding (a page's whole share in the form for many rows).
+    constexpr int kHold = kLanes == kThreads ? kMaxPage / kRows : 1;
+    uint4 held_x[kHold], held_y[kHold];
+    auto row_at = [&](int r, const uint4& vx, const uint4& vy) {
+      unpack8(x, vx);
+      unpack8(y, vy);
       if (rot) rotate16(x, y, u, p.rope + static_cast<int64_t>(first + r) * p.rot, rot, p.interleaved);
+    };
+    auto load = [&](int r, uint4& vx, uint4& vy) {
+      const uint4* g = reinterpret_cast<const uint4*>(base + static_cast<int64_t>(first + r) * stride);
+      vx = __ldg(g + va);
+      vy = __ldg(g + vb);
+    };
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (r0 + i * kRows < rows) load(r0 + i * kRows, held_x[i], held_y[i]);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (r0 + i * kRows < rows) {
+        row_at(r0 + i * kRows, held_x[i], held_y[i]);
+        m = finite_max(finite_max(m, x), y);
+      }
+    for (int r = r0 + kHold * kRows; r < rows; r += kRows) {
+      uint4 vx, vy;
+      load(r, vx, vy);
+      row_at(r, vx, vy);
       m = finite_max(finite_max(m, x), y);
     }
     m = group_max<kLanes>(m, s_max);
@@ -263,14 +287,22 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KVAppendParam
       }
     }
     const float inv = pow2_inverse(s);
-    for (int r = r0; r < rows; r += kRows) {
-      const uint4* g = reinterpret_cast<const uint4*>(base + static_cast<int64_t>(first + r) * stride);
-      unpack8(x, __ldg(g + va));
-      unpack8(y, __ldg(g + vb));
-      if (rot) rotate16(x, y, u, p.rope + static_cast<int64_t>(first + r) * p.rot, rot, p.interleaved);
+    auto store = [&](int r) {
       uint2* o = reinterpret_cast<uint2*>(block + (held + r) * kD);
       o[va] = encode8(x, inv);
       o[vb] = encode8(y, inv);
+    };
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (r0 + i * kRows < rows) {
+        row_at(r0 + i * kRows, held_x[i], held_y[i]);
+        store(r0 + i * kRows);
+      }
+    for (int r = r0 + kHold * kRows; r < rows; r += kRows) {
+      uint4 vx, vy;
+      load(r, vx, vy);
+      row_at(r, vx, vy);
+      store(r);
     }
     // Every thread of the group has read the old scale before it changes.
     if (kLanes > 32) __syncthreads();
@@ -278,12 +310,23 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KVAppendParam
     if (lane == 0) *scale = s;
     return;
   }
-  // Queries: a thread for each 16 channels of a (token, head).
+  // Queries: a thread for 16 channels of kQueryHeads heads of a token, which
+  // share the token's cosines and sines.
   const int64_t i = (blockIdx.x - kv_blocks) * kThreads + tid;
-  const int per_token = p.QH * kRowLanes;
+  const int per_token = (p.QH + kQueryHeads - 1) / kQueryHeads * kRowLanes;
   const int64_t t = i / per_token;
   if (t >= c.N) return;
-  const int rest = static_cast<int>(i % per_token), head = rest / kRowLanes, u = rest % kRowLanes;
+  const int rest = static_cast<int>(i - t * per_token), u = rest % kRowLanes, h0 = rest / kRowLanes * kQueryHeads;
+  int va, vb;
+  vectors_of(u, p.rot, p.interleaved, va, vb);
+  uint4 vx[kQueryHeads], vy[kQueryHeads];
+#pragma unroll
+  for (int h = 0; h < kQueryHeads; ++h)
+    if (h0 + h < p.QH) {
+      const uint4* g = reinterpret_cast<const uint4*>(p.q + t * p.q_stride + (h0 + h) * kD);
+      vx[h] = g[va];
+      vy[h] = g[vb];
+    }
   int b = static_cast<int>(t);
   if (c.cu) {  // the last sequence that starts at or before t
     int lo = 0, hi = c.B;
@@ -298,26 +341,28 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KVAppendParam
   if (!tokens_of(c, b, t0, n) || t < t0 || t >= t0 + n) return;
   const int len = __ldg(c.lens + b);
   if (!length_ok(p, len, n)) return;
-  int va, vb;
-  vectors_of(u, p.rot, p.interleaved, va, vb);
-  const uint4* g = reinterpret_cast<const uint4*>(p.q + t * p.q_stride + head * kD);
-  float x[8], y[8];
-  unpack8(x, g[va]);
-  unpack8(y, g[vb]);
-  if (p.rot)
-    rotate16(x, y, u, p.rope + static_cast<int64_t>(len - n + (t - t0)) * p.rot, p.rot, p.interleaved);
-  uint4* o = reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + head * kD);
-  o[va] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                     pack_bf16x2(x[6], x[7]));
-  o[vb] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                     pack_bf16x2(y[6], y[7]));
+  const float* row = p.rope + static_cast<int64_t>(len - n + (t - t0)) * p.rot;
+#pragma unroll
+  for (int h = 0; h < kQueryHeads; ++h) {
+    if (h0 + h >= p.QH) break;
+    float x[8], y[8];
+    unpack8(x, vx[h]);
+    unpack8(y, vy[h]);
+    if (p.rot) rotate16(x, y, u, row, p.rot, p.interleaved);
+    uint4* o = reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + (h0 + h) * kD);
+    o[va] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                       pack_bf16x2(x[6], x[7]));
+    o[vb] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                       pack_bf16x2(y[6], y[7]));
+  }
 }
 
 template <int kD, int kLanes>
 cudaError_t launch(const KVAppendParams& p, cudaStream_t s) {
   const int groups = kThreads / kLanes;
   const int64_t kv = static_cast<int64_t>(p.units) * ((2 * p.c.KH + groups - 1) / groups);
-  const int64_t q = (static_cast<int64_t>(p.c.N) * p.QH * (kD / 16) + kThreads - 1) / kThreads;
+  const int64_t q =
+      (static_cast<int64_t>(p.c.N) * ((p.QH + kQueryHeads - 1) / kQueryHeads) * (kD / 16) + kThreads - 1) / kThreads;
   if (kv + q > INT32_MAX) return cudaErrorInvalidValue;
   return launch_kernel(kv_append_kernel<kD, kLanes>, dim3(static_cast<unsigned>(kv + q)), dim3(kThreads), 0, s,
                        /*dependent=*/true, p);

@@ -757,17 +757,17 @@ __global__ void __launch_bounds__(kThreads)
       // A shared unit: the last block to arrive adds the parts, in order.
       const int c_first = owner_of(total, blocks, g.unit * q.KS);
       const int c_last = owner_of(total, blocks, (g.unit + 1) * q.KS - 1);
-      __threadfence();
       epilogue_sync();
       if (m == 0) {
         unsigned* counter = q.counters + c_first * kC + rank;
+        __threadfence();  // the block's writes, which the barrier has ordered before it
         const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(c_last - c_first);
         if (last) *counter = 0u;
+        __threadfence();
         sh.last = last;
       }
       epilogue_sync();
       if (sh.last) {
-        __threadfence();
         for (int c0 = 0; c0 < rows8; c0 += 8) {
           float v[8];
 #pragma unroll

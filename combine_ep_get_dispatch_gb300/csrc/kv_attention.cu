@@ -77,7 +77,7 @@ struct Unit {
   int first;         // first token of chunk 0
   int c0, c1, total; // chunks [c0, c1) of `total`
   int it;            // the block's running number of chunk c0
-  int64_t at;        // place of chunk 0 among all units' places
+  int first_block, last_block;  // the blocks that share its chunks
 };
 
 // A sequence's units.
@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
       d.len = s.len;
       d.first = s.first;
       d.total = s.chunks;
-      d.at = unit_at + kUnitCost;
+      d.first_block = owner_of(total, blocks, unit_at + kUnitCost);
+      d.last_block = owner_of(total, blocks, unit_at + s.places() - 1);
       d.c0 = from;
       d.c1 = upto;
       d.it = it;
@@ -525,8 +526,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
     int e0 = 0;
     bool started = false;
 
-    int it = d.it + (tw - d.it % kTW + kTW) % kTW;  // the first of its chunks that is this group's
-    for (; it < d.it + d.c1 - d.c0; it += kTW) {
+    for (int it = d.it + tw; it < d.it + d.c1 - d.c0; it += kTW) {  // the groups take turns
       const int stage = it % kStages;
       // (A wait that gives up leaves wrong results and says so; the warp stays
       // for the barriers below, and the loading warp ends the work.)
@@ -779,23 +779,22 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
     // the last to arrive and in order: with one level a long sequence's last
     // block read 76 parts one after the other (82 us for 131072 tokens x 4
     // cache heads).
-    const int c_first = owner_of(total, blocks, d.at), c_last = owner_of(total, blocks, d.at + d.total - 1);
+    const int c_first = d.first_block, c_last = d.last_block;
     auto part = [&](int block, bool starts) {
       return partial + (static_cast<int64_t>(block) * 2 + (starts ? 1 : 0)) * kPart;
     };
     // One block's arrival on a counter that expects `n`: whether it is the last.
     auto arrive = [&](unsigned* counter, int n) {
-      __threadfence();
       compute_sync();
       if (tid == 0) {
+        __threadfence();  // the block's writes, which the barrier has ordered before it
         const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(n - 1);
         if (last) *counter = 0u;
+        __threadfence();
         sh.last = last;
       }
       compute_sync();
-      const bool last = sh.last;
-      if (last) __threadfence();
-      return last;
+      return sh.last != 0;
     };
     // Join parts first, first + step, ... below stop (the unit's first one lies in its block's
     // second slot): into part `to`, or as the result when `to` is null.

@@ -41,7 +41,8 @@ constexpr int kStep = 128;                  // inputs a step
 constexpr int kTileM = 128;                 // outputs a unit (with GLU: 64 gates, 64 ups)
 constexpr int kTileBytes = kTileM * kStep;  // weights of a step in shared memory (8-bit containers)
 constexpr int kTileTx = kTileBytes / 2;     // ... and as TMA counts them
-constexpr int kSteps = 2;                   // steps a stage holds
+constexpr int kMaxSteps = 2;                // most steps a stage holds
+constexpr int kWideSteps = 1;               // steps of a stage, where there are clusters
 constexpr int kCluster = 4;                 // blocks of a cluster, where there are clusters
 constexpr int kRowMaps = 8;                 // boxes of 8, 16 .. 64 rows
 constexpr int kScaleBytes = 512;            // scale bytes of 128 rows for one step
@@ -61,7 +62,8 @@ struct Params {
   int tile_rows;    // rows of a full tile
   int cols_cap;     // its columns
   int KB;           // steps of a unit: K / 128
-  int KS;           // stages of a unit: two steps each, the last one perhaps one
+  int steps;        // of a stage, 1 or 2
+  int KS;           // stages of a unit; the last one may hold one step of two
   int MT;           // units of a tile: an expert's output tiles, a cluster's blocks taking one each
   int stages;
   unsigned stage_bytes;
@@ -231,11 +233,11 @@ __global__ void __launch_bounds__(kThreads) expert_rows_kernel(const Params q) {
     // Of a stage's steps (the last one may hold one of two): their codes, then their scales.
     const int step = cols * kStep + q.scale_bytes;
     auto codes = [&](int kb) {
-      const int h = kb % kSteps;
+      const int h = kb % q.steps;
       return image + static_cast<int64_t>(kb - h) * step + h * cols * kStep;
     };
     auto scales = [&](int kb) {
-      const int h = kb % kSteps, n = min(kSteps, q.KB - (kb - h));
+      const int h = kb % q.steps, n = min(q.steps, q.KB - (kb - h));
       return image + static_cast<int64_t>(kb - h) * step + n * cols * kStep + h * q.scale_bytes;
     };
     // Column c of step kb, 16-byte piece `piece`.
@@ -411,7 +413,8 @@ struct RowMaps {
 
 // kFp8: x in E4M3. kC: blocks of a cluster; more than one where tiles have 128
 // columns or more.
-template <bool kFp8, int kC>
+// kSteps: steps of a stage.
+template <bool kFp8, int kC, int kSteps>
 __global__ void __launch_bounds__(kThreads)
     expert_linear_kernel(const Params q, const __grid_constant__ CUtensorMap map,
                          const __grid_constant__ RowMaps maps) {
@@ -584,8 +587,8 @@ __global__ void __launch_bounds__(kThreads)
         full = mbar_ask(&sh.full[r.stage], r.parity);
         scales = mbar_ask(&sh.scale_full[group], group_parity);
         const uint64_t ws = ws0 + (this_group * 4 + (kb & 3)) * (kScaleBytes / 16);
-        const uint32_t sc = tmem + kTmemScales + slot * kSteps * kScaleCols;
-        const bool both = kb + 1 < q.KB;
+        const uint32_t sc = tmem + kTmemScales + slot * kMaxSteps * kScaleCols;
+        const bool both = kSteps > 1 && kb + 1 < q.KB;
         const uint64_t xs = xs0 + at + (both ? 2 : 1) * x_step;
         // 32 inputs a product: 32 bytes on.
         auto step = [&](int h, bool accumulate) {
@@ -836,10 +839,10 @@ Sizes sizes_of(int E, int64_t max_rows, int K, bool fp8) {
 
 namespace {
 
-template <bool kFp8, int kC>
+template <bool kFp8, int kC, int kSteps>
 cudaError_t launch_products(const Params& q, const CUtensorMap& map, const RowMaps& maps, size_t smem, int dev, int sms,
                             cudaStream_t s) {
-  const auto kernel = expert_linear_kernel<kFp8, kC>;
+  const auto kernel = expert_linear_kernel<kFp8, kC, kSteps>;
   const void* fn = reinterpret_cast<const void*>(kernel);
   const cudaError_t err = ensure_dynamic_smem(fn, dev, smem);
   if (err != cudaSuccess) return err;
@@ -864,7 +867,8 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   q.tile_rows = z.tile_rows;
   q.cols_cap = z.tile_rows * q.mult;
   q.KB = p.K / kStep;
-  q.KS = (q.KB + kSteps - 1) / kSteps;
+  q.steps = cluster_for(q.cols_cap) == 1 ? kMaxSteps : kWideSteps;
+  q.KS = (q.KB + q.steps - 1) / q.steps;
   const int cluster = cluster_for(q.cols_cap);
   q.MT = p.glu ? (p.M / 2 + 63) / 64 : (p.M + kTileM - 1) / kTileM;
   q.MT = (q.MT + cluster - 1) / cluster;
@@ -872,7 +876,7 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   q.partial = reinterpret_cast<float*>(p.ws + z.partial);
   q.image = p.ws + z.image;
   q.scale_bytes = q.cols_cap > 128 ? 2 * kScaleBytes : kScaleBytes;
-  q.stage_bytes = (kSteps * (kTileBytes + q.cols_cap * kStep + q.scale_bytes) + 1023) / 1024 * 1024;
+  q.stage_bytes = (q.steps * (kTileBytes + q.cols_cap * kStep + q.scale_bytes) + 1023) / 1024 * 1024;
   constexpr unsigned kRing = kScaleGroups * 4 * kScaleBytes;
   const unsigned tables = static_cast<unsigned>(table_bytes(p.E));
   const unsigned most = 227 * 1024 - sizeof(Shared) - 2048 - kRing - tables;
@@ -890,7 +894,7 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
                               static_cast<cuuint64_t>(p.E)};
   const cuuint64_t strides[4] = {row, rows * row, kStep / 2, p.M * row};
   const cuuint32_t box[5] = {kStep, static_cast<cuuint32_t>(kTileM / parts), static_cast<cuuint32_t>(parts),
-                             static_cast<cuuint32_t>(kSteps), 1};
+                             static_cast<cuuint32_t>(q.steps), 1};
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 5, const_cast<uint8_t*>(p.w), dims, strides, box, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -920,10 +924,10 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
                     tables, s, /*dependent=*/true, q);
   if (err != cudaSuccess) return err;
   if (cluster == 1)
-    return fp8 ? launch_products<true, 1>(q, map, maps, smem, dev, sms, s)
-               : launch_products<false, 1>(q, map, maps, smem, dev, sms, s);
-  return fp8 ? launch_products<true, kCluster>(q, map, maps, smem, dev, sms, s)
-             : launch_products<false, kCluster>(q, map, maps, smem, dev, sms, s);
+    return fp8 ? launch_products<true, 1, 2>(q, map, maps, smem, dev, sms, s)
+               : launch_products<false, 1, 2>(q, map, maps, smem, dev, sms, s);
+  return fp8 ? launch_products<true, kCluster, kWideSteps>(q, map, maps, smem, dev, sms, s)
+             : launch_products<false, kCluster, kWideSteps>(q, map, maps, smem, dev, sms, s);
 }
 
 }  // namespace ep

@@ -42,9 +42,7 @@ constexpr int kTileM = 128;                 // outputs a unit (with GLU: 64 gate
 constexpr int kTileBytes = kTileM * kStep;  // weights of a step in shared memory (8-bit containers)
 constexpr int kTileTx = kTileBytes / 2;     // ... and as TMA counts them
 constexpr int kMaxSteps = 2;                // most steps a stage holds
-constexpr int kWideSteps = 1;               // steps of a stage, where there are clusters
-constexpr int kCluster = 4;                 // blocks of a cluster, where there are clusters
-constexpr int kRowMaps = 8;                 // boxes of 8, 16 .. 64 rows
+constexpr int kRowMaps = 12;                // boxes of 8, 16 .. 96 rows
 constexpr int kScaleBytes = 512;            // scale bytes of 128 rows for one step
 constexpr int kMaxCols = 192;
 constexpr int kMaxBlocks = 160;             // blocks a workspace has room for
@@ -411,8 +409,7 @@ struct RowMaps {
   CUtensorMap box[kRowMaps];
 };
 
-// kFp8: x in E4M3. kC: blocks of a cluster; more than one where tiles have 128
-// columns or more.
+// kFp8: x in E4M3. kC: blocks of a cluster.
 // kSteps: steps of a stage.
 template <bool kFp8, int kC, int kSteps>
 __global__ void __launch_bounds__(kThreads)
@@ -565,7 +562,7 @@ __global__ void __launch_bounds__(kThreads)
       tmem_fence_after();
       const uint32_t d = tmem + buf * kMaxCols;
       const uint32_t idesc = idesc_e2m1_e4m3(g.cols);
-      const bool wide = kC > 1 && g.cols > 128;
+      const bool wide = kSteps == 1 && g.cols > 128;
       const unsigned x_step = loaded_cols<kFp8, kC>(g.cols) * kStep >> 4, xs_step = q.scale_bytes >> 4;
       for (int st = g.s0; st < g.s1; ++st) {
         const int kb = st * kSteps;
@@ -811,8 +808,20 @@ int tile_rows_for(int E, int64_t max_rows, int mult) {
   return kMaxCols / mult;
 }
 
-// Blocks of a cluster.
-int cluster_for(int cols) { return cols >= 128 ? kCluster : 1; }
+// Steps of a stage: two halve what a stage costs besides its bytes, unless a
+// tile's rows leave room for too few of them (128 rows an expert: 1477 us with
+// two stages of two steps, 1204 with four of one).
+int steps_for(int cols) { return cols <= 64 ? 2 : 1; }
+
+// Blocks of a cluster. Sharing the loads of rows pays from two columns tiles
+// of 16 on: 128 tokens x 256 experts 704 us alone, 676 in pairs; 128 rows an
+// expert 1338 in pairs, 1204 in fours, 1326 in eights (of which fewer fit the
+// GPU at once). Not where the last cluster of an expert's `tiles` output tiles
+// would stand idle for a good part.
+int cluster_for(int cols, int tiles) {
+  if (cols <= 64) return cols >= 32 && (tiles % 2 == 0 || tiles >= 8) ? 2 : 1;
+  return tiles % 4 == 0 || tiles >= 16 ? 4 : 2;
+}
 
 struct Sizes {
   int tile_rows;
@@ -853,6 +862,15 @@ cudaError_t launch_products(const Params& q, const CUtensorMap& map, const RowMa
   return launch_kernel_cluster(kernel, dim3(grid), dim3(kThreads), smem, s, kC, q, map, maps);
 }
 
+template <bool kFp8>
+cudaError_t launch_cluster(int cluster, const Params& q, const CUtensorMap& map, const RowMaps& maps, size_t smem,
+                           int dev, int sms, cudaStream_t s) {
+  if (cluster == 1) return launch_products<kFp8, 1, 2>(q, map, maps, smem, dev, sms, s);
+  if (q.steps == 2) return launch_products<kFp8, 2, 2>(q, map, maps, smem, dev, sms, s);
+  if (cluster == 2) return launch_products<kFp8, 2, 1>(q, map, maps, smem, dev, sms, s);
+  return launch_products<kFp8, 4, 1>(q, map, maps, smem, dev, sms, s);
+}
+
 }  // namespace
 
 size_t expert_linear_ws_bytes(int E, int64_t max_rows, int K, bool fp8) { return sizes_of(E, max_rows, K, fp8).total; }
@@ -867,10 +885,10 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   q.tile_rows = z.tile_rows;
   q.cols_cap = z.tile_rows * q.mult;
   q.KB = p.K / kStep;
-  q.steps = cluster_for(q.cols_cap) == 1 ? kMaxSteps : kWideSteps;
+  q.steps = steps_for(q.cols_cap);
   q.KS = (q.KB + q.steps - 1) / q.steps;
-  const int cluster = cluster_for(q.cols_cap);
   q.MT = p.glu ? (p.M / 2 + 63) / 64 : (p.M + kTileM - 1) / kTileM;
+  const int cluster = cluster_for(q.cols_cap, q.MT);
   q.MT = (q.MT + cluster - 1) / cluster;
   q.counters = reinterpret_cast<unsigned*>(p.ws + z.counters);
   q.partial = reinterpret_cast<float*>(p.ws + z.partial);
@@ -923,11 +941,8 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
       launch_kernel(expert_rows_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(items, 6 * sms))), dim3(kThreads),
                     tables, s, /*dependent=*/true, q);
   if (err != cudaSuccess) return err;
-  if (cluster == 1)
-    return fp8 ? launch_products<true, 1, 2>(q, map, maps, smem, dev, sms, s)
-               : launch_products<false, 1, 2>(q, map, maps, smem, dev, sms, s);
-  return fp8 ? launch_products<true, kCluster, kWideSteps>(q, map, maps, smem, dev, sms, s)
-             : launch_products<false, kCluster, kWideSteps>(q, map, maps, smem, dev, sms, s);
+  return fp8 ? launch_cluster<true>(cluster, q, map, maps, smem, dev, sms, s)
+             : launch_cluster<false>(cluster, q, map, maps, smem, dev, sms, s);
 }
 
 }  // namespace ep

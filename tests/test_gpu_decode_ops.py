@@ -444,6 +444,13 @@ LINEARS = [
     (2048, 128, [1] * 20, False),
     (7168, 256, [4, 0, 1, 33], True),
     (896, 640, [0, 0, 0, 7], False),
+    # clusters of two and four blocks, whole and with an idle end; odd numbers of 128 inputs
+    (256, 256, [4, 5, 3, 4], False),
+    (640, 1168, [9, 2, 0, 7, 12], False),
+    (384, 512, [30, 25, 11], True),
+    (256, 1024, [130, 40], False),
+    (384, 2080, [200, 0, 90, 191, 193], False),
+    (896, 528, [150, 100], True),
 ]
 
 

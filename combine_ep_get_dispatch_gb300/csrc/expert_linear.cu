@@ -19,9 +19,21 @@
 // adds them in the order of the steps, so that the result does not depend on
 // which one that was.
 //
-// With many rows the blocks' reads of x, not HBM, set the pace: each of an
-// expert's 32 or more output tiles needs all of its rows. Blocks then work in
-// clusters of neighbouring output tiles, each loads a share of the rows for all.
+// Next after HBM comes shared memory: 4-bit codes lie there in 8-bit
+// containers, so 256 inputs of 128 outputs are written (32 KB) and read (32 KB)
+// at 128 bytes a cycle in 512 of the 750 cycles that HBM gives them; a product
+// of 16 columns costs 75 cycles beside those writes, 43 alone, whatever the
+// tensor cores could do. Loads ahead of the ring into L2 only cost (995 us
+// where 783 were without: every load passes the same engine).
+//
+// With more rows the blocks' reads of x set the pace: each of an expert's
+// output tiles needs all of its rows. Blocks then work in clusters of
+// neighbouring output tiles, each loads a share of the rows for all.
+//
+// Measured (256 experts, 7168 inputs, 2 x 2048 gated outputs; copy rate 6.69
+// TB/s): 4 BF16 rows an expert 676 us, 5.8 TB/s; 128 E4M3 rows 1204 us, 3.6
+// TB/s and 1.6 PFLOP/s; one token's eight experts 36 us, of which 12 pass before
+// the first weights have come and 4 after the last.
 //
 // Two launches: expert_rows_kernel splits BF16 rows into the tensor cores'
 // shared-memory layout (of E4M3 rows it lays out the scales; their codes come

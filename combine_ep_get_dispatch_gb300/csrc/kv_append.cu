@@ -15,6 +15,14 @@
 // on any order. A row of a head is held by D / 16 threads, 16 channels each:
 // the two 8-channel vectors that rotate into one another. The queries' blocks
 // follow in the same launch.
+//
+// What bounds it: a few tokens' launch (1 token 2.8 us, 256 tokens 3.7 us on the
+// device); for prompts HBM: 16.9 k tokens, 32 query and 4 cache heads of 128,
+// 200 MB in 38.5 us, 5.2 TB/s (copy rate 6.69). Rows stay in registers between the
+// maximum and the encoding, and a thread rotates four heads of a token with one
+// read of its cosines and sines (a head each: 46 us).
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -375,11 +383,17 @@ cudaError_t launch_kv_append(const KVAppendParams& in, cudaStream_t s) {
   KVAppendParams p = in;
   const KVParams& c = p.c;
   p.units = c.cu ? (c.N >> c.log2P) + 2 * c.B : c.B;
-  // A few threads a block where a sequence brings a token or so, a thread
-  // block where it brings many.
-  const bool few = c.N <= 2 * static_cast<int64_t>(c.B);
-  if (c.D == 64) return few ? launch<64, 4>(p, s) : launch<64, 128>(p, s);
-  return few ? launch<128, 8>(p, s) : launch<128, 128>(p, s);
+  // Threads of a block (page, head, keys or values): few where a sequence
+  // brings few tokens, a warp where it brings a good part of a page, and 128
+  // where there are too few blocks to fill the GPU otherwise. 200 sequences, 8
+  // heads of 128, pages of 64, in us with 8 / 32 / 128 threads: 1 token each 3.3 /
+  // 5.4 / 13.1, 8 tokens 14.4 / 16.8 / 36.2, 16 tokens 28.4 / 26.2 / 45.6, 64 tokens
+  // 127 / 86 / 106; five prompts of 16.9 k tokens, 4 heads, pages of 128: 207 / 72 / 39.
+  const int64_t each = std::min<int64_t>(c.P, (c.N + c.B - 1) / c.B);
+  const int64_t blocks = (static_cast<int64_t>(c.N >> c.log2P) + c.B) * 2 * c.KH;
+  const int lanes = each >= 32 && blocks * 32 < 65536 ? 128 : each >= 12 && c.P >= 32 ? 32 : 8;
+  if (c.D == 64) return lanes == 8 ? launch<64, 8>(p, s) : lanes == 32 ? launch<64, 32>(p, s) : launch<64, 128>(p, s);
+  return lanes == 8 ? launch<128, 8>(p, s) : lanes == 32 ? launch<128, 32>(p, s) : launch<128, 128>(p, s);
 }
 
 }  // namespace ep

@@ -33,6 +33,13 @@
 // at the end of a unit. A unit that several blocks share is joined by the last
 // of them to finish, in the order of its chunks, so results do not depend on
 // which one that was.
+//
+// Measured (head size 128): 128 sequences x 8192 tokens x 8 cache heads, 8 rows
+// each, 331 us, 6.5 TB/s (copy rate 6.69); one sequence of 131072 tokens, 4 x 16
+// rows, 37 us: 4 before its first chunk, 23 for the chunks, 10 for joining 76
+// parts. 32 rows: the products' warps, not HBM, set the pace (20000 tokens x 24
+// x 4 heads: 153 us, 88 with the computing left out). Tried there without gain:
+// four column tiles a warp, two chunks at once, smaller tiles on more warps.
 #include <cuda.h>
 
 #include "common.cuh"
@@ -46,7 +53,8 @@ namespace {
 constexpr int kChunk = 32;       // tokens
 constexpr int kWarps = 4;        // computing warps
 constexpr int kThreads = 256;    // the computing warps, a loading one, and three that complete its warpgroup
-constexpr int kComputeRegs = 216, kLoadRegs = 40;  // of the 2 x 128 a thread pair is launched with
+constexpr int kComputeRegs = 216, kLoadRegs = 40;  // of the 2 x 128 a thread pair is launched with (400 us -> 331
+                                                   // for 128 x 8192 tokens: nothing spills)
 constexpr int kMaxBlocks = 320;  // blocks a workspace has room for
 constexpr int kFan = 8;          // parts of a shared unit that one block joins at once
 constexpr int kUnitCost = 6;     // chunks that a unit costs besides its own: queries, joining, results

@@ -79,6 +79,9 @@ APPENDS = [
     (128, 128, 4, 4, 16, False, [(100, 300), (0, 129), (127, 1)]),
     (64, 128, 5, 10, 0, False, [(2, 131), (0, 17)]),
     (128, 16, 17, 17, 128, False, [(0, 40)]),
+    (128, 64, 1, 2, 128, False, [(10, 15), (60, 20), (0, 12)]),
+    (64, 32, 3, 3, 64, True, [(31, 13), (1, 30), (0, 64)]),
+    (64, 64, 2, 1, 32, False, [(7, 130)]),
 ]
 
 

@@ -22,7 +22,7 @@ int cache_setup(const ep_kv_cache_t* C, const int32_t* seq_lens, const int32_t* 
   if (D != 64 && D != 128) return EP_ERR_INVALID_ARG;
   if (C->num_pages < 0 || C->num_heads < 1 || C->num_heads > 1024 || C->num_seqs < 0 || C->max_pages < 0)
     return EP_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(C->max_pages) * P > INT32_MAX) return EP_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(C->max_pages) * P > INT32_MAX || C->num_seqs > (1 << 28)) return EP_ERR_INVALID_ARG;
   if (!cu_tokens && N != C->num_seqs) return EP_ERR_INVALID_ARG;
   if (N > 0) {
     if (!seq_lens || C->num_seqs < 1 || C->num_pages < 1) return EP_ERR_INVALID_ARG;

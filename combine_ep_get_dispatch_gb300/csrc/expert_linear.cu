@@ -554,6 +554,9 @@ __global__ void __launch_bounds__(kThreads)
         x += kSteps * image_step;
       }
     }
+    if (!ok) {  // given up: loads in flight land before the block ends
+      for (int i = 0; i < q.stages; ++i) mbar_drain(&sh.full[i], i < r.stage ? r.parity : r.parity ^ 1);
+    }
   } else if (warp == 1) {
     // Products.
     Segment g;
@@ -581,6 +584,7 @@ __global__ void __launch_bounds__(kThreads)
         const bool group_start = st == g.s0 || (kb & 3) == 0;
         if ((group_start && !mbar_wait_asked(scales, &sh.scale_full[group], group_parity, p.status)) ||
             !mbar_wait_asked(full, &sh.full[r.stage], r.parity, p.status)) {
+          mbar_drain(&sh.full[r.stage], r.parity);
           ok = false;
           break;
         }

@@ -180,7 +180,8 @@ __device__ __forceinline__ float group_max(float m, float* s_max) {
 }
 
 // The unit at place `u` of the grid: its sequence. Sequence b's places start
-// at cu[b] / P + 2 b: at least as many as the pages its tokens can touch.
+// at cu[b] / P + 2 b: at least as many as the pages its tokens can touch. Sequences
+// that cu_tokens has out of order have none.
 // Whole block; every thread returns b, or -1.
 __device__ int sequence_of_place(const KVParams& c, int u, int* s_b) {
   if (!c.cu) return u;
@@ -190,6 +191,10 @@ __device__ int sequence_of_place(const KVParams& c, int u, int* s_b) {
     const int b = b0 + threadIdx.x;
     if (b < c.B) {
       const int lo = __ldg(c.cu + b), hi = __ldg(c.cu + b + 1);
+      if (lo < 0 || hi < lo || hi > c.N) {  // it has no places, or not all of them
+        flag(c.status, EP_ST_BAD_INDEX);
+        continue;
+      }
       if (u >= (lo >> c.log2P) + 2 * b && u < (hi >> c.log2P) + 2 * (b + 1)) *s_b = b;
     }
   }

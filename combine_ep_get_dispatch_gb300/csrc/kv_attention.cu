@@ -7,7 +7,9 @@
 // into the exponent, p_j = 2^(s_j + ev - m) with m the maximum of s_j + ev, so
 // that p stays in [0, 1] whatever the scales (taken times 2^15 in fp16, so that
 // weights keep 11 bits down to 2^-29 of the largest); the normaliser sums p_j 2^(e0 - ev),
-// e0 the first block's exponent. Codes and p enter the products as fp16 (an
+// e0 the first block's exponent, kept in [-26, 0]: its block may be one that no
+// row sees, whose scale can be anything, and 2^(e0 - ev) stays in fp32's range for
+// every ev in [-127, 100]. Codes and p enter the products as fp16 (an
 // E4M3 value is exact in it, p keeps 11 bits); q as fp16 too, divided by a power
 // of two that brings its row's largest magnitude to [1, 2).
 //
@@ -193,7 +195,7 @@ __device__ __forceinline__ Sequence sequence_at(const KVAttentionParams& p, int 
   const int stop = s.len < cap ? max(s.len, 0) : static_cast<int>(cap);
   const int64_t low = p.window > 0 ? static_cast<int64_t>(s.len) - s.n - p.window + 1 : 0;
   s.first = low > 0 ? static_cast<int>(low) & ~(kChunk - 1) : 0;
-  s.chunks = max(1, (stop - s.first + kChunk - 1) / kChunk);
+  s.chunks = stop > s.first ? (stop - s.first - 1) / kChunk + 1 : 1;
   s.tiles = static_cast<int>((static_cast<int64_t>(s.n) * p.G + tile_rows - 1) / tile_rows);
   return s;
 }
@@ -339,7 +341,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
       d.c1 = upto;
       d.it = it;
       const int slot = un % kUnits;
-      if (un >= kUnits && !mbar_wait_warp(&sh.unit_empty[slot], (un / kUnits - 1) & 1, c.status)) break;
+      if (un >= kUnits && !mbar_wait_warp(&sh.unit_empty[slot], (un / kUnits - 1) & 1, c.status)) {
+        ok = false;
+        break;
+      }
       if (lane == 0) {
         sh.unit[slot] = d;
         sh.more[slot] = 1;
@@ -444,6 +449,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
         }
       }
     }
+    if (!ok) {  // given up: loads in flight land before the block ends
+      for (int i = 0; i < kStages; ++i)
+        if (i < stage || it >= kStages) mbar_drain(&sh.full[i], i < stage ? parity : parity ^ 1);
+    }
     const int slot = un % kUnits;
     if (un < kUnits || mbar_wait_warp(&sh.unit_empty[slot], (un / kUnits - 1) & 1, c.status)) {
       if (lane == 0) {
@@ -538,12 +547,15 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
       const int stage = it % kStages;
       // (A wait that gives up leaves wrong results and says so; the warp stays
       // for the barriers below, and the loading warp ends the work.)
-      if (!mbar_wait_warp(&sh.full[stage], (it / kStages) & 1, c.status)) break;
+      if (!mbar_wait_warp(&sh.full[stage], (it / kStages) & 1, c.status)) {
+        mbar_drain(&sh.full[stage], (it / kStages) & 1);
+        break;
+      }
       const ChunkHeader hd = sh.header[stage];
       const uint32_t kbuf = sbase + stage * S::kStage, vbuf = kbuf + S::kSide;
       const int tok = d.first + (d.c0 + it - d.it) * kChunk;
       if (!started) {
-        e0 = hd.ev[0];
+        e0 = min(0, max(-26, hd.ev[0]));
         started = true;
       }
       // Scores: tokens 16 h + g (and + 8) of the chunk, rows 8 t + 2j, + 1.

@@ -573,7 +573,7 @@ int ep_fp8_quantize(const void* x, int64_t rows, int hidden, int fp8_flags, uint
  *                     length are not read; an entry outside [0, num_pages)
  *                     below it flags EP_ST_BAD_INDEX (append skips the page's
  *                     tokens, attention treats them as masked)
- *   page_size         16, 32, 64 or 128; head_dim 64 or 128
+ *   page_size         16, 32, 64 or 128; head_dim 64 or 128; num_seqs <= 2^28
  * Neither the codes past a sequence's last token nor the scales of unused
  * pages need to be initialised.
  */
@@ -620,8 +620,9 @@ typedef struct ep_kv_cache {
  *                 aligned; NULL with rope_dim 0: no rotation (queries are copied)
  *   rope_dim      a multiple of 16, <= head_dim
  *   status        EP_ST_BAD_INDEX: a page outside the cache, cu_tokens out of
- *                 order, a sequence shorter than its new tokens or longer than
- *                 rope_rows; EP_ST_CAPACITY: longer than max_pages * page_size.
+ *                 order (sequences that overlap may then be skipped too), a
+ *                 sequence shorter than its new tokens or longer than rope_rows;
+ *                 EP_ST_CAPACITY: longer than max_pages * page_size.
  *                 The sequence's tokens are then skipped, their queries too; for
  *                 a page outside the cache, its keys and values alone.
  */
@@ -643,9 +644,12 @@ size_t ep_kv_attention_workspace_bytes(int num_tokens, int num_q_heads, int num_
  * already holds the new tokens (ep_kv_append). Products take q as an 11-bit
  * significand scaled by its row's largest magnitude (a BF16 value keeps all
  * its bits down to 2^-14 of it) and softmax weights as 11-bit significands (down
- * to 2^-29 of the row's largest); sums, maxima and normalisers are fp32. A token with nothing to attend
- * (seq_lens[b] = 0, a negative position) gets zeros, and lse -inf. Codes at
- * masked positions are never used, NaN among them.
+ * to 2^-29 of the row's largest); sums, maxima and normalisers are fp32. A
+ * token with nothing to attend (seq_lens[b] = 0, a negative position) gets
+ * zeros, and lse -inf. Codes and scales at masked positions are never used, NaN
+ * among them. The scales of the value blocks that a token sees are expected
+ * within [2^-100, 2^100] (ep_kv_append's are, up to values of 2^108) and within
+ * 2^120 of one another.
  *
  *   q            [num_tokens, num_q_heads, head_dim] BF16, tokens q_stride
  *                elements apart (a multiple of 8)

@@ -210,6 +210,18 @@ def test_append_reports_what_it_skips():
         append_and_compare(dict(c, table=t), [20, 40, 9], cu, 13, KH, D, None, ep.EP_ST_BAD_INDEX, [0, 2], False)
 
 
+def test_append_reports_every_list_out_of_order():
+    """Also where the sequence that is out of order has no page of its own in the call."""
+    rng = np.random.default_rng(17)
+    c = random_cache(rng, [200, 200, 200], 16, 1, 64)
+    for cu in ([0, 100, 10, 110], [110, 110, 110, 110], [-5, -5, -5, 0], [0, 111, 111, 111], [500, 2, 3, 4]):
+        cache, st = device_cache(c), new_status()
+        k = torch.zeros(110, 1, 64, dtype=torch.bfloat16, device="cuda")
+        ep.kv_append(k, k, cache, to_dev(np.array([200, 200, 200], np.int32)), cu_tokens=to_dev(np.array(cu, np.int32)),
+                     status=st)
+        assert status_value(st) == (0 if cu[0] == 110 else ep.EP_ST_BAD_INDEX), cu
+
+
 def test_append_nothing():
     cache = ep.new_kv_cache(2, 2, 16, 64, torch.zeros((0, 4), dtype=torch.int32, device="cuda"))
     k = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
@@ -296,6 +308,36 @@ def test_attention_of_blocks_with_far_apart_scales():
         out, lse = ep.kv_attention(q, device_cache(c), torch.tensor([200], dtype=torch.int32, device="cuda"),
                                    scale=scale, return_lse=True)
         check_attention(c, [200], [0, 1], f64(q), scale, 0, out, lse)
+
+
+@pytest.mark.parametrize("unseen", [0.0, 2.0 ** -100, 2.0 ** 120, np.inf, np.nan])
+def test_attention_never_uses_the_scales_of_pages_it_does_not_see(unseen):
+    """Pages of 16 that the window leaves out, the first one of a chunk of tokens that it does not."""
+    rng = np.random.default_rng(18)
+    lens = [50, 61, 16 * 41 + 9]
+    c = random_cache(rng, lens, 16, 2, 64)
+    c["v_scale"] *= 2.0 ** 9   # blocks of magnitudes above 448: exponents above zero
+    for b, n in enumerate(lens):
+        for j in range((n - 10) // 16):
+            page = c["table"][b, j]
+            c["k"][page] = c["v"][page] = 0x7F
+            c["k_scale"][page] = c["v_scale"][page] = unseen
+    q = bf16(rng.normal(size=(3, 8, 64))).cuda()
+    out, lse = ep.kv_attention(q, device_cache(c), to_dev(np.array(lens, np.int32)), scale=0.1, window=10, return_lse=True)
+    check_attention(c, lens, [0, 1, 2, 3], f64(q), 0.1, 10, out, lse)
+
+
+@pytest.mark.parametrize("first", [True, False])
+def test_attention_of_zero_value_blocks_beside_large_ones(first):
+    """A block of zeros has the smallest scale, 2^-100; its tokens count in the normaliser as any others."""
+    rng = np.random.default_rng(19)
+    c = random_cache(rng, [64], 16, 1, 64)
+    zeros, large = c["table"][0, :2] if first else c["table"][0, [2, 0]]
+    c["v"][zeros], c["v_scale"][zeros] = 0, 2.0 ** -100
+    c["v_scale"][large] = 2.0 ** 19   # magnitudes up to 2^28
+    q = bf16(rng.normal(size=(1, 4, 64))).cuda()
+    out, lse = ep.kv_attention(q, device_cache(c), to_dev(np.array([64], np.int32)), scale=0.05, return_lse=True)
+    check_attention(c, [64], [0, 1], f64(q), 0.05, 0, out, lse)
 
 
 def test_attention_masks_bad_pages_and_reports_them():

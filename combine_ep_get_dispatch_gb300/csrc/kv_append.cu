@@ -388,15 +388,20 @@ cudaError_t launch_kv_append(const KVAppendParams& in, cudaStream_t s) {
   KVAppendParams p = in;
   const KVParams& c = p.c;
   p.units = c.cu ? (c.N >> c.log2P) + 2 * c.B : c.B;
-  // Threads of a block (page, head, keys or values): few where a sequence
-  // brings few tokens, a warp where it brings a good part of a page, and 128
-  // where there are too few blocks to fill the GPU otherwise. 200 sequences, 8
-  // heads of 128, pages of 64, in us with 8 / 32 / 128 threads: 1 token each 3.3 /
-  // 5.4 / 13.1, 8 tokens 14.4 / 16.8 / 36.2, 16 tokens 28.4 / 26.2 / 45.6, 64 tokens
-  // 127 / 86 / 106; five prompts of 16.9 k tokens, 4 heads, pages of 128: 207 / 72 / 39.
-  const int64_t each = std::min<int64_t>(c.P, (c.N + c.B - 1) / c.B);
+  // Threads of a block (page, head, keys or values). Eight hold one token's row
+  // of a head: enough for one token a sequence, and for a few where there are
+  // blocks enough to fill the GPU. A block's rows follow one another, so otherwise
+  // a warp takes them, and 128 threads where sequences bring many and blocks are
+  // few. In us with 8 / 32 / 128, 8 heads of 128: 200 sequences x 1 token 3.2 / 3.9 /
+  // 12.7, x 4 8.7 / 9.6 / 22.8, x 16 30 / 27 / 46, x 64 118 / 87 / 107; 33 of 1 to 9 tokens
+  // 8.1 / 4.2 / 5.7; 9 of 1 to 47 45 / 10.4 / 6.0; 4 of 1 to 500 59 / 13.3 / 6.7; 60 of 1
+  // to 30 22 / 8.0 / 8.7; five prompts of 16.9 k tokens, 4 heads: 207 / 72 / 39.
+  const int64_t each = std::min<int64_t>(c.P, (static_cast<int64_t>(c.N) + c.B - 1) / c.B);
   const int64_t blocks = (static_cast<int64_t>(c.N >> c.log2P) + c.B) * 2 * c.KH;
-  const int lanes = each >= 32 && blocks * 32 < 65536 ? 128 : each >= 12 && c.P >= 32 ? 32 : 8;
+  const int lanes = c.N <= c.B                                                     ? 8
+                    : (each >= 12 && blocks < 512) || (each >= 32 && blocks < 2048) ? 128
+                    : c.N <= 4 * static_cast<int64_t>(c.B) && blocks >= 2048        ? 8
+                                                                                    : 32;
   if (c.D == 64) return lanes == 8 ? launch<64, 8>(p, s) : lanes == 32 ? launch<64, 32>(p, s) : launch<64, 128>(p, s);
   return lanes == 8 ? launch<128, 8>(p, s) : lanes == 32 ? launch<128, 32>(p, s) : launch<128, 128>(p, s);
 }

@@ -82,6 +82,13 @@ APPENDS = [
     (128, 64, 1, 2, 128, False, [(10, 15), (60, 20), (0, 12)]),
     (64, 32, 3, 3, 64, True, [(31, 13), (1, 30), (0, 64)]),
     (64, 64, 2, 1, 32, False, [(7, 130)]),
+    (64, 16, 64, 1, 64, False, [(15, 3), (0, 0), (16, 1), (5, 11), (31, 2), (14, 5)] * 3),   # few tokens, many heads
+    (128, 16, 60, 1, 32, True, [(15, 3), (9, 9), (16, 1), (0, 1), (31, 2), (14, 5)] * 3),
+    (64, 16, 2, 2, 64, False, [(9, 90), (0, 17), (30, 3)]),
+    (64, 128, 3, 2, 64, True, [(9, 90), (100, 40)]),
+    (128, 16, 4, 2, 128, False, [(3, 20), (0, 0), (16, 1), (0, 33), (7, 0), (15, 2)]),   # a warp a block
+    (128, 128, 2, 3, 64, True, [(100, 60), (0, 3), (5, 2), (127, 1), (3, 9), (0, 1), (1, 2), (8, 1), (60, 1)]),
+    (64, 64, 3, 1, 32, False, [(60, 60), (0, 3), (5, 2), (127, 1), (3, 9), (0, 1), (1, 2), (8, 1), (60, 1)]),
 ]
 
 

@@ -247,6 +247,7 @@ struct KVAttentionParams {
   const uint16_t* q;
   int64_t q_stride;
   int QH, G;             // G = QH / KH query heads share a cache head
+  uint32_t g_inverse;    // ceil(2^31 / G)
   float scale_log2;      // scale * log2(e)
   int window;
   uint16_t* out;

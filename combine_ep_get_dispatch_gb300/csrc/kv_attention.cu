@@ -32,7 +32,11 @@
 // drafted each: 75 us without). In a block, one warp
 // loads (pages, scales, descriptors of what comes), four compute: kRW of them
 // hold 8 kNT rows each, 4 / kRW groups take turns with the chunks and are joined
-// at the end of a unit. A unit that several blocks share is joined by the last
+// at the end of a unit. A unit of few chunks is one group's alone, while the others
+// take the next ones: its cost is the latency of its steps (queries 1500 cycles, a
+// chunk 1650, joining 1000, results 1100), not their work. 8 heads of 64 tokens x 200
+// sequences 24.0 us together, 17.7 alone; 16 heads of 150 tokens (5 chunks) 49.6 and
+// 42.0; 8 heads of 200 tokens (7 chunks) 33.5 and 36.0. A unit that several blocks share is joined by the last
 // of them to finish, in the order of its chunks, so results do not depend on
 // which one that was.
 //
@@ -60,7 +64,8 @@ constexpr int kComputeRegs = 216, kLoadRegs = 40;  // of the 2 x 128 a thread pa
 constexpr int kMaxBlocks = 320;  // blocks a workspace has room for
 constexpr int kFan = 8;          // parts of a shared unit that one block joins at once
 constexpr int kUnitCost = 6;     // chunks that a unit costs besides its own: queries, joining, results
-constexpr int kUnits = 4;        // units whose descriptors are in flight
+constexpr int kUnits = 8;        // units whose descriptors are in flight
+constexpr int kSolo = 5;         // most chunks of a unit that one group of warps takes alone
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTop = 15.0f;    // the largest weight enters the products as 2^15
 
@@ -83,6 +88,7 @@ struct ChunkHeader {
 struct Unit {
   int b, h, rt;      // sequence, cache head, row tile
   int t0, n;         // its tokens in the call
+  int tok0, head0;   // token and head (of the cache head's) of the tile's first row
   int len;           // sequence length
   int first;         // first token of chunk 0
   int c0, c1, total; // chunks [c0, c1) of `total`
@@ -330,6 +336,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
       d.b = b;
       d.rt = u % s.tiles;  // row tiles of a head follow one another: its cache comes from L2 after the first
       d.h = u / s.tiles;
+      d.tok0 = d.rt * kRows / p.G;
+      d.head0 = d.rt * kRows - d.tok0 * p.G;
       d.t0 = s.t0;
       d.n = s.n;
       d.len = s.len;
@@ -476,13 +484,24 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
     const Unit d = sh.unit[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.unit_empty[slot]);
+    // Few chunks: one group's work, while the others take the next units. (A warp
+    // has left a unit before it waits for another: that one's descriptor may
+    // only come once the other groups have consumed units in between, and they
+    // might stand at this unit's barriers.)
+    const bool whole = d.c0 == 0 && d.c1 == d.total;
+    const bool solo = kTW > 1 && whole && d.total <= kSolo;
+    if (solo && un % kTW != tw) continue;
 
     // This warp's rows. As columns of the score products: lane (g, j) holds
     // row 8 t + g of column tile t, channels of quad j; of the results it gets
     // rows 8 t + 2j and 8 t + 2j + 1.
     const int rows = min(kRows, d.n * p.G - d.rt * kRows);  // of the tile
     const int row_base = rw * 8 * kNT;
-    auto token_of = [&](int row) { return (d.rt * kRows + row) / p.G; };
+    // Row -> token and head: a division of at most 4096 + 64 by G, by its reciprocal,
+    // which is exact in this range (with divisions 79 sequences of up to 31 tokens,
+    // 48 rows each, took 16.0 us, now 13.8).
+    auto over_g = [&](int x) { return static_cast<int>(__umulhi(2u * static_cast<unsigned>(x), p.g_inverse)); };
+    auto token_of = [&](int row) { return d.tok0 + over_g(d.head0 + row); };
     auto position = [&](int row) { return row < rows ? d.len - d.n + token_of(row) : -1; };  // -1: no such row
     uint32_t qb[kNT][kSteps][2];
     float qf[kNT][2];   // score factors: scale log2(e) times the power of two taken from q
@@ -490,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
       const int row = row_base + 8 * t + g;
-      const int gr = d.rt * kRows + row;
-      const int i = gr / p.G, head = d.h * p.G + gr % p.G;
+      const int x0 = d.head0 + row, y0 = over_g(x0);
+      const int i = d.tok0 + y0, head = d.h * p.G + x0 - y0 * p.G;
       const bool live = row < rows;
       constexpr int kMineCh = kD / 4;  // channels of a lane
       uint4 raw[kMineCh / 8];
@@ -543,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
     int e0 = 0;
     bool started = false;
 
-    for (int it = d.it + tw; it < d.it + d.c1 - d.c0; it += kTW) {  // the groups take turns
+    for (int it = d.it + (solo ? 0 : tw); it < d.it + d.c1 - d.c0; it += solo ? 1 : kTW) {  // the groups take turns
       const int stage = it % kStages;
       // (A wait that gives up leaves wrong results and says so; the warp stays
       // for the barriers below, and the loading warp ends the work.)
@@ -725,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
     // Half of the groups hands over to the other half, until one is left.
 #pragma unroll
     for (int half = kTW / 2; half >= 1; half /= 2) {
+      if (solo) break;
       compute_sync();  // what was handed over before has been read
       if (tw >= half && tw < 2 * half) {
         const int w = (tw - half) * kRW + rw;
@@ -767,13 +787,12 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
       }
     }
     auto out_of = [&](int row) {  // (token, head) of a row of the tile
-      const int gr = d.rt * kRows + row;
-      return static_cast<int64_t>(d.t0 + gr / p.G) * p.QH + d.h * p.G + gr % p.G;
+      const int x = d.head0 + row, y = over_g(x);
+      return static_cast<int64_t>(d.t0 + d.tok0 + y) * p.QH + d.h * p.G + x - y * p.G;
     };
-    const bool whole = d.c0 == 0 && d.c1 == d.total;
     // Lane (g, j) holds rows 8 t + 2j and + 1, channels [g kD / 8, (g + 1) kD / 8).
     if (whole) {
-      if (tw == 0) {
+      if (solo || tw == 0) {
 #pragma unroll
         for (int t = 0; t < kNT; ++t)
 #pragma unroll
@@ -975,8 +994,10 @@ size_t kv_attention_ws_bytes(int N, int QH, int KH, int D) {
   return 4096 + sizeof(float) * kMaxBlocks * 2 * rows * static_cast<size_t>(D + 4);
 }
 
-cudaError_t launch_kv_attention(const KVAttentionParams& p, cudaStream_t s) {
+cudaError_t launch_kv_attention(const KVAttentionParams& in, cudaStream_t s) {
+  KVAttentionParams p = in;
   if (p.c.N <= 0) return cudaSuccess;
+  p.g_inverse = ((1u << 31) + p.G - 1) / p.G;
   const int64_t each = (static_cast<int64_t>(p.c.N) + p.c.B - 1) / p.c.B;  // new tokens a sequence
   const int rows = tile_rows_for(each * p.G);
   return p.c.D == 64 ? launch_rows<64>(p, rows, s) : launch_rows<128>(p, rows, s);

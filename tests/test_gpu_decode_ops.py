@@ -293,6 +293,21 @@ def test_attention(D, P, KH, QH, seqs, window):
     assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("D,P,KH,G,n,window", [(64, 16, 16, 1, 1, 0), (128, 64, 16, 1, 1, 0), (64, 32, 16, 8, 2, 0),
+                                               (128, 32, 8, 8, 4, 70), (64, 128, 8, 12, 5, 0)])
+def test_attention_of_many_short_sequences(D, P, KH, G, n, window):
+    """Several units a block, of one chunk of tokens to ten, in any order."""
+    rng = np.random.default_rng(D + P + n)
+    seqs = 96 if n == 1 else 40 if n == 2 else 20
+    lens = [int(x) for x in np.floor(np.exp(rng.uniform(0, np.log(330), seqs)))]
+    c = random_cache(rng, lens, P, KH, D)
+    q = bf16(rng.normal(size=(seqs * n, KH * G, D))).cuda()
+    cu = np.arange(seqs + 1) * n
+    out, lse = ep.kv_attention(q, device_cache(c), to_dev(np.array(lens, np.int32)), cu_tokens=to_dev(cu.astype(np.int32)),
+                               scale=0.1, window=window, return_lse=True)
+    check_attention(c, lens, cu, f64(q), 0.1, window, out, lse)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
 def test_attention_scales(scale):
     rng = np.random.default_rng(8)

@@ -11,6 +11,7 @@
 // shared-memory limit call inside it (see ensure_dynamic_smem).
 #include <map>
 #include <mutex>
+#include <set>
 #include <tuple>
 
 #include "kernels.cuh"
@@ -78,6 +79,16 @@ cudaError_t ensure_dynamic_smem(const void* fn, int dev, size_t smem) {
   if (err != cudaSuccess) return err;
   v = smem;
   return cudaSuccess;
+}
+
+cudaError_t prefer_shared(const void* fn, int dev) {
+  static std::set<std::pair<const void*, int>> done;  // guarded by g_mutex
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (done.count({fn, dev})) return cudaSuccess;
+  const cudaError_t err =
+      cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (err == cudaSuccess) done.insert({fn, dev});
+  return err;
 }
 
 int blocks_per_sm(const void* fn, int dev, int threads, size_t smem) {

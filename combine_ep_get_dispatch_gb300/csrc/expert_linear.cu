@@ -117,8 +117,8 @@ struct Tables {
 constexpr size_t table_bytes(int E) { return sizeof(int) * (3 * static_cast<size_t>(E) + 2); }
 
 struct Scan {
-  long long row_sum[kThreads / 32];
-  int slot_sum[kThreads / 32], tile_sum[kThreads / 32];
+  long long rows[kThreads / 32];
+  unsigned long long both[kThreads / 32];  // slots << 32 | tiles
 };
 
 // Counts -> tiles, by a whole block of kThreads; ends with a block barrier.
@@ -135,34 +135,59 @@ __device__ void tile_experts(const Params& q, Scan& sc, const Tables& tb) {
     mine[i] = e0 + i < e1 ? rows_of(p, e0 + i, __ldg(p.count + e0 + i), first) : 0;
     rows += mine[i];
   }
-  auto scan = [&](auto v, auto* sums) {  // exclusive over the block
-    auto s = v;
+  // One scan of rows, slots and tiles at once. If there are more rows than
+  // max_rows, what is over is taken off and the rest scanned again. (Rows are
+  // counted in 64 bits; up to max_rows, slots and tiles fit 27.)
+  unsigned long long both = 0;
+  long long used = 0;
+  for (bool capped = false;; capped = true) {
+    unsigned long long of_mine = 0;
+#pragma unroll
+    for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i)
+      of_mine += static_cast<unsigned long long>(static_cast<unsigned>(round8(mine[i]))) << 32 |
+                 static_cast<unsigned>((mine[i] + q.tile_rows - 1) / q.tile_rows);
+    used = rows;
+    both = of_mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const auto u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
+      const long long u = __shfl_up_sync(0xffffffffu, used, o);
+      const unsigned long long t = __shfl_up_sync(0xffffffffu, both, o);
+      if (lane >= o) {
+        used += u;
+        both += t;
+      }
     }
-    if (lane == 31) sums[w] = s;
+    if (lane == 31) {
+      sc.rows[w] = used;
+      sc.both[w] = both;
+    }
     __syncthreads();
-    auto before = s - v;
-    for (int i = 0; i < w; ++i) before += sums[i];
-    return before;
-  };
-  // Rows are counted in 64 bits up to max_rows; what is left of them fits 27.
-  long long used = scan(rows, sc.row_sum);
-  int slots = 0, tiles = 0;
+    used -= rows;
+    both -= of_mine;
+    long long all = 0;
 #pragma unroll
-  for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i) {
-    const long long left = used < p.max_rows ? p.max_rows - used : 0;
-    used += mine[i];
-    if (mine[i] > left) {
-      mine[i] = static_cast<int>(left);
-      flag(p.status, EP_ST_CAPACITY);
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < w) {
+        used += sc.rows[i];
+        both += sc.both[i];
+      }
+      all += sc.rows[i];
     }
-    slots += round8(mine[i]);
-    tiles += (mine[i] + q.tile_rows - 1) / q.tile_rows;
+    if (capped || all <= p.max_rows) break;
+    rows = 0;
+#pragma unroll
+    for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i) {
+      const long long left = used < p.max_rows ? p.max_rows - used : 0;
+      used += mine[i];
+      if (mine[i] > left) {
+        mine[i] = static_cast<int>(left);
+        flag(p.status, EP_ST_CAPACITY);
+      }
+      rows += mine[i];
+    }
+    __syncthreads();  // the sums have been read
   }
-  int s0 = scan(slots, sc.slot_sum), t0 = scan(tiles, sc.tile_sum);
+  int s0 = static_cast<int>(both >> 32), t0 = static_cast<int>(both & 0xFFFFFFFFu);
 #pragma unroll
   for (int i = 0; i < EP_MAX_EXPERTS / kThreads; ++i) {
     if (e0 + i < e1) {

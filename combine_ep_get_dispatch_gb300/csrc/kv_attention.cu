@@ -27,7 +27,7 @@
 // Work: the rows of one (sequence, cache head), up to 8 kNT kRW of them, are a
 // unit of chunks of 32 tokens. The blocks take equal runs of consecutive
 // places over all units, whatever the sequences' lengths; a unit has a place
-// for each chunk and kUnitCost more in front, so that a block with many short
+// for each chunk and unit_cost more in front, so that a block with many short
 // sequences is not the last to finish (24 sequences of 4 to 30011 tokens, 4
 // drafted each: 75 us without). In a block, one warp
 // loads (pages, scales, descriptors of what comes), four compute: kRW of them
@@ -63,7 +63,12 @@ constexpr int kComputeRegs = 216, kLoadRegs = 40;  // of the 2 x 128 a thread pa
                                                    // for 128 x 8192 tokens: nothing spills)
 constexpr int kMaxBlocks = 320;  // blocks a workspace has room for
 constexpr int kFan = 8;          // parts of a shared unit that one block joins at once
-constexpr int kUnitCost = 6;     // chunks that a unit costs besides its own: queries, joining, results
+// Chunks that a unit costs besides its own: queries, joining, results. Chunks of
+// 64 rows cost more themselves: in us with 6 / 4 / 3 / 2, 60 sequences of up to 3000
+// tokens, 8 drafted, 8 heads of 64: 42.2 / 40.5 / 38.6 / 40.2, 30 of 300: 23.1 / 23.2 /
+// 24.0 / 24.0, 20 of up to 20000, 5 drafted: 57.0 / 56.5 / 56.6 / 55.6. With 32 rows and
+// fewer it depends on the lengths alone (6 / 4: 49.4 / 47.3, 24.3 / 24.7, 37.3 / 38.4).
+constexpr int unit_cost(int row_warps) { return row_warps < 4 ? 6 : 4; }
 constexpr int kUnits = 8;        // units whose descriptors are in flight
 constexpr int kSolo = 5;         // most chunks of a unit that one group of warps takes alone
 constexpr float kLn2 = 0.6931471805599453f;
@@ -103,8 +108,8 @@ struct Sequence {
   int chunks;  // of each of its units
   int tiles;   // row tiles
   bool ok;
-  __device__ __forceinline__ int places() const { return chunks + kUnitCost; }  // of a unit
-  __device__ __forceinline__ int64_t all(int heads) const { return static_cast<int64_t>(places()) * tiles * heads; }
+  __device__ __forceinline__ int places(int cost) const { return chunks + cost; }  // of a unit
+  __device__ __forceinline__ int64_t all(int heads, int cost) const { return static_cast<int64_t>(places(cost)) * tiles * heads; }
 };
 
 template <int kD, int kNT, int kRW>
@@ -217,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
     kv_attention_kernel(const KVAttentionParams p, float* partial, unsigned* counters,
                         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   constexpr int kTW = kWarps / kRW;
+  constexpr int kUnitCost = unit_cost(kRW);
   using S = Shape<kD, kNT>;
   constexpr int kRows = 8 * kNT * kRW;
   constexpr int kStages = S::kStages;
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
   const int64_t cap = static_cast<int64_t>(c.MP) * c.P;
   for (int b = b0; b < b1; ++b) {
     const Sequence s = sequence_at(p, b, kRows);
-    mine += s.all(c.KH);
+    mine += s.all(c.KH, kUnitCost);
     if (!s.ok) sh.bad = 1;
     if (blockIdx.x == 0) {
       if (!s.ok) flag(c.status, EP_ST_BAD_INDEX);
@@ -283,13 +289,13 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
     long long at = before;
     for (int b = b0; b < b1; ++b) {
       const Sequence s = sequence_at(p, b, kRows);
-      if (begin < at + s.all(c.KH)) {
+      if (begin < at + s.all(c.KH, kUnitCost)) {
         sh.find_b = b;
         sh.find_at = at;
         sh.find = s;
         break;
       }
-      at += s.all(c.KH);
+      at += s.all(c.KH, kUnitCost);
     }
   }
   if (sh.bad) {
@@ -322,14 +328,14 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
     bool ok = true;
     while (ok && at < end) {
       // The unit that holds place `at`.
-      while (at >= seq_at + s.all(c.KH)) {
-        seq_at += s.all(c.KH);
+      while (at >= seq_at + s.all(c.KH, kUnitCost)) {
+        seq_at += s.all(c.KH, kUnitCost);
         s = sequence_at(p, ++b, kRows);
       }
-      const int u = static_cast<int>((at - seq_at) / s.places());
-      const int64_t unit_at = seq_at + static_cast<int64_t>(u) * s.places();
+      const int u = static_cast<int>((at - seq_at) / s.places(kUnitCost));
+      const int64_t unit_at = seq_at + static_cast<int64_t>(u) * s.places(kUnitCost);
       const int from = max(0, static_cast<int>(at - unit_at) - kUnitCost);
-      at = min(end, unit_at + s.places());
+      at = min(end, unit_at + s.places(kUnitCost));
       const int upto = static_cast<int>(at - unit_at) - kUnitCost;
       if (upto <= from) continue;  // only places in front of its chunks
       Unit d;
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
       d.first = s.first;
       d.total = s.chunks;
       d.first_block = owner_of(total, blocks, unit_at + kUnitCost);
-      d.last_block = owner_of(total, blocks, unit_at + s.places() - 1);
+      d.last_block = owner_of(total, blocks, unit_at + s.places(kUnitCost) - 1);
       d.c0 = from;
       d.c1 = upto;
       d.it = it;

@@ -785,7 +785,12 @@ def low_latency_clean_mask_buffer(handle, num_ranks: Optional[int] = None, strea
 # ------------------------------------- the decode step around the dispatch ----
 @dataclasses.dataclass
 class KVCache:
-    """A paged key/value cache in E4M3 with a power-of-two scale per (page, head)."""
+    """A paged key/value cache in E4M3 with a power-of-two scale per (page, head).
+
+    An array may be replaced (cache.page_table = larger_table): the next call
+    uses the new one. An array's values may change at any time on the stream;
+    its storage must not (resize_, set_).
+    """
     k: torch.Tensor           # [num_pages, num_heads, page_size, head_dim] uint8 (E4M3)
     v: torch.Tensor
     k_scale: torch.Tensor     # [num_pages, num_heads] fp32
@@ -793,9 +798,19 @@ class KVCache:
     page_table: torch.Tensor  # [num_seqs, max_pages] int32
     _c: Optional[ep_kv_cache_t] = dataclasses.field(default=None, init=False, repr=False, compare=False)
 
+    def __setattr__(self, name, value) -> None:
+        object.__setattr__(self, name, value)
+        if name in _KV_ARRAYS:  # the handle names the array that was there before
+            object.__setattr__(self, "_c", None)
+
+    def __getstate__(self) -> dict:
+        """A copy builds a handle of its own."""
+        return {name: getattr(self, name) for name in _KV_ARRAYS} | {"_c": None}
+
     def c_struct(self) -> ep_kv_cache_t:
-        """The C handle, built once: a cache's arrays are fixed when it is made."""
-        if self._c is None:
+        """The C handle of the arrays, kept until one of them is replaced."""
+        c = self._c
+        if c is None:
             if self.k.dim() != 4 or self.page_table.dim() != 2:
                 raise ValueError("KVCache: k is [pages, heads, page_size, head_dim], page_table [seqs, max_pages]")
             pages, heads, size, dim = self.k.shape
@@ -804,20 +819,30 @@ class KVCache:
                          _address(self.k_scale, "k_scale", torch.float32, (pages, heads)),
                          _address(self.v_scale, "v_scale", torch.float32, (pages, heads)),
                          _address(self.page_table, "page_table", torch.int32))
-            self._c = ep_kv_cache_t(*addresses, pages, heads, size, dim, seqs, most)
-            self.c_ref = ctypes.byref(self._c)
+            c = ep_kv_cache_t(*addresses, pages, heads, size, dim, seqs, most)
+            self.c_ref = ctypes.byref(c)
             self.heads, self.dim = heads, dim
             self.seqs, self.cu_shape = torch.Size((seqs,)), torch.Size((seqs + 1,))
-        return self._c
+            self._c = c  # last: who sees it sees the rest
+        return c
+
+
+_KV_ARRAYS = frozenset(("k", "v", "k_scale", "v_scale", "page_table"))
 
 
 def new_kv_cache(num_pages: int, num_heads: int, page_size: int, head_dim: int, page_table: torch.Tensor) -> KVCache:
-    """An empty cache on page_table's device."""
+    """An empty cache on page_table's device.
+
+    The cache holds page_table itself (int32, contiguous, [num_seqs, max_pages]),
+    so that the caller's later changes to it are seen.
+    """
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
+        raise ValueError("page_table: expected a contiguous int32 tensor [num_seqs, max_pages]")
     dev = page_table.device
     shape = (num_pages, num_heads, page_size, head_dim)
     return KVCache(torch.zeros(shape, dtype=torch.uint8, device=dev), torch.zeros(shape, dtype=torch.uint8, device=dev),
                    torch.zeros(shape[:2], dtype=torch.float32, device=dev),
-                   torch.zeros(shape[:2], dtype=torch.float32, device=dev), page_table.to(torch.int32).contiguous())
+                   torch.zeros(shape[:2], dtype=torch.float32, device=dev), page_table)
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, seq_lens: torch.Tensor,

@@ -179,26 +179,6 @@ cudaError_t launch_kernel(void (*fn)(Params...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, fn, static_cast<Args&&>(args)...);
 }
 
-// The same as a programmatic dependent, in clusters of `cluster` blocks.
-template <typename... Params, typename... Args>
-cudaError_t launch_kernel_cluster(void (*fn)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                                  int cluster, Args&&... args) {
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fn, static_cast<Args&&>(args)...);
-}
-
 // ---- grid-wide barrier (cooperative launches only) --------------------------
 // One barrier per launch over two words that persist across launches: bar[0]
 // counts arrivals and is zero between launches, bar[1] is a generation

@@ -27,14 +27,16 @@
 // where 783 were without: every load passes the same engine).
 //
 // With more rows the blocks' reads of x set the pace: each of an expert's
-// output tiles needs all of its rows. Blocks then work in clusters of
-// neighbouring output tiles, each loads a share of the rows for all.
+// output tiles needs all of its rows, and each block loads them for itself
+// (x may lie in any memory that the device can read, so no load serves several
+// blocks at once). At 128 rows that is 15 GB of rows beside 8 GB of weights and
+// scales, 12.5 TB/s out of L2.
 //
 // Measured (256 experts, 7168 inputs, 2 x 2048 gated outputs; copy rate 6.69
-// TB/s): 4 BF16 rows an expert 672 us, 5.9 TB/s; 128 E4M3 rows 1182 us, 3.7
-// TB/s and 1.6 PFLOP/s; one token's eight experts 35 us, of which 10 pass before
-// the first weights have come and 4 after the last; 2048 inputs, 7168 outputs, 4
-// BF16 rows an expert 328 us, 6.0 TB/s.
+// TB/s): 4 BF16 rows an expert 698 us, 5.6 TB/s; 128 E4M3 rows 1839 us, 2.4
+// TB/s of what must be read and 1.05 PFLOP/s; one token's eight experts 35 us, of
+// which 10 pass before the first weights have come and 4 after the last; 2048
+// inputs, 7168 outputs, 4 BF16 rows an expert 325 us, 6.1 TB/s.
 //
 // Two launches: expert_rows_kernel splits BF16 rows into the tensor cores'
 // shared-memory layout (of E4M3 rows it lays out the scales; their codes come
@@ -55,9 +57,9 @@ constexpr int kTileM = 128;                 // outputs a unit (with GLU: 64 gate
 constexpr int kTileBytes = kTileM * kStep;  // weights of a step in shared memory (8-bit containers)
 constexpr int kTileTx = kTileBytes / 2;     // ... and as TMA counts them
 constexpr int kMaxSteps = 2;                // most steps a stage holds
-constexpr int kRowMaps = 12;                // boxes of 8, 16 .. 96 rows
 constexpr int kScaleBytes = 512;            // scale bytes of 128 rows for one step
 constexpr int kMaxCols = 192;
+constexpr int kRowMaps = kMaxCols / 8;      // boxes of 8, 16 .. kMaxCols rows
 constexpr int kMaxBlocks = 160;             // blocks a workspace has room for
 constexpr int kThreads = 256;
 constexpr int kMaxStages = 12;
@@ -75,7 +77,7 @@ struct Params {
   int KB;           // steps of a unit: K / 128
   int steps;        // of a stage, 1 or 2
   int KS;           // stages of a unit; the last one may hold one step of two
-  int MT;           // units of a tile: an expert's output tiles, a cluster's blocks taking one each
+  int MT;           // units of a tile: an expert's output tiles
   int stages;
   unsigned stage_bytes;
   int scale_bytes;     // of a step's rows: 512 for each 128 columns that a tile can have
@@ -345,19 +347,6 @@ __global__ void __launch_bounds__(kThreads) expert_rows_kernel(const Params q) {
 }
 
 // ---- the products ------------------------------------------------------------------
-// E4M3 rows come straight from x, each block of the cluster loading a box of
-// this many, so a stage holds up to 8 kC - 8 columns more than the tile's.
-template <int kC>
-__device__ __forceinline__ int row_share(int cols) {
-  return round8((cols + kC - 1) / kC);
-}
-template <bool kFp8, int kC>
-__device__ __forceinline__ unsigned loaded_cols(int cols) {
-  if (!kFp8) return cols;
-  const int share = row_share<kC>(cols);
-  return (cols + share - 1) / share * share;
-}
-
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t scale_full[kScaleGroups], scale_empty[kScaleGroups];
@@ -370,7 +359,7 @@ struct Shared {
 
 // A run of steps of one unit.
 struct Segment {
-  int e, tile, mt;  // mt: of this block
+  int e, tile, mt;
   int s0, s1;     // stages
   int cols;       // columns of its tile
   int rows;       // rows of its tile
@@ -413,7 +402,7 @@ __device__ __forceinline__ int owner_of(int64_t total, int blocks, int64_t i) {
 // outputs) follow one another, so that its weights come from L2 after the first.
 // (Each role passes here between two units: with divisions and a search each
 // time the products of 2048 inputs, eight stages a unit, took 366 us, now 330.)
-__device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, int cluster, int rank, Run& run, Segment& s) {
+__device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, Run& run, Segment& s) {
   if (run.at >= run.end) return false;
   const int E = q.p.E;
   if (run.e < 0) {
@@ -451,7 +440,7 @@ __device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, 
   s.slot0 = uniform(tb.slot0[run.e]);
   s.tile0 = run.tile0;
   s.tile = run.tile;
-  s.mt = run.mt * cluster + rank;
+  s.mt = run.mt;
   s.rows = min(q.tile_rows, uniform(tb.rows[run.e]) - s.tile * q.tile_rows);
   s.cols = round8(s.rows) * q.mult;
   return true;
@@ -477,9 +466,8 @@ struct RowMaps {
   CUtensorMap box[kRowMaps];
 };
 
-// kFp8: x in E4M3. kC: blocks of a cluster.
-// kSteps: steps of a stage.
-template <bool kFp8, int kC, int kSteps>
+// kFp8: x in E4M3. kSteps: steps of a stage.
+template <bool kFp8, int kSteps>
 __global__ void __launch_bounds__(kThreads)
     expert_linear_kernel(const Params q, const __grid_constant__ CUtensorMap map,
                          const __grid_constant__ RowMaps maps) {
@@ -493,7 +481,7 @@ __global__ void __launch_bounds__(kThreads)
   if (tid == 0) {
     for (int i = 0; i < q.stages; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], kC);  // every block has used what its peers load for it
+      mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < kScaleGroups; ++i) {
       mbar_init(&sh.scale_full[i], 1);
@@ -516,14 +504,10 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t total = static_cast<int64_t>(uniform(tb.tile0[p.E])) * q.MT * q.KS;
   const int outs = p.glu ? p.M / 2 : p.M;
   // Every block that takes part has steps: the join counts on it.
-  const int rank = kC > 1 ? static_cast<int>(uniform(cluster_rank())) : 0;
-  const int me = static_cast<int>(blockIdx.x) / kC;  // the cluster's number
-  const int blocks =  // clusters
-      static_cast<int>(min(static_cast<int64_t>(gridDim.x / kC), max(total / kMinStages, int64_t{1})));
-  constexpr uint16_t kAll = static_cast<uint16_t>((1u << kC) - 1u);
+  const int me = static_cast<int>(blockIdx.x);
+  const int blocks = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(total / kMinStages, int64_t{1})));
   Run run{0, 0};
   if (me < blocks) run = Run{run_begin(total, blocks, me), run_begin(total, blocks, me + 1)};
-  if (kC > 1) cluster_sync();  // barriers are set up before a peer's load arrives
   // A stage: weights, rows, the rows' scales. Behind the stages: the ring of
   // the weights' scales.
   constexpr unsigned x_at = kSteps * kTileBytes;
@@ -541,13 +525,13 @@ __global__ void __launch_bounds__(kThreads)
       tma_load_5d(smem + r.offset, &map, 0, out_row(g.mt, 0), 0, st * kSteps, g.e, bar);
     };
     auto steps_of = [&](int st) { return static_cast<unsigned>(min(kSteps, q.KB - st * kSteps)); };
-    // Bytes of a step's rows, and of what this cluster's blocks load of them.
-    auto step_bytes = [&](const Segment& g) { return loaded_cols<kFp8, kC>(g.cols) * kStep + q.scale_bytes; };
+    // Bytes of a step's rows: codes and scales.
+    auto step_bytes = [&](const Segment& g) { return static_cast<unsigned>(g.cols) * kStep + q.scale_bytes; };
     const Run start = run;
     Segment g;
     Ring r;
     int ahead = 0;
-    while (ahead < q.stages && next_segment(q, tb, kC, rank, run, g)) {
+    while (ahead < q.stages && next_segment(q, tb, run, g)) {
       for (int st = g.s0; st < g.s1 && ahead < q.stages; ++st, ++ahead) {
         if (elect_one()) load_w(g, st, kSteps * kTileTx + steps_of(st) * step_bytes(g), r);
         r.advance(q);
@@ -559,17 +543,14 @@ __global__ void __launch_bounds__(kThreads)
     unsigned round = 0;  // passes over the ring
     unsigned empty = 0;  // asked a stage ahead
     bool ok = true;
-    while (ok && next_segment(q, tb, kC, rank, run, g)) {
+    while (ok && next_segment(q, tb, run, g)) {
       const unsigned step = step_bytes(g), xcodes = step - q.scale_bytes;
       const unsigned image_step = kFp8 ? q.scale_bytes : step;
       const uint8_t* x =
           q.image + image_at(q, g.slot0, g.tile0, g.tile) + static_cast<int64_t>(g.s0) * kSteps * image_step;
-      // E4M3: this block's share of the rows, one box a step.
-      const int share = row_share<kC>(g.cols);
-      const int row = static_cast<int>(uniform(first_row(p, g.e))) + g.tile * q.tile_rows + rank * share;
-      const bool mine = rank * share < g.cols;
-      const CUtensorMap* box = &maps.box[share / 8 - 1];
-      const unsigned share_at = x_at + rank * share * kStep;
+      // E4M3 rows come straight from x, one box a step.
+      const int row = static_cast<int>(uniform(first_row(p, g.e))) + g.tile * q.tile_rows;
+      const CUtensorMap* box = &maps.box[g.cols / 8 - 1];
       for (int st = g.s0; st < g.s1; ++st) {
         const bool loaded = ahead > 0;
         if (loaded) {
@@ -589,21 +570,11 @@ __global__ void __launch_bounds__(kThreads)
           uint8_t* to = smem + at.offset;
           if (kFp8) {
             bulk_g2s(to + x_at + steps * xcodes, x, steps * q.scale_bytes, bar);
-            if (mine) {
 #pragma unroll
-              for (int h = 0; h < kSteps; ++h) {
-                if (h == steps) break;
-                const int k = (st * kSteps + h) * kStep;
-                if (kC == 1) tma_load_2d(to + share_at + h * xcodes, box, k, row, bar);
-                else tma_load_2d_cluster(to + share_at + h * xcodes, box, k, row, bar, kAll);
-              }
-            }
-          } else if (kC == 1) {
-            bulk_g2s(to + x_at, x, steps * step, bar);
+            for (int h = 0; h < kSteps; ++h)
+              if (h < steps) tma_load_2d(to + x_at + h * xcodes, box, (st * kSteps + h) * kStep, row, bar);
           } else {
-            const unsigned bytes = steps * step, part = (bytes / kC + 127) & ~127u, from = min(bytes, rank * part);
-            const unsigned n = min(part, bytes - from);
-            if (n > 0) bulk_g2s_cluster(to + x_at + from, x + from, n, bar, kAll);
+            bulk_g2s(to + x_at, x, steps * step, bar);
           }
         }
         __syncwarp();
@@ -627,14 +598,14 @@ __global__ void __launch_bounds__(kThreads)
     // What the next stage needs is looked for before this one's products are
     // issued, so that the look costs no time between them.
     unsigned full = 0, scales = 0;
-    while (ok && next_segment(q, tb, kC, rank, run, g)) {
+    while (ok && next_segment(q, tb, run, g)) {
       const int buf = seg & 1;
       if (seg >= 2 && !mbar_wait_warp(&sh.acc_empty[buf], (seg / 2 - 1) & 1, p.status)) break;
       tmem_fence_after();
       const uint32_t d = tmem + buf * kMaxCols;
       const uint32_t idesc = idesc_e2m1_e4m3(g.cols);
       const bool wide = kSteps == 1 && g.cols > 128;
-      const unsigned x_step = loaded_cols<kFp8, kC>(g.cols) * kStep >> 4, xs_step = q.scale_bytes >> 4;
+      const unsigned x_step = static_cast<unsigned>(g.cols) * kStep >> 4, xs_step = q.scale_bytes >> 4;
       for (int st = g.s0; st < g.s1; ++st) {
         const int kb = st * kSteps;
         const bool group_start = st == g.s0 || (kb & 3) == 0;
@@ -674,8 +645,7 @@ __global__ void __launch_bounds__(kThreads)
         if (elect_one()) {
           step(0, st > g.s0);
           if (both) step(1, true);
-          if (kC == 1) mma_commit(&sh.empty[stage]);
-          else mma_commit_cluster(&sh.empty[stage], kAll);
+          mma_commit(&sh.empty[stage]);
           if (group_end) mma_commit(&sh.scale_empty[this_group]);
           if (last) mma_commit(&sh.acc_full[buf]);
         }
@@ -698,13 +668,13 @@ __global__ void __launch_bounds__(kThreads)
     int lo[kAhead], hi[kAhead];
     Segment g;
     int next = 0;
-    bool more = next_segment(q, tb, kC, rank, run, g);
+    bool more = next_segment(q, tb, run, g);
     if (more) next = g.s0 * kSteps;
     auto advance = [&]() {  // to the next group
       if (!more) return;
       next = (next & ~3) + 4;
       if (next >= min(q.KB, g.s1 * kSteps)) {
-        more = next_segment(q, tb, kC, rank, run, g);
+        more = next_segment(q, tb, run, g);
         if (more) next = g.s0 * kSteps;
       }
     };
@@ -768,7 +738,7 @@ __global__ void __launch_bounds__(kThreads)
     grid_dependency_wait();
     Segment g;
     int seg = 0;
-    while (next_segment(q, tb, kC, rank, run, g)) {
+    while (next_segment(q, tb, run, g)) {
       const int buf = seg & 1;
       if (!epilogue_all(mbar_wait(&sh.acc_full[buf], (seg / 2) & 1, p.status))) break;
       ++seg;
@@ -779,7 +749,7 @@ __global__ void __launch_bounds__(kThreads)
       const int64_t row0 = first_row(p, g.e) + g.tile * q.tile_rows;
       const int o = p.glu ? g.mt * 64 + (m & 63) : g.mt * kTileM + m;
       auto slot = [&](int block, bool starts) {
-        return q.partial + ((static_cast<int64_t>(block) * kC + rank) * 2 + (starts ? 1 : 0)) * q.tile_rows * kTileM;
+        return q.partial + (static_cast<int64_t>(block) * 2 + (starts ? 1 : 0)) * q.tile_rows * kTileM;
       };
       // Eight finished sums of this thread's output row: to y.
       auto finish = [&](float* v, int c0) {
@@ -831,7 +801,7 @@ __global__ void __launch_bounds__(kThreads)
       const int c_last = owner_of(total, blocks, (g.unit + 1) * q.KS - 1);
       epilogue_sync();
       if (m == 0) {
-        unsigned* counter = q.counters + c_first * kC + rank;
+        unsigned* counter = q.counters + c_first;
         __threadfence();  // the block's writes, which the barrier has ordered before it
         const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(c_last - c_first);
         if (last) *counter = 0u;
@@ -862,7 +832,6 @@ __global__ void __launch_bounds__(kThreads)
     tmem_fence_after();
     tmem_free(tmem, kTmemCols);
   }
-  if (kC > 1) cluster_sync();  // no block leaves while a peer may still arrive on its barriers
 }
 
 // Rows of a full tile: enough for nearly every expert's rows in one tile (the
@@ -880,20 +849,13 @@ int tile_rows_for(int E, int64_t max_rows, int mult) {
   return kMaxCols / mult;
 }
 
-// Steps of a stage: two halve what a stage costs besides its bytes, unless a
-// tile's rows leave room for too few of them (128 rows an expert: 1477 us with
-// two stages of two steps, 1204 with four of one).
+// Steps of a stage: two halve what a stage costs besides its bytes. With more
+// than 64 columns they are large enough for it not to matter, and one step lets
+// a tile have more than 128. In us with one / two steps, rows an expert (256
+// experts, 7168 inputs, 2 x 2048 gated outputs): 4 BF16 787 / 744, 12 BF16 928 /
+// 920, 4 E4M3 765 / 677, 24 E4M3 853 / 840; of more than 64 columns 24 BF16 1117 /
+// 1122, 40 BF16 1467 / 1464, 48 E4M3 1110 / 1114, 72 E4M3 1333 / 1338.
 int steps_for(int cols) { return cols <= 64 ? 2 : 1; }
-
-// Blocks of a cluster. Sharing the loads of rows pays from two columns tiles
-// of 16 on: 128 tokens x 256 experts 704 us alone, 676 in pairs; 128 rows an
-// expert 1338 in pairs, 1204 in fours, 1326 in eights (of which fewer fit the
-// GPU at once). Not where the last cluster of an expert's `tiles` output tiles
-// would stand idle for a good part.
-int cluster_for(int cols, int tiles) {
-  if (cols <= 64) return cols >= 32 && (tiles % 2 == 0 || tiles >= 8) ? 2 : 1;
-  return tiles % 4 == 0 || tiles >= 16 ? 4 : 2;
-}
 
 struct Sizes {
   int tile_rows;
@@ -920,27 +882,23 @@ Sizes sizes_of(int E, int64_t max_rows, int K, bool fp8) {
 
 namespace {
 
-template <bool kFp8, int kC, int kSteps>
+template <bool kFp8, int kSteps>
 cudaError_t launch_products(const Params& q, const CUtensorMap& map, const RowMaps& maps, size_t smem, int dev, int sms,
                             cudaStream_t s) {
-  const auto kernel = expert_linear_kernel<kFp8, kC, kSteps>;
+  const auto kernel = expert_linear_kernel<kFp8, kSteps>;
   const void* fn = reinterpret_cast<const void*>(kernel);
   const cudaError_t err = ensure_dynamic_smem(fn, dev, smem);
   if (err != cudaSuccess) return err;
-  // One block an SM; of clusters, as many as are resident at once.
-  int grid = std::min(sms, kMaxBlocks);
-  if (kC > 1) grid = std::min(grid / kC, clusters_resident(fn, dev, kThreads, smem, kC, grid)) * kC;
-  if (grid < 1) return cudaErrorInvalidConfiguration;
-  return launch_kernel_cluster(kernel, dim3(grid), dim3(kThreads), smem, s, kC, q, map, maps);
+  // One block an SM.
+  return launch_kernel(kernel, dim3(std::min(sms, kMaxBlocks)), dim3(kThreads), smem, s, /*dependent=*/true, q, map,
+                       maps);
 }
 
 template <bool kFp8>
-cudaError_t launch_cluster(int cluster, const Params& q, const CUtensorMap& map, const RowMaps& maps, size_t smem,
-                           int dev, int sms, cudaStream_t s) {
-  if (cluster == 1) return launch_products<kFp8, 1, 2>(q, map, maps, smem, dev, sms, s);
-  if (q.steps == 2) return launch_products<kFp8, 2, 2>(q, map, maps, smem, dev, sms, s);
-  if (cluster == 2) return launch_products<kFp8, 2, 1>(q, map, maps, smem, dev, sms, s);
-  return launch_products<kFp8, 4, 1>(q, map, maps, smem, dev, sms, s);
+cudaError_t launch_steps(const Params& q, const CUtensorMap& map, const RowMaps& maps, size_t smem, int dev, int sms,
+                         cudaStream_t s) {
+  return q.steps == 2 ? launch_products<kFp8, 2>(q, map, maps, smem, dev, sms, s)
+                      : launch_products<kFp8, 1>(q, map, maps, smem, dev, sms, s);
 }
 
 }  // namespace
@@ -960,8 +918,6 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   q.steps = steps_for(q.cols_cap);
   q.KS = (q.KB + q.steps - 1) / q.steps;
   q.MT = p.glu ? (p.M / 2 + 63) / 64 : (p.M + kTileM - 1) / kTileM;
-  const int cluster = cluster_for(q.cols_cap, q.MT);
-  q.MT = (q.MT + cluster - 1) / cluster;
   q.counters = reinterpret_cast<unsigned*>(p.ws + z.counters);
   q.partial = reinterpret_cast<float*>(p.ws + z.partial);
   q.image = p.ws + z.image;
@@ -995,7 +951,7 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   if (fp8) {
     const cuuint64_t xd[2] = {static_cast<cuuint64_t>(p.K), static_cast<cuuint64_t>(p.x_rows)};
     const cuuint64_t xs[1] = {static_cast<cuuint64_t>(p.K)};
-    for (int i = 0; i < q.cols_cap / cluster / 8; ++i) {
+    for (int i = 0; i < q.cols_cap / 8; ++i) {
       const cuuint32_t b[2] = {kStep, static_cast<cuuint32_t>(8 * (i + 1))};
       if (encode(&maps.box[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p.x), xd, xs, b, ones,
                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1017,8 +973,8 @@ cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s) {
   err = launch_kernel(expert_rows_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(items, 6 * sms))), dim3(kThreads),
                       tables, s, /*dependent=*/true, q);
   if (err != cudaSuccess) return err;
-  return fp8 ? launch_cluster<true>(cluster, q, map, maps, smem, dev, sms, s)
-             : launch_cluster<false>(cluster, q, map, maps, smem, dev, sms, s);
+  return fp8 ? launch_steps<true>(q, map, maps, smem, dev, sms, s)
+             : launch_steps<false>(q, map, maps, smem, dev, sms, s);
 }
 
 }  // namespace ep

@@ -174,8 +174,6 @@ bool device_cooperative(int dev);
 cudaError_t prefer_shared(const void* fn, int dev);  // its SMs keep their shared memory as large as it can be
 cudaError_t ensure_dynamic_smem(const void* fn, int dev, size_t smem);  // raise the kernel's limit to >= smem
 int blocks_per_sm(const void* fn, int dev, int threads, size_t smem);   // occupancy, 0 on failure
-// Clusters of `cluster` blocks that are resident at once, of a grid of at most `blocks`; 0 on failure.
-int clusters_resident(const void* fn, int dev, int threads, size_t smem, int cluster, int blocks);
 
 // The routing layout of ep_get_dispatch_layout: every check first (an error
 // code, with nothing enqueued), then, when reset_barrier is set, a zero fill

@@ -105,31 +105,6 @@ int blocks_per_sm(const void* fn, int dev, int threads, size_t smem) {
   return per_sm;
 }
 
-int clusters_resident(const void* fn, int dev, int threads, size_t smem, int cluster, int blocks) {
-  static std::map<std::tuple<const void*, int, int, size_t, int>, int> known;  // guarded by g_mutex
-  const auto key = std::make_tuple(fn, dev, threads, smem, cluster);
-  {
-    std::lock_guard<std::mutex> lock(g_mutex);
-    const auto it = known.find(key);
-    if (it != known.end()) return it->second;
-  }
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks / cluster * cluster);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lock(g_mutex);
-  known[key] = n;
-  return n;
-}
-
 EncodeTiled encode_tiled() {
   static const EncodeTiled fn = [] {
     void* f = nullptr;

@@ -783,6 +783,9 @@ def low_latency_clean_mask_buffer(handle, num_ranks: Optional[int] = None, strea
 
 
 # ------------------------------------- the decode step around the dispatch ----
+# A call's `stream` (a torch stream or a raw handle; default: torch's current
+# one) runs all of it: what the call makes for itself or returns is made there.
+# Its arguments have to be ready on that stream, and to live until it is done.
 @dataclasses.dataclass
 class KVCache:
     """A paged key/value cache in E4M3 with a power-of-two scale per (page, head).
@@ -845,6 +848,26 @@ def new_kv_cache(num_pages: int, num_heads: int, page_size: int, head_dim: int, 
                    torch.zeros(shape[:2], dtype=torch.float32, device=dev), page_table)
 
 
+def _on_stream(stream, call, *args):
+    """A call with its stream as torch's current one.
+
+    What the call makes and fills is then ordered with its kernels, and memory
+    that it lets go serves that stream first. Its results also count as used
+    by the caller's stream, so that they are not given out again on `stream`
+    while that one still reads them.
+    """
+    s = stream if isinstance(stream, torch.cuda.Stream) else \
+        torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream))
+    caller = torch.cuda.current_stream()
+    with torch.cuda.stream(s):
+        made = call(*args)
+    if s != caller:
+        for t in made if isinstance(made, tuple) else (made,):
+            if t is not None:
+                t.record_stream(caller)
+    return made
+
+
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, seq_lens: torch.Tensor,
               cu_tokens: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None,
               q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
@@ -856,9 +879,11 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, seq_lens: torch.
     rope_dim] fp32 holds cosines, then sines. k, v and q may be slices of one
     fused projection. Returns the rotated queries (q_out, made if not given).
     """
+    if stream is not None:
+        return _on_stream(stream, kv_append, k, v, cache, seq_lens, cu_tokens, rope, q, q_out, interleaved, status)
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ep_kv_append(cache, seq_lens, cu_tokens, k, v, q, q_out, rope, interleaved, status, stream)
+    ep_kv_append(cache, seq_lens, cu_tokens, k, v, q, q_out, rope, interleaved, status)
     return q_out
 
 
@@ -881,13 +906,16 @@ def kv_attention(q: torch.Tensor, cache: KVCache, seq_lens: torch.Tensor, cu_tok
     workspace passed in must have been zero-filled once (kv_attention_workspace
     makes one); without it, one is made. Returns out, or (out, lse).
     """
+    if stream is not None:
+        return _on_stream(stream, kv_attention, q, cache, seq_lens, cu_tokens, scale, window, out, return_lse, workspace,
+                          status)
     if out is None:
         out = torch.empty(q.shape, dtype=_BF16, device=q.device)
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
     if workspace is None:
         workspace = kv_attention_workspace(q, cache)
     ep_kv_attention(cache, seq_lens, cu_tokens, q, q.shape[2] ** -0.5 if scale is None else scale, window, out, lse,
-                    workspace, status, stream)
+                    workspace, status)
     return (out, lse) if return_lse else out
 
 
@@ -917,6 +945,9 @@ def expert_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Ten
     are in out. max_rows bounds the rows received by all experts (default: all
     of x's), and sizes the workspace.
     """
+    if stream is not None:
+        return _on_stream(stream, expert_linear, x, weight, weight_scale, row_count, row_offset, x_scale, glu, out,
+                          max_rows, workspace, status)
     E, M, half = weight.shape
     K = x.shape[-1]
     rows = x.numel() // K
@@ -939,5 +970,5 @@ def expert_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Ten
     if workspace is None:
         workspace = expert_linear_workspace(x, weight, limit)
     ep_expert_linear(x, x_scale, rows, K, row_count, row_offset, x.shape[1] if row_offset is None else 0, limit, weight,
-                     weight_scale, EP_LINEAR_GLU if glu else 0, out, workspace, status, stream)
+                     weight_scale, EP_LINEAR_GLU if glu else 0, out, workspace, status)
     return out

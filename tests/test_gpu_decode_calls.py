@@ -41,3 +41,62 @@ def test_a_replaced_page_table_and_pool_reach_the_next_call():
         assert torch.equal(getattr(cache, name), getattr(whole, name)), name
     assert torch.equal(ep.kv_attention(q, cache, ints(40), status=st), ep.kv_attention(q, whole, ints(40)))
     assert int(st.item()) == 0
+
+
+def busy_caller(need):
+    """The caller's stream has half a second of work ahead, and memory that it let go holds ones everywhere."""
+    torch.cuda.synchronize()
+    for size in {512, *need}:
+        dirty = [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        del dirty
+    torch.cuda.synchronize()
+    torch.cuda._sleep(int(1e9))
+
+
+def test_attention_on_a_stream_of_its_own_beside_a_busy_one():
+    """What a call makes for its stream waits for nothing on the caller's, and is not given out while it is in use."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    P, pages, KH, D = 64, 300, 2, 128
+    cache = ep.new_kv_cache(pages, KH, P, D, torch.arange(pages, dtype=torch.int32, device="cuda").view(1, pages))
+    n = pages * P - 5  # long enough to be shared by many blocks, whose counters lie in the workspace
+    kv = torch.randn(n, 2 * KH, D, generator=g, device="cuda").to(torch.bfloat16)
+    ep.kv_append(kv[:, :KH], kv[:, KH:], cache, ints(n), cu_tokens=ints(0, n))
+    q = torch.randn(1, 16, D, generator=g, device="cuda").to(torch.bfloat16)
+    lens = ints(n)
+    want, want_lse = ep.kv_attention(q, cache, lens, return_lse=True)
+    need = ep.ep_kv_attention_workspace_bytes(1, 16, KH, D)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        busy_caller((need, want.numel() * 2, want_lse.numel() * 4))
+        got, lse = ep.kv_attention(q, cache, lens, return_lse=True, stream=stream)
+        with torch.cuda.stream(side):  # the next ones to ask for memory there
+            after = [torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        side.synchronize()
+        assert not torch.cuda.current_stream().query()  # the caller's work is still ahead
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(lse, want_lse) and all((t == 0xFF).all() for t in after)
+
+
+def test_append_and_experts_on_a_stream_of_their_own_beside_a_busy_one():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    k = torch.randn(30, 2, 64, generator=g, device="cuda").to(torch.bfloat16)
+    table = ints(0, 1).view(1, 2)
+    rope = torch.randn(30, 64, generator=g, device="cuda")
+    lens, cu = ints(30), ints(0, 30)
+    want = ep.kv_append(k, k, ep.new_kv_cache(2, 2, 16, 64, table), lens, cu_tokens=cu, rope=rope, q=k)
+    cache = ep.new_kv_cache(2, 2, 16, 64, table)
+    w = torch.randint(0, 256, (3, 64, 512), generator=g, dtype=torch.uint8, device="cuda")
+    s = torch.full((3, 64, 32), 120, dtype=torch.uint8, device="cuda")
+    x = torch.randn(3, 7, 1024, generator=g, device="cuda").to(torch.bfloat16)
+    count = ints(7, 7, 7)
+    want_y = ep.expert_linear(x, w, s, count)
+    side = torch.cuda.Stream()
+    busy_caller((want.numel() * 2, want_y.numel() * 2, ep.ep_expert_linear_workspace_bytes(3, 21, 1024, False)))
+    q = ep.kv_append(k, k, cache, lens, cu_tokens=cu, rope=rope, q=k, stream=side)
+    y = ep.expert_linear(x, w, s, count, stream=side)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    assert torch.equal(q, want) and torch.equal(y, want_y)

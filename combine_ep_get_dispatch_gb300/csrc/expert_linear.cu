@@ -446,19 +446,6 @@ __device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, 
   return true;
 }
 
-// The epilogue's threads agree on whether they go on, since they meet at barriers.
-__device__ __forceinline__ bool epilogue_all(bool ok) {
-  unsigned r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(ok ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // E4M3 rows: maps for boxes of 8, 16, .. rows.
@@ -740,7 +727,7 @@ __global__ void __launch_bounds__(kThreads)
     int seg = 0;
     while (next_segment(q, tb, run, g)) {
       const int buf = seg & 1;
-      if (!epilogue_all(mbar_wait(&sh.acc_full[buf], (seg / 2) & 1, p.status))) break;
+      if (!all_agree(mbar_wait(&sh.acc_full[buf], (seg / 2) & 1, p.status))) break;
       ++seg;
       tmem_fence_after();
       const uint32_t acc = tmem + buf * kMaxCols + (static_cast<uint32_t>(warp & 3) << 21);

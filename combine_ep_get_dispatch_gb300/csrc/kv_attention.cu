@@ -463,10 +463,6 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
         }
       }
     }
-    if (!ok) {  // given up: loads in flight land before the block ends
-      for (int i = 0; i < kStages; ++i)
-        if (i < stage || it >= kStages) mbar_drain(&sh.full[i], i < stage ? parity : parity ^ 1);
-    }
     const int slot = un % kUnits;
     if (un < kUnits || mbar_wait_warp(&sh.unit_empty[slot], (un / kUnits - 1) & 1, c.status)) {
       if (lane == 0) {
@@ -474,6 +470,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
         mbar_arrive(&sh.unit_full[slot]);
       }
     }
+    // Every load has landed before the block ends, also if those who wait for it
+    // (or this warp) have given up.
+    for (int i = 0; i < kStages; ++i)
+      if (i < stage || it >= kStages) mbar_drain(&sh.full[i], i < stage ? parity : parity ^ 1);
     return;
   }
 
@@ -485,8 +485,18 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
   const uint32_t sbase = smem_addr(smem);
   for (int un = 0;; ++un) {
     const int slot = un % kUnits;
-    if (!mbar_wait_warp(&sh.unit_full[slot], (un / kUnits) & 1, c.status)) break;
-    if (!sh.more[slot]) break;
+    // (The warps leave together: each votes once in every unit that has barriers,
+    // and once more with a no, at the end of the units or when its wait for one
+    // has run out, which is the answer to the others' next vote. So none of them
+    // stands at a barrier that another will not reach.)
+    if (!mbar_wait_warp(&sh.unit_full[slot], (un / kUnits) & 1, c.status)) {
+      all_agree(false);
+      break;
+    }
+    if (!sh.more[slot]) {
+      all_agree(false);
+      break;
+    }
     const Unit d = sh.unit[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.unit_empty[slot]);
@@ -747,11 +757,14 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
         md[t][r] = m[t][r] - kTop;
         m[t][r] = md[t][r] + static_cast<float>(e0);
       }
+    // (Whole units of one group's have no barriers. From here on nobody leaves
+    // this unit, and what was handed over in the one before has been read.)
+    if (!solo && (kTW > 1 || !whole) && !all_agree(true)) break;
     // Half of the groups hands over to the other half, until one is left.
 #pragma unroll
     for (int half = kTW / 2; half >= 1; half /= 2) {
       if (solo) break;
-      compute_sync();  // what was handed over before has been read
+      if (half < kTW / 2) compute_sync();  // what was handed over before has been read
       if (tw >= half && tw < 2 * half) {
         const int w = (tw - half) * kRW + rw;
 #pragma unroll

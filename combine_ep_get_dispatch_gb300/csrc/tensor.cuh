@@ -36,6 +36,21 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, unsigned parity, i
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
 
+// The 128 threads of barrier 1 meet: whether all of them go on. A thread whose
+// wait has run out may not leave alone, since the others meet there again.
+__device__ __forceinline__ bool all_agree(bool ok) {
+  unsigned r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
 // Whether the phase has completed, without waiting: non-zero. The answer takes
 // about 100 cycles, so a loop that has other work asks a turn ahead (raw, and
 // mbar_wait_asked when it needs to know) instead of standing still.

@@ -861,6 +861,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
       constexpr int kVec = kD / 4;            // float4 of a row
       constexpr int kAtOnce = 2;              // rows a thread works on side by side
       constexpr int kStride = 128 / kVec;     // rows of the block's threads
+      static_assert(kVec == 32 || kVec == 16, "a row's threads are a warp or half of one");
       const int ch = tid % kVec;
       for (int r0 = tid / kVec; r0 < rows; r0 += kAtOnce * kStride) {
         float top[kAtOnce], topd[kAtOnce], sum[kAtOnce];
@@ -913,8 +914,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kD, kNT>::kBlocksPerSM)
         }
         // (A group's sum goes where its first part lay: a thread overwrites what
         // it alone has read, but for a row's references, which all threads of
-        // the row, in one warp, have read before.)
-        __syncwarp(__activemask());
+        // the row, a warp or half of one, have read before.)
+        __syncwarp(kVec == 32 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16));
 #pragma unroll
         for (int a = 0; a < kAtOnce; ++a) {
           const int row = r0 + a * kStride;

@@ -15,3 +15,10 @@ def test_no_load_into_several_blocks_shared_memory(path):
     is for this device's own memory alone, and nothing checks that a caller's rows are there."""
     with open(path) as f:
         assert "multi" + "cast" not in f.read().lower()
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_warps_wait_for_lanes_that_are_named(path):
+    """The mask of the lanes that happen to run together names nobody that a wait is for."""
+    with open(path) as f:
+        assert "__activemask" not in f.read()

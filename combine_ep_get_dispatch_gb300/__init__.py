@@ -875,7 +875,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, seq_lens: torch.
     """Append k, v [tokens, heads, dim] bf16 to the cache, rotating k (and q) by position.
 
     seq_lens [seqs] int32 counts the appended tokens; cu_tokens [seqs + 1]
-    int32 delimits each sequence's tokens (None: one each). rope [positions,
+    int32 delimits each sequence's tokens (None: one each; tokens that it does
+    not cover are padding, their queries come back as zeros). rope [positions,
     rope_dim] fp32 holds cosines, then sines. k, v and q may be slices of one
     fused projection. Returns the rotated queries (q_out, made if not given).
     """

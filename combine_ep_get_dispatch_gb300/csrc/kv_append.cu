@@ -351,7 +351,18 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const KVAppendPa
     b = lo;
   }
   int t0, n;
-  if (!tokens_of(c, b, t0, n) || t < t0 || t >= t0 + n) return;
+  if (!tokens_of(c, b, t0, n) || t < t0 || t >= t0 + n) {
+    // A token of no sequence: zeros, so that nobody meets what lay there before.
+    if (t < __ldg(c.cu) || t >= __ldg(c.cu + c.B)) {
+#pragma unroll
+      for (int h = 0; h < kQueryHeads; ++h) {
+        if (h0 + h >= p.QH) break;
+        uint4* o = reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + (h0 + h) * kD);
+        o[va] = o[vb] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    return;
+  }
   const int len = __ldg(c.lens + b);
   if (!length_ok(p, len, n)) return;
   const float* row = p.rope + static_cast<int64_t>(len - n + (t - t0)) * p.rot;

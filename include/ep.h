@@ -559,9 +559,13 @@ int ep_fp8_quantize(const void* x, int64_t rows, int hidden, int fp8_flags, uint
  *
  * Tokens of a call lie in sequence order: sequence b's are rows
  * [cu_tokens[b], cu_tokens[b + 1]) (cu_tokens [num_seqs + 1] int32, ascending
- * from 0; NULL = one token per sequence, num_tokens == num_seqs). seq_lens[b]
- * counts the sequence's tokens with this call's included, so its i-th of n
- * tokens here has position seq_lens[b] - n + i.
+ * from 0; NULL = one token per sequence, num_tokens == num_seqs). Tokens that
+ * the list does not cover (from cu_tokens[num_seqs] on, or before cu_tokens[0])
+ * are padding, of a call captured for more tokens for instance, and not an
+ * error: nothing is appended for them, their q_out rows are zeros, and the
+ * attention gives them empty rows. seq_lens[b] counts the sequence's tokens
+ * with this call's included, so its i-th of n tokens here has position
+ * seq_lens[b] - n + i.
  *
  * The cache: pages of page_size tokens; page_table[b, j] names the page that
  * holds positions [j * page_size, (j + 1) * page_size) of sequence b. The

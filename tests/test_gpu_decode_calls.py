@@ -100,3 +100,40 @@ def test_append_and_experts_on_a_stream_of_their_own_beside_a_busy_one():
     assert not torch.cuda.current_stream().query()
     torch.cuda.synchronize()
     assert torch.equal(q, want) and torch.equal(y, want_y)
+
+
+@pytest.mark.parametrize("D,P,QH,rot,cu", [(64, 16, 3, 64, (0, 4, 4, 9)), (128, 64, 8, 0, (0, 1, 2, 3)),
+                                           (64, 32, 5, 32, (3, 4, 6, 9)), (128, 16, 2, 128, (13, 13, 13, 13)),
+                                           (64, 16, 4, 16, (0, 0, 0, 0))])
+def test_tokens_that_no_sequence_covers_are_padding(D, P, QH, rot, cu):
+    """They append nothing, their queries are zeros and their attention rows are empty; the others are as without them."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    n, lo, hi = 13, cu[0], cu[-1]
+    lens = ints(*(20 + b - a for a, b in zip(cu, cu[1:])))
+    qkv = torch.randn(n, QH + 2, D, generator=g, device="cuda").to(torch.bfloat16)
+    q, k, v = qkv.split([QH, 1, 1], 1)
+    rope = torch.randn(40, rot, generator=g, device="cuda") if rot else None
+    table = torch.arange(3 * 4, dtype=torch.int32, device="cuda").view(3, 4)
+    caches = []
+    for _ in range(2):
+        c = ep.new_kv_cache(12, 1, P, D, table)
+        c.k.fill_(0x38), c.v.fill_(0x30), c.k_scale.fill_(0.125), c.v_scale.fill_(0.125)
+        caches.append(c)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    G = QH + QH % 2  # (in place: a strided slice whose other heads stay)
+    out = torch.full((n, G, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    ep.kv_append(k, v, caches[0], lens, cu_tokens=ints(*cu), rope=rope, q=q, q_out=out[:, :QH], status=st)
+    assert not out[:lo, :QH].any() and not out[hi:, :QH].any() and (out[:, QH:] == 9.0).all()
+    if hi > lo:
+        want = ep.kv_append(k[lo:hi], v[lo:hi], caches[1], lens, cu_tokens=ints(*(x - lo for x in cu)), rope=rope,
+                            q=q[lo:hi])
+        assert torch.equal(out[lo:hi, :QH], want)
+    for name in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(getattr(caches[0], name), getattr(caches[1], name)), name
+    o, lse = ep.kv_attention(out[:, :QH], caches[0], lens, cu_tokens=ints(*cu), return_lse=True, status=st)
+    inside = np.zeros(n, bool)
+    inside[lo:hi] = True
+    inside = torch.from_numpy(inside).cuda()
+    assert not o[~inside].any() and torch.isneginf(lse[~inside]).all() and torch.isfinite(lse[inside]).all()
+    assert int(st.item()) == 0

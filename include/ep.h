@@ -697,9 +697,9 @@ size_t ep_expert_linear_workspace_bytes(int num_experts, int64_t max_rows, int i
  *   x_scale       [x_rows, in_features / 128] UE8M0 bytes (the FP8 dispatch with
  *                 EP_FP8_UE8M0), or NULL: x is BF16. BF16 rows enter the products
  *                 as two E4M3 terms with a scale per 32 inputs, which hold every
- *                 bit down to 2^-14 of the 32's largest magnitude, and 2^-23 of it
- *                 below that (magnitudes under 2^-135 count as zero). A row with
- *                 an infinity or a NaN gives NaNs. E4M3: x_rows <= INT32_MAX.
+ *                 bit down to 2^-13 of the 32's largest magnitude, and are within
+ *                 2^-21.8 of it below that (no step is finer than 2^-135). A row
+ *                 with an infinity or a NaN gives NaNs. E4M3: x_rows <= INT32_MAX.
  *   in_features   a multiple of 128, <= EP_MAX_HIDDEN
  *   out_features  a multiple of 8 (of 16 with EP_LINEAR_GLU), <= 2^20
  *   max_rows      an upper bound of the rows received by all experts; rows beyond

@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Callable, Optional, Tuple
 
@@ -489,6 +490,39 @@ def ep_expert_linear(x, x_scale, x_rows, in_features, row_count, row_offset, row
 
 
 # -------------------------------------------------------------- page-level ----
+# A call's `stream` (a torch stream or a raw handle; default: torch's current
+# one) runs all of it: what the call makes for itself or returns is made there.
+# Its arguments have to be ready on that stream, and to live until it is done.
+def _on_stream(stream, call, *args):
+    """A call with its stream as torch's current one.
+
+    What the call makes and fills is then ordered with its kernels, and memory
+    that it lets go serves that stream first. Its results also count as used
+    by the caller's stream, so that they are not given out again on `stream`
+    while that one still reads them.
+    """
+    s = stream if isinstance(stream, torch.cuda.Stream) else \
+        torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream))
+    caller = torch.cuda.current_stream()
+    with torch.cuda.stream(s):
+        made = call(*args)
+    if s != caller:
+        _record(made, caller)
+    return made
+
+
+def _record(made, stream) -> None:
+    """The tensors in a result (tuples and dataclasses of them) are used by the stream as well."""
+    if hasattr(made, "record_stream"):
+        made.record_stream(stream)
+    elif isinstance(made, tuple):
+        for part in made:
+            _record(part, stream)
+    elif dataclasses.is_dataclass(made):
+        for field in dataclasses.fields(made):
+            _record(getattr(made, field.name), stream)
+
+
 def _status(dev) -> torch.Tensor:
     return torch.zeros(1, dtype=torch.int32, device=dev)
 
@@ -503,6 +537,9 @@ def get_dispatch_layout(topk_idx: torch.Tensor, num_experts: int, num_ranks: int
     passed in must have been zero-filled once when it was allocated (each
     call leaves it ready for the next); without one, a zeroed one is made.
     """
+    if stream is not None:
+        return _on_stream(stream, get_dispatch_layout, topk_idx, num_experts, num_ranks, status, workspace, None,
+                          expert_alignment)
     topk_idx = topk_idx.to(torch.int32).contiguous()
     N, K = topk_idx.shape
     layout = new_layout(topk_idx, num_experts, num_ranks, expert_alignment)
@@ -511,7 +548,7 @@ def get_dispatch_layout(topk_idx: torch.Tensor, num_experts: int, num_ranks: int
         raise EPError("get_dispatch_layout", EP_ERR_INVALID_ARG)
     if workspace is None or workspace.numel() < need:
         workspace = torch.zeros(need, dtype=torch.uint8, device=topk_idx.device)
-    ep_get_dispatch_layout(layout, workspace, status, stream)
+    ep_get_dispatch_layout(layout, workspace, status)
     return layout
 
 
@@ -571,6 +608,9 @@ def dispatch(x: torch.Tensor, layout: Layout, topk_weights: Optional[torch.Tenso
     rows), with no host synchronisation; exact=True reads the counts first
     (one device->host copy) and sizes them exactly.
     """
+    if stream is not None:
+        return _on_stream(stream, dispatch, x, layout, topk_weights, use_fp8, with_rank, with_expert, exact, status,
+                          None, round_scale, use_ue8m0)
     if exact:
         cap_r = int(layout.rank_offset[-1].item())
         cap_e = int(layout.expert_offset[-1].item())
@@ -578,7 +618,7 @@ def dispatch(x: torch.Tensor, layout: Layout, topk_weights: Optional[torch.Tenso
         cap_r, cap_e = _worst_case_caps(x.shape[0], layout)
     res, rb, eb = _recv_buffers(x, layout, topk_weights, use_fp8, use_ue8m0, with_rank, with_expert, cap_r, cap_e)
     tw = topk_weights.contiguous() if topk_weights is not None else None
-    ep_dispatch(layout, x.contiguous(), fp8_flags(use_fp8, round_scale, use_ue8m0), tw, rb, eb, status, stream)
+    ep_dispatch(layout, x.contiguous(), fp8_flags(use_fp8, round_scale, use_ue8m0), tw, rb, eb, status)
     return res
 
 
@@ -594,6 +634,9 @@ def get_layout_and_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, num_experts
     GPU; the receive buffers are sized for the worst case, since the counts
     are not known before the call.
     """
+    if stream is not None:
+        return _on_stream(stream, get_layout_and_dispatch, x, topk_idx, num_experts, num_ranks, topk_weights, use_fp8,
+                          with_rank, with_expert, status, workspace, None, expert_alignment, round_scale, use_ue8m0)
     topk_idx = topk_idx.to(torch.int32).contiguous()
     N, K = topk_idx.shape
     layout = new_layout(topk_idx, num_experts, num_ranks, expert_alignment)
@@ -606,7 +649,7 @@ def get_layout_and_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, num_experts
     res, rb, eb = _recv_buffers(x, layout, topk_weights, use_fp8, use_ue8m0, with_rank, with_expert, cap_r, cap_e)
     tw = topk_weights.contiguous() if topk_weights is not None else None
     ep_layout_dispatch(layout, workspace, x.contiguous(), fp8_flags(use_fp8, round_scale, use_ue8m0), tw, rb, eb,
-                       status, stream)
+                       status)
     return layout, res
 
 
@@ -614,33 +657,39 @@ def combine(expert_y: torch.Tensor, layout: Layout, topk_weights: torch.Tensor,
             out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
             stream=None, bias: Optional[torch.Tensor] = None) -> torch.Tensor:
     """out [N, H] bf16 = sum_k w[t,k] * expert_y[expert_slot[t,k]] (+ bias), fp32 accumulation."""
+    if stream is not None:
+        return _on_stream(stream, combine, expert_y, layout, topk_weights, out, status, None, bias)
     N = layout.topk_idx.shape[0]
     if out is None:
         out = torch.empty((N, expert_y.shape[1]), dtype=torch.bfloat16, device=expert_y.device)
     b = bias.contiguous() if bias is not None else None
-    ep_combine(layout, expert_y.contiguous(), topk_weights.contiguous(), out, status, stream, bias=b)
+    ep_combine(layout, expert_y.contiguous(), topk_weights.contiguous(), out, status, bias=b)
     return out
 
 
 def dispatch_backward(grad_expert_x: torch.Tensor, layout: Layout, status: Optional[torch.Tensor] = None,
                       stream=None) -> torch.Tensor:
     """grad_x [N, H] bf16: the unit-weight sum of each token's expert-major row gradients."""
+    if stream is not None:
+        return _on_stream(stream, dispatch_backward, grad_expert_x, layout, status)
     N = layout.topk_idx.shape[0]
     out = torch.empty((N, grad_expert_x.shape[1]), dtype=torch.bfloat16, device=grad_expert_x.device)
     c = layout.c_struct()
     g = grad_expert_x.contiguous()
     _check(lib().ep_combine(ctypes.byref(c), _p(g), g.shape[0], g.shape[1], None, None, _p(out), _p(status),
-                            _stream(stream)), "ep_combine")
+                            _stream(None)), "ep_combine")
     return out
 
 
 def combine_backward(grad_out: torch.Tensor, layout: Layout, expert_y: torch.Tensor, topk_weights: torch.Tensor,
                      status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(grad_y [rows, H] bf16, grad_w [N, K] fp32) of out = sum_k w * expert_y[expert_slot]."""
+    if stream is not None:
+        return _on_stream(stream, combine_backward, grad_out, layout, expert_y, topk_weights, status)
     grad_y = torch.zeros_like(expert_y)
     grad_w = torch.empty_like(topk_weights, dtype=torch.float32)
     ep_combine_backward(layout, grad_out.contiguous(), expert_y.contiguous(), topk_weights.contiguous(), grad_y,
-                        grad_w, status, stream)
+                        grad_w, status)
     return grad_y, grad_w
 
 
@@ -652,14 +701,16 @@ def combine_two_level(expert_y: torch.Tensor, layout: Layout, topk_weights: torc
     Returns (out [N, H], rank_rows [D_r, H]); reads the per-rank row count
     from the layout (one device->host copy).
     """
+    if stream is not None:
+        return _on_stream(stream, combine_two_level, expert_y, layout, topk_weights, bias, status)
     N = layout.topk_idx.shape[0]
     H = expert_y.shape[1]
     D_r = int(layout.rank_offset[-1].item())
     rank_rows = torch.empty((D_r, H), dtype=torch.bfloat16, device=expert_y.device)
-    ep_combine_to_ranks(layout, expert_y.contiguous(), topk_weights.contiguous(), rank_rows, status, stream)
+    ep_combine_to_ranks(layout, expert_y.contiguous(), topk_weights.contiguous(), rank_rows, status)
     out = torch.empty((N, H), dtype=torch.bfloat16, device=expert_y.device)
     b = bias.contiguous() if bias is not None else None
-    ep_combine_ranks(layout, rank_rows, out, status, stream, bias=b)
+    ep_combine_ranks(layout, rank_rows, out, status, bias=b)
     return out, rank_rows
 
 
@@ -691,6 +742,11 @@ def low_latency_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, num_max_dispat
     return_recv_hook=False the receive phase is launched at once and hook is
     None.
     """
+    if stream is not None:
+        *results, hook = _on_stream(stream, low_latency_dispatch, x, topk_idx, num_max_dispatch_tokens_per_rank,
+                                    num_experts, num_ranks, use_fp8, return_recv_hook, status, workspace, None,
+                                    round_scale, use_ue8m0, cumulative_local_expert_recv_stats)
+        return (*results, hook and functools.partial(_on_stream, stream, hook))
     N, H = x.shape
     K = topk_idx.shape[1]
     E, R, T = num_experts, num_ranks, num_max_dispatch_tokens_per_rank
@@ -708,11 +764,11 @@ def low_latency_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, num_max_dispat
     layout_range = torch.empty((E, R), dtype=torch.int64, device=dev)
     idx = topk_idx.to(torch.int32).contiguous()
     ep_ll_dispatch_send(x.contiguous(), idx, H, E, R, T, fp8_flags(use_fp8, round_scale, use_ue8m0), recv_x,
-                        recv_scales, recv_src, workspace, status, stream)
+                        recv_scales, recv_src, workspace, status)
     handle = LLHandle(workspace, N, K, H, E, R, T, recv_src, layout_range)
 
     def hook() -> None:
-        ep_ll_dispatch_recv(workspace, N, K, E, R, T, recv_count, layout_range, status, stream,
+        ep_ll_dispatch_recv(workspace, N, K, E, R, T, recv_count, layout_range, status, None,
                             cumulative_local_expert_recv_stats)
 
     out_x = (recv_x, recv_scales) if use_fp8 else recv_x
@@ -732,6 +788,10 @@ def low_latency_combine(expert_y: torch.Tensor, topk_weights: torch.Tensor, hand
     returned hook runs the weighted sum; returns (out, hook), out valid after
     hook() ("DeepEP V1 (legacy) guide", section 6.1).
     """
+    if stream is not None:
+        made = _on_stream(stream, low_latency_combine, expert_y, topk_weights, handle, out, status, return_recv_hook,
+                          None, bias)
+        return (made[0], functools.partial(_on_stream, stream, made[1])) if return_recv_hook else made
     h = handle
     if out is None:
         out = torch.empty((h.N, h.H), dtype=torch.bfloat16, device=expert_y.device)
@@ -739,13 +799,13 @@ def low_latency_combine(expert_y: torch.Tensor, topk_weights: torch.Tensor, hand
     w = topk_weights.contiguous()
     b = bias.contiguous() if bias is not None else None
     if not return_recv_hook:
-        ep_ll_combine(y, w, h.workspace, h.N, h.K, h.H, h.E, h.R, h.T, out, status, stream, bias=b)
+        ep_ll_combine(y, w, h.workspace, h.N, h.K, h.H, h.E, h.R, h.T, out, status, bias=b)
         return out
     staging = torch.empty((h.N * h.K, h.H), dtype=torch.bfloat16, device=y.device)
-    ep_ll_combine_send(y, h.workspace, h.N, h.K, h.H, h.E, h.R, h.T, staging, status, stream)
+    ep_ll_combine_send(y, h.workspace, h.N, h.K, h.H, h.E, h.R, h.T, staging, status)
 
     def hook() -> None:
-        ep_ll_combine_recv(staging, w, h.workspace, h.N, h.K, h.H, h.E, h.R, h.T, out, status, stream, bias=b)
+        ep_ll_combine_recv(staging, w, h.workspace, h.N, h.K, h.H, h.E, h.R, h.T, out, status, bias=b)
 
     return out, hook
 
@@ -772,8 +832,10 @@ def low_latency_update_mask_buffer(handle, rank: int, mask: bool = True, num_ran
 
 def low_latency_query_mask_buffer(handle, num_ranks: Optional[int] = None, stream=None) -> torch.Tensor:
     """The current rank mask, [R] int32 on the device (non-zero = masked)."""
+    if stream is not None:
+        return _on_stream(stream, low_latency_query_mask_buffer, handle, num_ranks)
     ws, R = _ws_ranks(handle, num_ranks)
-    return ep_ll_query_mask(ws, R, stream=stream)
+    return ep_ll_query_mask(ws, R)
 
 
 def low_latency_clean_mask_buffer(handle, num_ranks: Optional[int] = None, stream=None) -> None:
@@ -783,9 +845,6 @@ def low_latency_clean_mask_buffer(handle, num_ranks: Optional[int] = None, strea
 
 
 # ------------------------------------- the decode step around the dispatch ----
-# A call's `stream` (a torch stream or a raw handle; default: torch's current
-# one) runs all of it: what the call makes for itself or returns is made there.
-# Its arguments have to be ready on that stream, and to live until it is done.
 @dataclasses.dataclass
 class KVCache:
     """A paged key/value cache in E4M3 with a power-of-two scale per (page, head).
@@ -846,26 +905,6 @@ def new_kv_cache(num_pages: int, num_heads: int, page_size: int, head_dim: int, 
     return KVCache(torch.zeros(shape, dtype=torch.uint8, device=dev), torch.zeros(shape, dtype=torch.uint8, device=dev),
                    torch.zeros(shape[:2], dtype=torch.float32, device=dev),
                    torch.zeros(shape[:2], dtype=torch.float32, device=dev), page_table)
-
-
-def _on_stream(stream, call, *args):
-    """A call with its stream as torch's current one.
-
-    What the call makes and fills is then ordered with its kernels, and memory
-    that it lets go serves that stream first. Its results also count as used
-    by the caller's stream, so that they are not given out again on `stream`
-    while that one still reads them.
-    """
-    s = stream if isinstance(stream, torch.cuda.Stream) else \
-        torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream))
-    caller = torch.cuda.current_stream()
-    with torch.cuda.stream(s):
-        made = call(*args)
-    if s != caller:
-        for t in made if isinstance(made, tuple) else (made,):
-            if t is not None:
-                t.record_stream(caller)
-    return made
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, seq_lens: torch.Tensor,

@@ -31,14 +31,14 @@
 // With more rows the blocks' reads of x set the pace: each of an expert's
 // output tiles needs all of its rows, and each block loads them for itself
 // (x may lie in any memory that the device can read, so no load serves several
-// blocks at once). At 128 rows that is 15 GB of rows beside 8 GB of weights and
-// scales, 12.8 TB/s out of L2.
+// blocks at once). The blocks then work on an expert's output tiles side by
+// side, so that its rows come from L2 but for the first time (work_together).
 //
 // Measured (256 experts, 7168 inputs, 2 x 2048 gated outputs; copy rate 6.69
-// TB/s): 4 BF16 rows an expert 698 us, 5.6 TB/s; 128 E4M3 rows 1839 us, 2.4
-// TB/s of what must be read and 1.05 PFLOP/s; one token's eight experts 35 us, of
-// which 10 pass before the first weights have come and 4 after the last; 2048
-// inputs, 7168 outputs, 4 BF16 rows an expert 325 us, 6.1 TB/s.
+// TB/s): 4 BF16 rows an expert 637 us, 6.2 TB/s; 128 E4M3 rows 1054 us, 4.1
+// TB/s and 1.83 PFLOP/s; one token's eight experts 34 us, of which 10 pass before
+// the first weights have come and 4 after the last; 2048 inputs, 7168 outputs, 4
+// BF16 rows an expert 330 us, 6.0 TB/s.
 //
 // Two launches: expert_rows_kernel splits BF16 rows into the tensor cores'
 // shared-memory layout (of E4M3 rows it lays out the scales; their codes come
@@ -369,6 +369,24 @@ struct Segment {
   int64_t unit;
 };
 
+// Which unit comes v-th in the blocks' runs when experts are worked on together
+// (work_together): the j-th unit of run a is the a-th of the units that the
+// blocks take at the same time, so that the output tiles of an expert, which read
+// the same rows, are worked on side by side. `length` is the units of a run,
+// rounded; of the last of `runs`, `full` are left.
+struct Order {
+  unsigned length, runs, full;
+  __device__ __forceinline__ Order(unsigned units, unsigned blocks) {
+    length = max(1u, (units + blocks / 2) / blocks);
+    runs = (units + length - 1) / length;
+    full = units - (runs - 1) * length;
+  }
+  __device__ __forceinline__ int unit(int64_t v) const {
+    const unsigned a = static_cast<unsigned>(v) / length, j = static_cast<unsigned>(v) - a * length;
+    return static_cast<int>(j < full ? j * runs + a : full * runs + (j - full) * (runs - 1) + a);
+  }
+};
+
 // A block's stages: positions [at, end) of units * KS. Behind a first unit
 // that had to be looked for, the next ones are counted on.
 struct Run {
@@ -404,16 +422,18 @@ __device__ __forceinline__ int owner_of(int64_t total, int blocks, int64_t i) {
 // outputs) follow one another, so that its weights come from L2 after the first.
 // (Each role passes here between two units: with divisions and a search each
 // time the products of 2048 inputs, eight stages a unit, took 366 us, now 330.)
-__device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, Run& run, Segment& s) {
+template <bool kTogether>
+__device__ __forceinline__ bool next_segment(const Params& q, const Tables& tb, const Order& order, Run& run, Segment& s) {
   if (run.at >= run.end) return false;
   const int E = q.p.E;
-  if (run.e < 0) {
+  if (run.e < 0 || kTogether) {
     s.unit = run.at / q.KS;
     s.s0 = static_cast<int>(run.at - s.unit * q.KS);
-    run.e = uniform(expert_of(tb.tile0, E, static_cast<int>(s.unit / q.MT)));
+    const int unit = kTogether ? order.unit(s.unit) : static_cast<int>(s.unit);
+    run.e = uniform(expert_of(tb.tile0, E, unit / q.MT));
     run.tile0 = uniform(tb.tile0[run.e]);
     run.tiles = uniform(tb.tile0[run.e + 1]) - run.tile0;
-    const int u = static_cast<int>(s.unit - static_cast<int64_t>(run.tile0) * q.MT);
+    const int u = unit - run.tile0 * q.MT;
     run.mt = u / run.tiles;
     run.tile = u - run.mt * run.tiles;
   } else {
@@ -455,8 +475,8 @@ struct RowMaps {
   CUtensorMap box[kRowMaps];
 };
 
-// kFp8: x in E4M3. kSteps: steps of a stage.
-template <bool kFp8, int kSteps>
+// kFp8: x in E4M3. kSteps: steps of a stage. kTogether: the units' order, see Order.
+template <bool kFp8, int kSteps, bool kTogether>
 __global__ void __launch_bounds__(kThreads)
     expert_linear_kernel(const Params q, const __grid_constant__ CUtensorMap map,
                          const __grid_constant__ RowMaps maps) {
@@ -495,6 +515,7 @@ __global__ void __launch_bounds__(kThreads)
   // Every block that takes part has steps: the join counts on it.
   const int me = static_cast<int>(blockIdx.x);
   const int blocks = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(total / kMinStages, int64_t{1})));
+  const Order order(static_cast<unsigned>(uniform(tb.tile0[p.E]) * q.MT), blocks);
   Run run{0, 0};
   if (me < blocks) run = Run{run_begin(total, blocks, me), run_begin(total, blocks, me + 1)};
   // A stage: weights, rows, the rows' scales. Behind the stages: the ring of
@@ -520,7 +541,7 @@ __global__ void __launch_bounds__(kThreads)
     Segment g;
     Ring r;
     int ahead = 0;
-    while (ahead < q.stages && next_segment(q, tb, run, g)) {
+    while (ahead < q.stages && next_segment<kTogether>(q, tb, order, run, g)) {
       for (int st = g.s0; st < g.s1 && ahead < q.stages; ++st, ++ahead) {
         if (elect_one()) load_w(g, st, kSteps * kTileTx + steps_of(st) * step_bytes(g), r);
         r.advance(q);
@@ -532,7 +553,7 @@ __global__ void __launch_bounds__(kThreads)
     unsigned round = 0;  // passes over the ring
     unsigned empty = 0;  // asked a stage ahead
     bool ok = true;
-    while (ok && next_segment(q, tb, run, g)) {
+    while (ok && next_segment<kTogether>(q, tb, order, run, g)) {
       const unsigned step = step_bytes(g), xcodes = step - q.scale_bytes;
       const unsigned image_step = kFp8 ? q.scale_bytes : step;
       const uint8_t* x =
@@ -587,7 +608,7 @@ __global__ void __launch_bounds__(kThreads)
     // What the next stage needs is looked for before this one's products are
     // issued, so that the look costs no time between them.
     unsigned full = 0, scales = 0;
-    while (ok && next_segment(q, tb, run, g)) {
+    while (ok && next_segment<kTogether>(q, tb, order, run, g)) {
       const int buf = seg & 1;
       if (seg >= 2 && !mbar_wait_warp(&sh.acc_empty[buf], (seg / 2 - 1) & 1, p.status)) break;
       tmem_fence_after();
@@ -657,13 +678,13 @@ __global__ void __launch_bounds__(kThreads)
     int lo[kAhead], hi[kAhead];
     Segment g;
     int next = 0;
-    bool more = next_segment(q, tb, run, g);
+    bool more = next_segment<kTogether>(q, tb, order, run, g);
     if (more) next = g.s0 * kSteps;
     auto advance = [&]() {  // to the next group
       if (!more) return;
       next = (next & ~3) + 4;
       if (next >= min(q.KB, g.s1 * kSteps)) {
-        more = next_segment(q, tb, run, g);
+        more = next_segment<kTogether>(q, tb, order, run, g);
         if (more) next = g.s0 * kSteps;
       }
     };
@@ -727,7 +748,7 @@ __global__ void __launch_bounds__(kThreads)
     grid_dependency_wait();
     Segment g;
     int seg = 0;
-    while (next_segment(q, tb, run, g)) {
+    while (next_segment<kTogether>(q, tb, order, run, g)) {
       const int buf = seg & 1;
       if (!all_agree(mbar_wait(&sh.acc_full[buf], (seg / 2) & 1, p.status))) break;
       ++seg;
@@ -841,10 +862,23 @@ int tile_rows_for(int E, int64_t max_rows, int mult) {
 // Steps of a stage: two halve what a stage costs besides its bytes. With more
 // than 64 columns they are large enough for it not to matter, and one step lets
 // a tile have more than 128. In us with one / two steps, rows an expert (256
-// experts, 7168 inputs, 2 x 2048 gated outputs): 4 BF16 787 / 744, 12 BF16 928 /
-// 920, 4 E4M3 765 / 677, 24 E4M3 853 / 840; of more than 64 columns 24 BF16 1117 /
-// 1122, 40 BF16 1467 / 1464, 48 E4M3 1110 / 1114, 72 E4M3 1333 / 1338.
+// experts, 7168 inputs, 2 x 2048 gated outputs): 4 BF16 733 / 667, 12 BF16 769 /
+// 737, 4 E4M3 737 / 641, 24 E4M3 758 / 710; of more than 64 columns 24 BF16 843 /
+// 864, 40 BF16 971 / 970, 48 E4M3 850 / 852, 72 E4M3 882 / 895.
 int steps_for(int cols) { return cols <= 64 ? 2 : 1; }
+
+// Whether the blocks work on an expert's output tiles side by side, so that its
+// rows come from L2, or each on its own run of them. With more than 64 columns
+// always: in runs all experts' rows are in use at once (235 MB at 128 rows of 256
+// experts, and 12.2 GB came from HBM where 4.4 must). With fewer columns for long
+// units alone, since each unit of this order has to be looked for. In us in runs /
+// together (256 experts, 4096 outputs): 7168 inputs, about 128 E4M3 rows 1936 /
+// 1070, 72 E4M3 1360 / 921, 40 BF16 1484 / 992, 384 inputs (1536 outputs), 128 E4M3
+// 195 / 184; up to 64 columns, 4 BF16, 12 BF16, 4 E4M3 and 28 E4M3 rows: 7168 inputs
+// 732, 889, 662, 891 / 661, 732, 641, 726; 5120 496, 564, 468, 563 / 483, 534, 466,
+// 530; 4096 387, 433, 373, 434 / 395, 439, 383, 438; 1024 134, 141, 132, 168 / 170,
+// 169, 163, 173.
+bool work_together(int steps, int KB) { return steps == 1 || KB >= 40; }
 
 struct Sizes {
   int tile_rows;
@@ -871,10 +905,10 @@ Sizes sizes_of(int E, int64_t max_rows, int K, bool fp8) {
 
 namespace {
 
-template <bool kFp8, int kSteps>
+template <bool kFp8, int kSteps, bool kTogether>
 cudaError_t launch_products(const Params& q, const CUtensorMap& map, const RowMaps& maps, size_t smem, int dev, int sms,
                             cudaStream_t s) {
-  const auto kernel = expert_linear_kernel<kFp8, kSteps>;
+  const auto kernel = expert_linear_kernel<kFp8, kSteps, kTogether>;
   const void* fn = reinterpret_cast<const void*>(kernel);
   const cudaError_t err = ensure_dynamic_smem(fn, dev, smem);
   if (err != cudaSuccess) return err;
@@ -886,8 +920,9 @@ cudaError_t launch_products(const Params& q, const CUtensorMap& map, const RowMa
 template <bool kFp8>
 cudaError_t launch_steps(const Params& q, const CUtensorMap& map, const RowMaps& maps, size_t smem, int dev, int sms,
                          cudaStream_t s) {
-  return q.steps == 2 ? launch_products<kFp8, 2>(q, map, maps, smem, dev, sms, s)
-                      : launch_products<kFp8, 1>(q, map, maps, smem, dev, sms, s);
+  if (!work_together(q.steps, q.KB)) return launch_products<kFp8, 2, false>(q, map, maps, smem, dev, sms, s);
+  return q.steps == 2 ? launch_products<kFp8, 2, true>(q, map, maps, smem, dev, sms, s)
+                      : launch_products<kFp8, 1, true>(q, map, maps, smem, dev, sms, s);
 }
 
 }  // namespace

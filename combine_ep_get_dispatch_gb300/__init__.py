@@ -983,7 +983,10 @@ def expert_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Ten
     weight_scale [E, out, in/32] UE8M0 bytes. glu: y = silu(gate) * up of the
     two halves of the outputs. Rows that no expert received are left as they
     are in out. max_rows bounds the rows received by all experts (default: all
-    of x's), and sizes the workspace.
+    of x's). It sizes the workspace and the products' tiles, so give it in the
+    [E, cap, in] layout, where all of x's rows are every slot of every region:
+    tokens * topk is enough. A workspace that is kept need not be zero-filled
+    at each call.
     """
     if stream is not None:
         return _on_stream(stream, expert_linear, x, weight, weight_scale, row_count, row_offset, x_scale, glu, out,

@@ -16,7 +16,7 @@
 // the two 8-channel vectors that rotate into one another. The queries' blocks
 // follow in the same launch.
 //
-// What bounds it: a few tokens' launch (1 token 2.8 us, 256 tokens 3.7 us on the
+// What bounds it: a few tokens' launch (1 token 2.6 us, 256 tokens 3.5 us on the
 // device); for prompts HBM: 16.9 k tokens, 32 query and 4 cache heads of 128,
 // 200 MB in 38.5 us, 5.2 TB/s (copy rate 6.69). Rows stay in registers between the
 // maximum and the encoding, and a thread rotates four heads of a token with one

@@ -67,7 +67,10 @@ constexpr int kFan = 8;          // parts of a shared unit that one block joins 
 // 64 rows cost more themselves: in us with 6 / 4 / 3 / 2, 60 sequences of up to 3000
 // tokens, 8 drafted, 8 heads of 64: 42.2 / 40.5 / 38.6 / 40.2, 30 of 300: 23.1 / 23.2 /
 // 24.0 / 24.0, 20 of up to 20000, 5 drafted: 57.0 / 56.5 / 56.6 / 55.6. With 32 rows and
-// fewer it depends on the lengths alone (6 / 4: 49.4 / 47.3, 24.3 / 24.7, 37.3 / 38.4).
+// fewer it depends on the lengths alone (32 rows, 6 / 4: 49.4 / 47.3, 24.3 / 24.7,
+// 37.3 / 38.4; 9 / 6 / 4 / 2 with heads of 128: 60 sequences of up to 3000 tokens, 8
+// heads of 8 rows 21.1 / 20.2 / 20.1 / 21.5, of 16 rows 30.7 / 31.1 / 32.3 / 36.1, 24 of up to
+// 30000, 4 heads of 8 rows 25.8 / 27.5 / 28.8 / 27.9, of 16 rows 34.1 / 36.0 / 37.5 / 38.6).
 constexpr int unit_cost(int row_warps) { return row_warps < 4 ? 6 : 4; }
 constexpr int kUnits = 8;        // units whose descriptors are in flight
 constexpr int kSolo = 5;         // most chunks of a unit that one group of warps takes alone

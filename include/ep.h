@@ -666,7 +666,9 @@ size_t ep_kv_attention_workspace_bytes(int num_tokens, int num_q_heads, int num_
  *                ready for the next. Not to be shared by calls in flight.
  *   status       EP_ST_BAD_INDEX: a page outside the cache (masked) or cu_tokens
  *                out of order; EP_ST_CAPACITY: a sequence longer than
- *                max_pages * page_size (the rest of it is masked)
+ *                max_pages * page_size (the rest of it is masked);
+ *                EP_ST_TIMEOUT: a bounded wait gave up, results are wrong and the
+ *                workspace has to be zero-filled again
  * Results do not depend on the order in which blocks run.
  */
 int ep_kv_attention(const ep_kv_cache_t* C, const int32_t* seq_lens, const int32_t* cu_tokens, int num_tokens,
@@ -703,7 +705,9 @@ size_t ep_expert_linear_workspace_bytes(int num_experts, int64_t max_rows, int i
  *   in_features   a multiple of 128, <= EP_MAX_HIDDEN
  *   out_features  a multiple of 8 (of 16 with EP_LINEAR_GLU), <= 2^20
  *   max_rows      an upper bound of the rows received by all experts; rows beyond
- *                 it are skipped and flagged EP_ST_CAPACITY
+ *                 it are skipped and flagged EP_ST_CAPACITY. With max_rows or x_rows
+ *                 0 the counts are not looked at. It also chooses the size of the
+ *                 products' tiles of rows: a bound far above what comes costs time
  *   w             [num_experts, out_features, in_features / 2] bytes, two codes
  *                 each, the lower channel in the low four bits; 32-byte aligned
  *   w_scale       [num_experts, out_features, in_features / 32] UE8M0 bytes,
@@ -712,7 +716,8 @@ size_t ep_expert_linear_workspace_bytes(int num_experts, int64_t max_rows, int i
  *   workspace     at least ep_expert_linear_workspace_bytes(...) bytes, 256-byte
  *                 aligned, zero-filled before its first use; every call leaves it
  *                 ready for the next. Not to be shared by calls in flight.
- *   status        EP_ST_CAPACITY: rows outside x, or more than max_rows
+ *   status        EP_ST_CAPACITY: rows outside x, or more than max_rows;
+ *                 EP_ST_TIMEOUT as for ep_kv_attention
  */
 int ep_expert_linear(const void* x, const uint8_t* x_scale, int64_t x_rows, int in_features,
                      const int32_t* row_count, const int32_t* row_offset, int64_t rows_per_expert, int num_experts,

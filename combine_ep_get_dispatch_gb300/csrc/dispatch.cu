@@ -165,42 +165,6 @@ constexpr size_t kSmemPerSM = 228 * 1024;            // shared memory of one SM
 constexpr size_t kSmemReservedPerBlock = 1024;       // the runtime's share of it per block
 constexpr int kF8MaxDest = 2 * EP_MAX_TOPK;  // <= K expert copies + <= K rank copies
 
-// Smallest power of two >= s for s >= 0 (exact on the bit pattern; a
-// subnormal m * 2^-149 rounds to the next power of two of m).
-__device__ __forceinline__ float pow2_ceil(float s) {
-  unsigned u = __float_as_uint(s);
-  if (u == 0u) return s;
-  if ((u & 0x7F800000u) == 0u) return __uint_as_float(u == 1u ? 1u : (1u << (32 - __clz(u - 1u))));
-  if (u & 0x007FFFFFu) u = (u & 0xFF800000u) + 0x00800000u;
-  return __uint_as_float(u);
-}
-
-// UE8M0 byte 2^(b - 127) of a power-of-two scale >= 2^-127 (0 for s = 0).
-__device__ __forceinline__ uint8_t ue8m0_byte(float s) {
-  return static_cast<uint8_t>((__float_as_uint(s) >> 23) & 0xFFu);
-}
-
-// Packed fp32 pairs (lo in the low word): the sm_100-family f32x2
-// arithmetic, one instruction for two IEEE fp32 operations.
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
 }

@@ -50,10 +50,20 @@ EP_FP8_ROUND_SCALE = 0x2
 EP_FP8_UE8M0 = 0x4
 
 EP_LINEAR_GLU = 0x1
+EP_LINEAR_TRANSPOSED = 0x2
+EP_LINEAR_X_UE8M0 = 0x4
+EP_LINEAR_OUT_FP8 = 0x8
+EP_LINEAR_OUT_ROUND_SCALE = 0x10
+EP_LINEAR_OUT_UE8M0 = 0x20
+
+EP_ROUTE_BF16 = 0x1
+EP_ROUTE_SIGMOID = 0x2
+EP_ROUTE_RENORMALIZE = 0x4
 
 EP_MAX_EXPERTS = 1024
 EP_MAX_TOPK = 32
 EP_MAX_HIDDEN = 16384
+EP_MAX_ROUTE_GROUPS = 32
 
 
 class EPError(RuntimeError):
@@ -155,6 +165,10 @@ def lib() -> ctypes.CDLL:
                                 P]),
         "ep_expert_linear_workspace_bytes": (SZ, [I, I64, I, I]),
         "ep_expert_linear": (I, [P, P, I64, I, P, P, I64, I, I64, P, P, I, I, P, P, SZ, P, P]),
+        "ep_route": (I, [P, I64, I, I, I, P, I, I, I, I, ctypes.c_float, P, P, P, P]),
+        "ep_route_backward": (I, [P, P, P, I64, P, I, I, I, I, ctypes.c_float, P, P, P]),
+        "ep_expert_linear_fp8_workspace_bytes": (SZ, [I, I64]),
+        "ep_expert_linear_fp8": (I, [P, P, I64, I, P, P, I64, I, I64, P, P, I, I, P, P, P, SZ, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -487,6 +501,59 @@ def ep_expert_linear(x, x_scale, x_rows, in_features, row_count, row_offset, row
                                 workspace.numel(), _address(status, "status", _I32), _raw(stream))
     if rc != EP_OK:
         raise EPError("ep_expert_linear", rc)
+
+
+def _logits(t: torch.Tensor):
+    """(address, token stride, tokens, experts, flags) of [tokens, experts] bf16 or fp32 logits, rows apart as they may be."""
+    if t.dim() != 2 or t.dtype not in (_BF16, _F32) or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("logits: expected a CUDA tensor [tokens, experts] of bf16 or fp32, experts contiguous")
+    n, experts = t.shape
+    return t.data_ptr(), t.stride(0) if n > 1 else experts, n, experts, EP_ROUTE_BF16 if t.dtype is _BF16 else 0
+
+
+def ep_route(logits, num_topk, bias, num_groups, topk_groups, group_best, flags, scale, topk_idx, topk_weights,
+             scores=None, stream=None) -> None:
+    at, stride, tokens, experts, kind = _logits(logits)
+    rc = lib().ep_route(at, stride, tokens, experts, num_topk, _address(bias, "bias", _F32, (experts,)), num_groups,
+                        topk_groups, group_best, flags | kind, scale,
+                        _address(topk_idx, "topk_idx", _I32, (tokens, num_topk)),
+                        _address(topk_weights, "topk_weights", _F32, (tokens, num_topk)),
+                        _address(scores, "scores", _F32, (tokens, experts)), _raw(stream))
+    if rc != EP_OK:
+        raise EPError("ep_route", rc)
+
+
+def ep_route_backward(grad_weights, grad_scores, logits, topk_idx, flags, scale, grad_logits, status=None,
+                      stream=None) -> None:
+    at, stride, tokens, experts, kind = _logits(logits)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != tokens:
+        raise ValueError("topk_idx: expected [tokens, topk]")
+    rc = lib().ep_route_backward(_address(grad_weights, "grad_weights", _F32, topk_idx.shape),
+                                 _address(grad_scores, "grad_scores", _F32, (tokens, experts)), at, stride,
+                                 _address(topk_idx, "topk_idx", _I32), tokens, experts, topk_idx.shape[1], flags | kind,
+                                 scale, _address(grad_logits, "grad_logits", logits.dtype, (tokens, experts)),
+                                 _address(status, "status", _I32), _raw(stream))
+    if rc != EP_OK:
+        raise EPError("ep_route_backward", rc)
+
+
+def ep_expert_linear_fp8_workspace_bytes(num_experts: int, max_rows: int) -> int:
+    return int(lib().ep_expert_linear_fp8_workspace_bytes(num_experts, max_rows))
+
+
+def ep_expert_linear_fp8(x, x_scale, x_rows, in_features, row_count, row_offset, rows_per_expert, max_rows, w, w_scale,
+                         out_features, flags, y, y_scale, workspace, status=None, stream=None) -> None:
+    rc = lib().ep_expert_linear_fp8(_address(x, "x", _U8),
+                                    _address(x_scale, "x_scale", _U8 if flags & EP_LINEAR_X_UE8M0 else _F32), x_rows,
+                                    in_features, _address(row_count, "row_count", _I32),
+                                    _address(row_offset, "row_offset", _I32), rows_per_expert, w.shape[0], max_rows,
+                                    _address(w, "weight", _U8), _address(w_scale, "weight_scale", _F32), out_features,
+                                    flags, _address(y, "out", _U8 if flags & EP_LINEAR_OUT_FP8 else _BF16),
+                                    _address(y_scale, "out_scale", _U8 if flags & EP_LINEAR_OUT_UE8M0 else _F32),
+                                    _address(workspace, "workspace", _U8), workspace.numel(),
+                                    _address(status, "status", _I32), _raw(stream))
+    if rc != EP_OK:
+        raise EPError("ep_expert_linear_fp8", rc)
 
 
 # -------------------------------------------------------------- page-level ----
@@ -1015,3 +1082,179 @@ def expert_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Ten
     ep_expert_linear(x, x_scale, rows, K, row_count, row_offset, x.shape[1] if row_offset is None else 0, limit, weight,
                      weight_scale, EP_LINEAR_GLU if glu else 0, out, workspace, status)
     return out
+
+
+# ------------------------------------- the router and the 8-bit experts ----
+def _same_device(first: torch.Tensor, *tensors: Optional[torch.Tensor]) -> None:
+    """The tensors lie on the current device, where the call's kernels run."""
+    here = _get_device()
+    for t in (first, *tensors):
+        if t is not None and t.is_cuda and t.get_device() != here:
+            raise ValueError(f"expected tensors on the current device, cuda:{here}")
+
+
+def _route_flags(score: str, renormalize: bool) -> int:
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError(f"score: expected 'softmax' or 'sigmoid', not {score!r}")
+    return (EP_ROUTE_SIGMOID if score == "sigmoid" else 0) | (EP_ROUTE_RENORMALIZE if renormalize else 0)
+
+
+def route(logits: torch.Tensor, topk: int, bias: Optional[torch.Tensor] = None, score: str = "softmax",
+          groups: int = 1, topk_groups: Optional[int] = None, group_best: int = 2, renormalize: bool = True,
+          scale: float = 1.0, topk_idx: Optional[torch.Tensor] = None, topk_weights: Optional[torch.Tensor] = None,
+          return_scores: bool = False, stream=None):
+    """The experts and weights of each token, as dispatch and combine take them.
+
+    logits [tokens, experts] bf16 or fp32 (rows may be slices of a wider
+    tensor). Scores are the softmax over the experts or each one's sigmoid; bias
+    [experts] fp32 is added for the choice alone. groups > 1: only the experts
+    of the topk_groups best groups can be chosen, a group counting as the sum of
+    its best group_best (1 or 2) biased scores. Weights are the chosen scores,
+    divided by their sum with renormalize, times scale. Ties go to the lower
+    index; experts with a logit or bias of -inf or NaN are never chosen, and
+    places that none is left for hold index -1, weight 0. Returns (topk_idx int32
+    [tokens, topk], topk_weights fp32), and the scores fp32 [tokens, experts]
+    with return_scores.
+    """
+    if stream is not None:
+        return _on_stream(stream, route, logits, topk, bias, score, groups, topk_groups, group_best, renormalize, scale,
+                          topk_idx, topk_weights, return_scores)
+    flags = _route_flags(score, renormalize)
+    _same_device(logits, bias, topk_idx, topk_weights)
+    shape = (logits.shape[0], topk)
+    if topk_idx is None:
+        topk_idx = torch.empty(shape, dtype=_I32, device=logits.device)
+    if topk_weights is None:
+        topk_weights = torch.empty(shape, dtype=_F32, device=logits.device)
+    scores = torch.empty(logits.shape, dtype=_F32, device=logits.device) if return_scores else None
+    ep_route(logits, topk, bias, groups, groups if topk_groups is None else topk_groups, group_best, flags, scale,
+             topk_idx, topk_weights, scores)
+    return (topk_idx, topk_weights, scores) if return_scores else (topk_idx, topk_weights)
+
+
+def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor, score: str = "softmax",
+                   renormalize: bool = True, scale: float = 1.0, grad_scores: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """The logits' gradient (their type) from that of route's weights, and of its scores where they were used.
+
+    grad_weights [tokens, topk] fp32 (combine_backward's), grad_scores [tokens,
+    experts] fp32 or None; logits, topk_idx, score, renormalize and scale as in
+    the call of route. The choice of experts has no gradient; nor has the bias.
+    """
+    if stream is not None:
+        return _on_stream(stream, route_backward, grad_weights, logits, topk_idx, score, renormalize, scale, grad_scores,
+                          out, status)
+    flags = _route_flags(score, renormalize)
+    _same_device(logits, grad_weights, topk_idx, grad_scores, out, status)
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    ep_route_backward(grad_weights, grad_scores, logits, topk_idx, flags, scale, out, status)
+    return out
+
+
+def expert_linear_fp8_workspace(x: torch.Tensor, weight: torch.Tensor, max_rows: Optional[int] = None) -> torch.Tensor:
+    """A zero-filled workspace for expert_linear_fp8 (or its backward) of rows shaped like x, to keep between calls."""
+    rows = x.numel() // x.shape[-1] if max_rows is None else int(max_rows)
+    need = ep_expert_linear_fp8_workspace_bytes(weight.shape[0], rows)
+    if need == 0:
+        raise EPError("expert_linear_fp8", EP_ERR_INVALID_ARG)
+    return torch.zeros(need, dtype=torch.uint8, device=x.device)
+
+
+def _expert_linear_fp8(x, x_scale, weight, weight_scale, row_count, row_offset, glu, transposed, use_fp8, round_scale,
+                       use_ue8m0, out, out_scale, max_rows, workspace, status):
+    if weight.dim() != 3 or x.dim() < 2:
+        raise ValueError("weight: expected [experts, out, in], x: [.., channels]")
+    E, M, K = weight.shape
+    if transposed:
+        M, K = K, M
+    rows = x.numel() // K if K else 0
+    lead = x.shape[:-1]
+    if x.shape[-1] != K or x_scale.shape != (*lead, K // 128) or row_count.shape != (E,):
+        raise ValueError("x, x_scale, row_count: expected [.., channels] of the weight's, a scale for each 128 of "
+                         "them, and a count for each expert")
+    parts = 2 if glu else 1
+    blocks = (E, parts * -(-(M // parts) // 128), K // 128)
+    if transposed:
+        blocks = (E, K // 128, -(-M // 128))
+    if weight_scale.shape != blocks:
+        raise ValueError(f"weight_scale: expected shape {blocks}, a scale for each 128 x 128 block")
+    if row_offset is None:
+        if x.dim() != 3 or x.shape[0] != E:
+            raise ValueError("x: expected [num_experts, cap, channels] without row_offset")
+    elif row_offset.numel() < E:
+        raise ValueError("row_offset: expected an offset for each expert")
+    if not use_fp8 and (round_scale or use_ue8m0 or out_scale is not None):
+        raise ValueError("round_scale, use_ue8m0 and out_scale go with use_fp8")
+    shape = (*lead, M // parts)
+    if out is None:
+        out = torch.empty(shape, dtype=_U8 if use_fp8 else _BF16, device=x.device)
+    elif out.shape != shape:
+        raise ValueError(f"out: expected shape {shape}")
+    if use_fp8:
+        shape = (*lead, M // parts // 128)
+        if out_scale is None:
+            out_scale = torch.empty(shape, dtype=_U8 if use_ue8m0 else _F32, device=x.device)
+        elif out_scale.shape != shape:
+            raise ValueError(f"out_scale: expected shape {shape}")
+    _same_device(x, x_scale, weight, weight_scale, row_count, row_offset, out, out_scale, workspace, status)
+    limit = rows if max_rows is None else int(max_rows)
+    if workspace is None:
+        workspace = expert_linear_fp8_workspace(x, weight, limit)
+    flags = (EP_LINEAR_GLU if glu else 0) | (EP_LINEAR_TRANSPOSED if transposed else 0) | \
+        (EP_LINEAR_X_UE8M0 if x_scale.dtype is _U8 else 0)
+    if use_fp8:
+        flags |= EP_LINEAR_OUT_FP8 | (EP_LINEAR_OUT_ROUND_SCALE if round_scale else 0) | \
+            (EP_LINEAR_OUT_UE8M0 if use_ue8m0 else 0)
+    ep_expert_linear_fp8(x, x_scale, rows, K, row_count, row_offset, x.shape[1] if row_offset is None else 0, limit,
+                         weight, weight_scale, M, flags, out, out_scale, workspace, status)
+    return (out, out_scale) if use_fp8 else out
+
+
+def expert_linear_fp8(x: torch.Tensor, x_scale: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor,
+                      row_count: torch.Tensor, row_offset: Optional[torch.Tensor] = None, glu: bool = False,
+                      use_fp8: bool = False, round_scale: bool = False, use_ue8m0: bool = False,
+                      out: Optional[torch.Tensor] = None, out_scale: Optional[torch.Tensor] = None,
+                      max_rows: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None, stream=None):
+    """Each expert's product of its received rows with its 8-bit weights.
+
+    x uint8 (E4M3) with x_scale [.., in/128] fp32 or uint8 (UE8M0), as the FP8
+    dispatches deliver them: the expert-major buffer [rows, in] with row_offset
+    = expert_offset, or the low-latency [E, cap, in] (row_offset None). weight
+    [E, out, in] uint8 (E4M3), weight_scale [E, ceil(out/128), in/128] fp32. glu:
+    y = silu(gate) * up of the two halves of the outputs, each half with blocks
+    of its own. Returns bf16 rows, or with use_fp8 (E4M3 uint8, scales [..,
+    outputs/128] fp32 or UE8M0): what the next product takes. Rows that no expert
+    received are left as they are in out. max_rows bounds the rows received by
+    all experts, as for expert_linear; a workspace that is kept need not be
+    zero-filled at each call.
+    """
+    if stream is not None:
+        return _on_stream(stream, expert_linear_fp8, x, x_scale, weight, weight_scale, row_count, row_offset, glu,
+                          use_fp8, round_scale, use_ue8m0, out, out_scale, max_rows, workspace, status)
+    return _expert_linear_fp8(x, x_scale, weight, weight_scale, row_count, row_offset, glu, False, use_fp8, round_scale,
+                              use_ue8m0, out, out_scale, max_rows, workspace, status)
+
+
+def expert_linear_fp8_backward(grad_y: torch.Tensor, grad_scale: torch.Tensor, weight: torch.Tensor,
+                               weight_scale: torch.Tensor, row_count: torch.Tensor,
+                               row_offset: Optional[torch.Tensor] = None, use_fp8: bool = False,
+                               round_scale: bool = False, use_ue8m0: bool = False, out: Optional[torch.Tensor] = None,
+                               out_scale: Optional[torch.Tensor] = None, max_rows: Optional[int] = None,
+                               workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                               stream=None):
+    """The gradient of expert_linear_fp8's rows (without glu): each row of grad_y times its expert's weights.
+
+    grad_y [.., out] uint8 (E4M3) with grad_scale [.., out/128] fp32 or UE8M0
+    (ep_fp8_quantize makes them of a bf16 gradient); weight [E, out, in] and
+    weight_scale as in the product, out and in multiples of 128. The rest as
+    there. Returns [.., in] bf16, or (E4M3, scales) with use_fp8. The weights are
+    taken as constants.
+    """
+    if stream is not None:
+        return _on_stream(stream, expert_linear_fp8_backward, grad_y, grad_scale, weight, weight_scale, row_count,
+                          row_offset, use_fp8, round_scale, use_ue8m0, out, out_scale, max_rows, workspace, status)
+    return _expert_linear_fp8(grad_y, grad_scale, weight, weight_scale, row_count, row_offset, False, True, use_fp8,
+                              round_scale, use_ue8m0, out, out_scale, max_rows, workspace, status)

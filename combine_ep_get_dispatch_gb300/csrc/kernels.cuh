@@ -271,10 +271,53 @@ struct ExpertLinearParams {
   int32_t* status;
 };
 
+struct RouteParams {
+  const void* logits;        // [N, E] BF16 or fp32, rows `stride` elements apart
+  int64_t stride;
+  int N, E, K;
+  int bf16, sigmoid, renormalize;
+  float scale;
+  // forward
+  const float* bias;         // [E] or null
+  int groups, topk_groups, group_best;  // groups == 1: none
+  int32_t* idx;              // [N, K]
+  float* weights;            // [N, K]
+  float* scores;             // [N, E] or null
+  // backward
+  const float* grad_weights; // [N, K]
+  const float* grad_scores;  // [N, E] or null
+  const int32_t* chosen;     // [N, K]
+  void* grad_logits;         // [N, E], the logits' type
+  int32_t* status;
+};
+
+struct ExpertLinearFp8Params {
+  const uint8_t* x;
+  const void* x_scale;       // fp32, or UE8M0 bytes with x_ue8m0
+  int64_t x_rows;
+  const int32_t* count;      // [E]
+  const int32_t* offset;     // [E], or null: e * region
+  int64_t region;
+  int E, K, M;               // K channels of a row of x, M outputs (gates and ups together)
+  int glu, transposed, x_ue8m0;
+  int out_fp8, out_pow2, out_ue8m0;
+  int64_t max_rows;
+  const uint8_t* w;          // [E, M, K]; transposed [E, K, M]
+  const float* w_scale;
+  void* y;
+  void* y_scale;
+  uint8_t* ws;
+  int32_t* status;
+};
+
 cudaError_t launch_kv_append(const KVAppendParams& p, cudaStream_t s);
 size_t kv_attention_ws_bytes(int N, int QH, int KH, int D);
 cudaError_t launch_kv_attention(const KVAttentionParams& p, cudaStream_t s);
 size_t expert_linear_ws_bytes(int E, int64_t max_rows, int K, bool fp8);
 cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s);
+cudaError_t launch_route(const RouteParams& p, cudaStream_t s);
+cudaError_t launch_route_backward(const RouteParams& p, cudaStream_t s);
+size_t expert_linear_fp8_ws_bytes(int E, int64_t max_rows);
+cudaError_t launch_expert_linear_fp8(const ExpertLinearFp8Params& p, cudaStream_t s);
 
 }  // namespace ep

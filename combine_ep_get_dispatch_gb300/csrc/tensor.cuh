@@ -51,6 +51,17 @@ __device__ __forceinline__ bool all_agree(bool ok) {
   return r != 0;
 }
 
+// Registers of a warpgroup's threads, taken from or given back to what the
+// block was launched with (all four warps call it).
+template <int kRegs>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // Whether the phase has completed, without waiting: non-zero. The answer takes
 // about 100 cycles, so a loop that has other work asks a turn ahead (raw, and
 // mbar_wait_asked when it needs to know) instead of standing still.
@@ -97,6 +108,19 @@ __device__ __forceinline__ void tmem_load8(float* v, uint32_t addr) {
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 32 columns of it.
+__device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ---- shared-memory matrix descriptors ----------------------------------------
@@ -105,6 +129,14 @@ __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::l
 __device__ __forceinline__ uint64_t desc_rows128(uint32_t addr) {
   return (static_cast<uint64_t>(addr) >> 4 & 0x3FFF) | uint64_t(1) << 16 | uint64_t(1024 >> 4) << 32 |
          uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+
+// The transposed operand: rows of 128 bytes along the outputs, one row an
+// input, in the same swizzle; groups of eight inputs lie 1024 bytes apart,
+// groups of 128 outputs `apart` bytes.
+__device__ __forceinline__ uint64_t desc_inputs128(uint32_t addr, uint32_t apart) {
+  return (static_cast<uint64_t>(addr) >> 4 & 0x3FFF) | static_cast<uint64_t>(apart >> 4) << 16 |
+         uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
 }
 
 // Rows of 16 bytes one after the other (the scale factors' 32 x 128 bits).
@@ -141,6 +173,23 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
       : "memory");
 }
 
+// ---- product of 8-bit operands ---------------------------------------------------
+// D[128, N] (+)= A[128, 32] B[N, 32]^T, both E4M3, fp32 sums. The instruction
+// descriptor: fp32 sums (1) at bit 4, the operands' types (0: E4M3) at 7 and 10,
+// B transposed at 16, N / 8 at 17, M / 16 at 24.
+__device__ __forceinline__ uint32_t idesc_e4m3(int n, bool b_transposed) {
+  return 1u << 4 | (b_transposed ? 1u << 16 : 0u) | static_cast<uint32_t>(n / 8) << 17 | (128u / 16u) << 24;
+}
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
 // Arrive on an mbarrier once every product and copy issued so far by this
 // thread has completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -170,6 +219,15 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           smem_addr(smem_dst)),
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(smem_dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
       : "memory");
 }
 

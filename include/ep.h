@@ -724,6 +724,129 @@ int ep_expert_linear(const void* x, const uint8_t* x_scale, int64_t x_rows, int 
                      int64_t max_rows, const uint8_t* w, const uint8_t* w_scale, int out_features, int flags, void* y,
                      void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
+/*
+ * ---- the router ------------------------------------------------------------
+ * From a token's router logits z to the experts and weights that dispatch and
+ * combine take ("DeepSeek DeepEP lesson 14", practice task: softmax, top-k,
+ * renormalised weights; "DeepEP V1 (legacy) guide", sections 1 and 2.1:
+ * group-limited gating), and back.
+ */
+
+/* Flags of ep_route and ep_route_backward. */
+#define EP_ROUTE_BF16 0x1        /* logits (and their gradient) are BF16, not fp32 */
+#define EP_ROUTE_SIGMOID 0x2     /* scores are sigmoid(z), not softmax(z) */
+#define EP_ROUTE_RENORMALIZE 0x4 /* a token's weights are divided by their sum */
+#define EP_MAX_ROUTE_GROUPS 32
+
+/*
+ * Scores s = softmax(z) over the experts, or sigmoid(z); c = s + bias is what
+ * experts are chosen by. With num_groups > 1 the experts form groups of
+ * num_experts / num_groups neighbours; a group counts as the sum of its best
+ * group_best values of c (of those it has), and only the experts of the
+ * topk_groups best groups can be chosen. The num_topk experts with the largest c
+ * are chosen, best first. Equal values (of groups, of experts) go to the lower
+ * index; values closer than fp32 can tell are compared in 64 bits, so that the
+ * choice is that of the formula. The weights are the chosen experts' scores,
+ * without the bias: w_k = scale * s_k / (sum_j s_j + 1e-20) with
+ * EP_ROUTE_RENORMALIZE, otherwise scale * s_k.
+ *
+ * An expert whose logit or bias is -inf or NaN is never chosen, and a NaN has
+ * score 0 and no part in the softmax. A token with fewer than num_topk experts
+ * to choose from gets index -1 and weight 0 in the places that remain.
+ * Several logits of +inf share the softmax.
+ *
+ *   logits         [num_tokens, num_experts] fp32 or BF16, tokens logits_stride
+ *                  elements apart (>= num_experts), experts contiguous
+ *   bias           [num_experts] fp32, or NULL
+ *   num_experts    <= EP_MAX_EXPERTS, a multiple of num_groups
+ *   num_groups     <= EP_MAX_ROUTE_GROUPS; 1 <= topk_groups <= num_groups
+ *   num_topk       <= EP_MAX_TOPK, <= num_experts
+ *   group_best     1 or 2
+ *   topk_idx       [num_tokens, num_topk] int32
+ *   topk_weights   [num_tokens, num_topk] fp32
+ *   scores         [num_tokens, num_experts] fp32: every s (a balance loss), or NULL
+ */
+int ep_route(const void* logits, int64_t logits_stride, int num_tokens, int num_experts, int num_topk, const float* bias,
+             int num_groups, int topk_groups, int group_best, int flags, float scale, int32_t* topk_idx,
+             float* topk_weights, float* scores, void* stream);
+
+/*
+ * Gradient of ep_route's weights (and scores) with respect to the logits, the
+ * choice of experts fixed. With dw the weights' gradient (ep_combine_backward's
+ * grad_w), S = sum_j s_j + 1e-20 over the chosen and w'_j = s_j / S, a chosen
+ * expert's score has ds_k = scale / S * (dw_k - sum_j dw_j w'_j), or scale * dw_k
+ * without EP_ROUTE_RENORMALIZE, and every score grad_scores besides. Then
+ * dz_i = s_i (ds_i - sum_j s_j ds_j) for the softmax, s_i (1 - s_i) ds_i for the
+ * sigmoid; sums in fp32, rounded once to the logits' type. The scores are
+ * computed from the logits anew. An index -1 adds nothing; an expert that a
+ * token names twice gets both gradients.
+ *
+ *   grad_weights   [num_tokens, num_topk] fp32
+ *   grad_scores    [num_tokens, num_experts] fp32, or NULL
+ *   logits, topk_idx  as ep_route took and gave them
+ *   grad_logits    [num_tokens, num_experts] in the logits' type
+ *   status         EP_ST_BAD_INDEX: an index outside [-1, num_experts), taken as -1
+ */
+int ep_route_backward(const float* grad_weights, const float* grad_scores, const void* logits, int64_t logits_stride,
+                      const int32_t* topk_idx, int num_tokens, int num_experts, int num_topk, int flags, float scale,
+                      void* grad_logits, int32_t* status, void* stream);
+
+/* Flags of ep_expert_linear_fp8, besides EP_LINEAR_GLU. */
+#define EP_LINEAR_TRANSPOSED 0x2      /* y = x W: the gradient of y = x W^T with respect to x */
+#define EP_LINEAR_X_UE8M0 0x4         /* x_scale holds UE8M0 bytes, not fp32 */
+#define EP_LINEAR_OUT_FP8 0x8         /* y in E4M3 with a scale for each 128 outputs, not BF16 */
+#define EP_LINEAR_OUT_ROUND_SCALE 0x10 /* ... the scales raised to powers of two */
+#define EP_LINEAR_OUT_UE8M0 0x20      /* ... and stored as UE8M0 bytes */
+
+/* Bytes of device workspace ep_expert_linear_fp8 needs (0: sizes out of range).
+ * Depends only on the arguments. */
+size_t ep_expert_linear_fp8_workspace_bytes(int num_experts, int64_t max_rows);
+
+/*
+ * The experts' products with 8-bit weights: for each expert e and each row j it
+ * received, y_row = x_row W_e^T, with x in E4M3 and a scale for each 128
+ * channels of a row (what the FP8 dispatch delivers), W_e [out_features,
+ * in_features] in E4M3 and a scale for each 128 x 128 block:
+ *   y[r, o] = sum_b (x_scale[r, b] * w_scale[e, o / 128, b]) * sum_{k in b} x[r, k] w[e, o, k].
+ * Sums are fp32, as is the product of the two scales, which has to be a finite
+ * number (a block of zeros may have the scale 0). With EP_LINEAR_GLU, W_e's first out_features / 2 rows are gates g and the
+ * others u, and y = silu(g) * u in fp32; gates and ups then have blocks of their
+ * own. y is rounded once: to BF16, or with EP_LINEAR_OUT_FP8 to E4M3 by the rule
+ * of ep_fp8_quantize applied to the fp32 values (one scale for each 128 outputs
+ * of a row), which is the next product's x.
+ *
+ * With EP_LINEAR_TRANSPOSED, y_row = x_row W_e for W_e [in_features,
+ * out_features]: given the E4M3 gradient of a product's outputs as x, and that
+ * product's w and w_scale as they are, y is the gradient of its rows.
+ *
+ * Rows: as for ep_expert_linear (row_count, row_offset or rows_per_expert,
+ * max_rows); rows that no expert received are not written.
+ *
+ *   x             [x_rows, in_features] E4M3, x_rows <= INT32_MAX
+ *   x_scale       [x_rows, in_features / 128] fp32, or UE8M0 bytes
+ *   in_features   a multiple of 128, <= EP_MAX_HIDDEN
+ *   out_features  a multiple of 8, or of 128 with EP_LINEAR_TRANSPOSED or
+ *                 EP_LINEAR_OUT_FP8 (twice that with EP_LINEAR_GLU), <= 2^20
+ *   w             [num_experts, out_features, in_features] E4M3, 16-byte aligned
+ *                 (transposed: [num_experts, in_features, out_features])
+ *   w_scale       [num_experts, ceil(out_features / 128), in_features / 128] fp32
+ *                 (with EP_LINEAR_GLU 2 * ceil(out_features / 2 / 128) rows of
+ *                 blocks; transposed: [num_experts, in_features / 128, out_features / 128])
+ *   y             [x_rows, out_features (/ 2 with EP_LINEAR_GLU)] BF16 or E4M3
+ *   y_scale       [x_rows, outputs / 128] fp32 or UE8M0 bytes, with EP_LINEAR_OUT_FP8
+ *   workspace     at least ep_expert_linear_fp8_workspace_bytes(...) bytes, 256-byte
+ *                 aligned, zero-filled before its first use; every call leaves it
+ *                 ready for the next. Not to be shared by calls in flight.
+ *   status        EP_ST_CAPACITY: rows outside x, or more than max_rows;
+ *                 EP_ST_TIMEOUT: a bounded wait gave up, results are wrong and the
+ *                 workspace has to be zero-filled again
+ * The result does not depend on the order in which blocks run.
+ */
+int ep_expert_linear_fp8(const uint8_t* x, const void* x_scale, int64_t x_rows, int in_features,
+                         const int32_t* row_count, const int32_t* row_offset, int64_t rows_per_expert, int num_experts,
+                         int64_t max_rows, const uint8_t* w, const float* w_scale, int out_features, int flags, void* y,
+                         void* y_scale, void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -99,6 +99,7 @@ int ep_expert_linear_fp8(const uint8_t* x, const void* x_scale, int64_t x_rows, 
   if (in_features < 128 || in_features > EP_MAX_HIDDEN || in_features % 128 != 0) return EP_ERR_INVALID_ARG;
   const int unit = (fp8 || transposed ? 128 : 8) * (glu ? 2 : 1);
   if (out_features < unit || out_features > (1 << 20) || out_features % unit != 0) return EP_ERR_INVALID_ARG;
+  if (!expert_linear_fp8_units_ok(num_experts, max_rows, out_features, glu)) return EP_ERR_INVALID_ARG;
   if (!row_offset && (rows_per_expert < 0 || rows_per_expert > INT32_MAX)) return EP_ERR_INVALID_ARG;
   if (!row_count || !w || !w_scale) return EP_ERR_INVALID_ARG;
   if (x_rows > 0 && max_rows > 0 && (!x || !x_scale || !y || (fp8 && !y_scale))) return EP_ERR_INVALID_ARG;

@@ -47,6 +47,9 @@ constexpr int kResultThreads = 256;
 constexpr int kMaxStages = 8;
 constexpr int kTmemCols = 512;          // two steps' sums
 constexpr int kMinStages = 2;           // fewest steps worth a block of their own
+constexpr int kMaxParts = 4;            // most blocks that share a unit
+constexpr int kJobs = 4;                // jobs between the loads and the results
+constexpr int kTakeAhead = 8;           // steps before a unit's end at which the next is taken
 constexpr int kAhead = 4;               // steps' scales in flight
 // Registers of a thread: 168 at launch, of which four warps give 80 each to the
 // eight that hold the sums (3 x 168 = 88 + 2 x 208).
@@ -57,18 +60,29 @@ struct Params {
   int mult;       // columns a row (expert_tiles.cuh): 1
   int tile_rows;  // rows of a full tile
   int KB;         // steps of a unit
-  int KS;         // the same: a stage holds one step
+  int KS;         // the same
   int MT;         // units of a tile: an expert's output tiles
   int stages;
   unsigned stage_bytes;
   int scale_rows, scale_cols;  // blocks of W in either direction
-  unsigned* counters;          // [kMaxBlocks]
+  unsigned* counters;          // [kMaxBlocks]: arrivals at a shared unit
+  unsigned* taken;             // whole units that blocks have taken, and blocks that are done
   float* partial;              // [kMaxBlocks][2][tile_rows][kTileN]
+};
+
+// A run of steps of one unit, as the loading warp passes it on.
+struct Job {
+  int steps;        // 0: no more jobs
+  int e, mt, s0;    // expert, output tile, first step
+  int row, rows;    // the tile's rows: the first, in x, and how many
+  int first, last;  // the blocks that share the unit
 };
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2];
+  uint64_t job_full[kJobs], job_empty[kJobs];
+  Job job[kJobs];
   uint32_t tmem;
   int last;                            // this block is the last to finish its shared unit
   Scan<kThreads> scan;
@@ -80,7 +94,91 @@ struct RowMaps {
   CUtensorMap box[kRowMaps];
 };
 
+// How the blocks share the units. As many as make full rounds of all blocks are
+// taken whole, one after the other as blocks become free; so units that follow
+// one another are worked on at the same time, and what they share (rows that read
+// the same weights, outputs that read the same rows) comes from HBM once. The
+// rest comes first, cut into equal runs of steps. (With every unit in one such cut
+// the blocks were at different places of their units and of the list: 32 experts
+// of 2048 rows, 7168 inputs, 4096 outputs took 2650 us. With a fixed list for each
+// block they drifted apart: 256 experts of about 128 rows read 9.6 GB where 7.8 must
+// be, and took 1498 us.)
+struct Share {
+  int units, KS, blocks;
+  int cut, cutters;  // units that are cut, blocks that share them
+  int at, end;       // this block's steps of them
+  __device__ Share(int units, int KS, int blocks, int me) : units(units), KS(KS), blocks(blocks) {
+    cut = units % blocks;
+    // Every block that takes part has steps: the join counts on it. (Of 32 experts
+    // of 128 rows 8 units are left to cut: in us, shared by 2, 4, 8, 16 and 19 blocks
+    // each, 232, 229, 237, 260 and 273; 2 units of 8 rows alone 22, 17, 18, 26, 38.)
+    cutters = min(min(blocks, kMaxParts * cut), max(cut * KS / kMinStages, 1));
+    at = end = 0;
+    if (me < cutters) {
+      at = begin(me);
+      end = begin(me + 1);
+    }
+  }
+  __device__ __forceinline__ int begin(int block) const {
+    return cut * KS * block / cutters;  // (below 160 * 128 * 160)
+  }
+  // The block that has step i of the cut units.
+  __device__ __forceinline__ int owner(int i) const {
+    const int total = cut * KS;
+    return ((i + 1) * cutters + total - 1) / total - 1;
+  }
+};
+
+// Where a unit lies, by a whole warp. An expert's tiles share its rows evenly:
+// blocks that work on tiles of different sizes drift apart (256 experts of about
+// 128 rows: 1783 us with tiles of 128 rows and the rest, 1498 so).
+__device__ __forceinline__ void locate(const Params& q, const Tables& tb, int unit, Job& j) {
+  j.e = uniform(expert_of(tb.tile0, q.p.E, unit / q.MT));
+  const int tile0 = uniform(tb.tile0[j.e]), tiles = uniform(tb.tile0[j.e + 1]) - tile0;
+  const int u = unit - tile0 * q.MT;
+  j.mt = u / tiles;
+  const int rows = uniform(tb.rows[j.e]), per = (rows + tiles - 1) / tiles, row = (u - j.mt * tiles) * per;
+  j.row = static_cast<int>(uniform(first_row(q.p, j.e))) + row;
+  j.rows = min(per, rows - row);
+}
+
+// A warp's place in the list of jobs.
+struct Jobs {
+  int at = 0;
+  unsigned parity = 0;
+  // Whether there is a next job, at job[at]; by a whole warp (false too if the wait
+  // has run out). done() gives its place back.
+  __device__ __forceinline__ bool next(Shared& sh, int32_t* status) {
+    return mbar_wait_warp(&sh.job_full[at], parity, status) && uniform(sh.job[at].steps) > 0;
+  }
+  __device__ __forceinline__ void done(Shared& sh) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.job_empty[at]);
+    advance();
+  }
+  __device__ __forceinline__ void advance() {
+    if (++at == kJobs) {
+      at = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 __device__ __forceinline__ void result_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Whether all of the results' threads go on: none may leave alone.
+__device__ __forceinline__ bool results_agree(bool ok) {
+  unsigned r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
 
 // 32 columns of tensor memory have arrived in r.
 __device__ __forceinline__ void arrived(uint32_t (&r)[32]) {
@@ -106,6 +204,15 @@ __device__ __forceinline__ float row_scale(const ExpertLinearFp8Params& p, int64
   if (!p.x_ue8m0) return __ldg(static_cast<const float*>(p.x_scale) + at);
   const uint32_t b = __ldg(static_cast<const uint8_t*>(p.x_scale) + at);
   return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FC00000u : b << 23);
+}
+
+// silu(g): the exponential within 2 ulp, the reciprocal within 1, and no branch.
+// (With an IEEE division, whose rare cases are a call, a unit's 64 gates and 64
+// quotients a thread took as long as the products of 30 steps.)
+__device__ __forceinline__ float silu(float g) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(1.0f + expf(-g)));
+  return g * y;
 }
 
 // Eight results to BF16.
@@ -138,15 +245,31 @@ __device__ __forceinline__ void store_fp8(const ExpertLinearFp8Params& p, const 
   if (p.out_pow2 && sc > 0.0f) sc = pow2_ceil(sc);
   if (p.out_ue8m0 && m > 0.0f) sc = fmaxf(sc, __uint_as_float(0x00400000u));  // 2^-127
   uint8_t* to = static_cast<uint8_t*>(p.y) + row * outs + o;
-  const float d = sc > 0.0f ? sc : 1.0f;
+  // v / s, correctly rounded: from one correctly rounded reciprocal y the quotient
+  // v y is within an ulp, its remainder v - s v y is exact by a fused
+  // multiply-add, and v y + remainder y rounds to v / s (Markstein, "Computation of
+  // elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev.
+  // 34(1), 1990), as long as the remainder does not underflow where a code is not
+  // a zero (s >= 2^-92) and y is a normal number (s <= 2^126).
+  const bool quick = sc >= 0x1p-92f && sc <= 0x1p126f;
+  const float y = quick ? __frcp_rn(sc) : 0.0f;
 #pragma unroll
   for (int i = 0; i < 64; i += 16) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float* u = v + i + 4 * j;
-      w[j] = pack_e4m3x2(__fdiv_rn(u[0], d), __fdiv_rn(u[1], d)) |
-             pack_e4m3x2(__fdiv_rn(u[2], d), __fdiv_rn(u[3], d)) << 16;
+      float u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x = v[i + 4 * j + k];
+        if (quick) {
+          const float t = x * y;
+          u[k] = copysignf(fmaf(fmaf(-sc, t, x), y, t), x);  // (a zero keeps its sign)
+        } else {
+          u[k] = sc > 0.0f ? __fdiv_rn(x, sc) : x;
+        }
+      }
+      w[j] = pack_e4m3x2(u[0], u[1]) | pack_e4m3x2(u[2], u[3]) << 16;
     }
     *reinterpret_cast<uint4*>(to + i) = make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -158,7 +281,6 @@ __device__ __forceinline__ void store_fp8(const ExpertLinearFp8Params& p, const 
     static_cast<float*>(p.y_scale)[at] = sc;
 }
 
-template <bool kTogether>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_linear_fp8_kernel(const Params q, const __grid_constant__ CUtensorMap map,
                              const __grid_constant__ RowMaps maps) {
@@ -178,6 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.acc_full[i], 1 + 2);   // the products, two warps of scales
       mbar_init(&sh.acc_empty[i], kResultThreads / 32);
     }
+    for (int i = 0; i < kJobs; ++i) {
+      mbar_init(&sh.job_full[i], 1);
+      mbar_init(&sh.job_empty[i], 1 + 2 + kResultThreads / 32);
+    }
     fence_mbar_init();
   }
   if (warp == 3) tmem_alloc(&sh.tmem, kTmemCols);
@@ -188,15 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = uniform(sh.tmem);
-  const int64_t total = static_cast<int64_t>(uniform(tb.tile0[p.E])) * q.MT * q.KS;
   const int outs = p.glu ? p.M / 2 : p.M;
-  // Every block that takes part has steps: the join counts on it.
-  const int me = static_cast<int>(blockIdx.x);
-  const int blocks = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(total / kMinStages, int64_t{1})));
-  const Order order(static_cast<unsigned>(uniform(tb.tile0[p.E]) * q.MT), blocks);
-  Run run{0, 0};
-  if (me < blocks) run = Run{run_begin(total, blocks, me), run_begin(total, blocks, me + 1)};
-  const unsigned steps = static_cast<unsigned>(run.end - run.at);
   // A stage: rows of x, then weights (a product always reads 128 rows: with
   // fewer, the lanes behind them hold nothing that is looked at).
   const unsigned w_at = static_cast<unsigned>(q.tile_rows) * kStep;
@@ -204,35 +322,74 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     give_registers<kLoadRegs>();
     if (warp == 0) {
-      // Loads.
-      Segment g;
+      // Loads. This warp finds the block's jobs and passes them on.
+      Share share(uniform(tb.tile0[p.E]) * q.MT, q.KS, gridDim.x, blockIdx.x);
       Ring r;
-      bool again = false;  // the ring has been filled once
-      bool ok = true;
-      while (ok && next_segment<kTogether>(q, tb, order, run, g)) {
-        const int boxes = (g.rows + 15) / 16;
+      Jobs jobs;
+      bool again = false, jobs_again = false;  // the rings have been filled once
+      int next = 0;                            // the next whole unit, in the first lane
+      auto take = [&]() {
+        if (lane == 0) next = share.cut + static_cast<int>(atomicAdd(q.taken, 1u));
+      };
+      auto pass_on = [&](const Job& j) {
+        if (jobs_again && !mbar_wait_warp(&sh.job_empty[jobs.at], jobs.parity ^ 1, p.status)) return false;
+        if (lane == 0) {
+          sh.job[jobs.at] = j;
+          mbar_arrive(&sh.job_full[jobs.at]);
+        }
+        __syncwarp();
+        jobs.advance();
+        if (jobs.at == 0) jobs_again = true;
+        return true;
+      };
+      auto load = [&](const Job& j, int take_at) {
+        const int boxes = (j.rows + 15) / 16;
         const unsigned bytes = kTileBytes + boxes * 16 * kStep;
         const CUtensorMap* box = &maps.box[boxes - 1];
-        const int row = static_cast<int>(uniform(first_row(p, g.e))) + g.tile * q.tile_rows;
-        for (int st = g.s0; st < g.s1; ++st) {
-          if (again && !mbar_wait_warp(&sh.empty[r.stage], r.parity ^ 1, p.status)) {
-            ok = false;
-            break;
-          }
+        for (int st = j.s0; st < j.s0 + j.steps; ++st) {
+          if (st == take_at) take();
+          if (again && !mbar_wait_warp(&sh.empty[r.stage], r.parity ^ 1, p.status)) return false;
           if (elect_one()) {
             uint64_t* bar = &sh.full[r.stage];
             uint8_t* to = smem + r.offset;
             mbar_arrive_expect_tx(bar, bytes);
             if (p.transposed)
-              tma_load_4d(to + w_at, &map, 0, st * kStep, g.mt * 2, g.e, bar);
+              tma_load_4d(to + w_at, &map, 0, st * kStep, j.mt * 2, j.e, bar);
             else
-              tma_load_4d(to + w_at, &map, st * kStep, g.mt * (p.glu ? kBlock : kTileN), 0, g.e, bar);
-            tma_load_2d(to, box, st * kStep, row, bar);
+              tma_load_4d(to + w_at, &map, st * kStep, j.mt * (p.glu ? kBlock : kTileN), 0, j.e, bar);
+            tma_load_2d(to, box, st * kStep, j.row, bar);
           }
           __syncwarp();
           r.advance(q);
           if (r.stage == 0) again = true;
         }
+        return true;
+      };
+      take();
+      bool ok = true;
+      while (ok) {
+        Job j;
+        int take_at = -1;
+        if (share.at < share.end) {
+          const int unit = share.at / q.KS, at = unit * q.KS;
+          locate(q, tb, unit, j);
+          j.s0 = share.at - at;
+          j.steps = min(q.KS - j.s0, share.end - share.at);
+          j.first = share.owner(at);
+          j.last = share.owner(at + q.KS - 1);
+          share.at += j.steps;
+        } else {
+          const int unit = uniform(next);
+          j.s0 = j.first = j.last = 0;
+          j.steps = 0;
+          if (unit < share.units) {
+            locate(q, tb, unit, j);
+            j.steps = q.KS;
+            take_at = max(q.KS - kTakeAhead, 0);
+          }
+        }
+        ok = pass_on(j) && load(j, take_at);
+        if (j.steps == 0) break;
       }
       if (!ok) {  // given up: loads in flight land before the block ends
         for (int i = 0; i < q.stages; ++i) mbar_drain(&sh.full[i], i < r.stage ? r.parity : r.parity ^ 1);
@@ -244,73 +401,89 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t b0 = p.transposed ? desc_inputs128(base + w_at, kBlock * kStep) : desc_rows128(base + w_at);
       // 32 inputs on: 32 bytes of a row, or 32 rows of 128 bytes.
       const unsigned b_step = (p.transposed ? 32 * 128 : 32) >> 4;
-      const uint32_t idesc = idesc_e4m3(kTileN, p.transposed);
+      const uint32_t idesc = idesc_e4m3(kTileRows, kTileN, p.transposed);
+      Jobs jobs;
       Ring r;
-      for (unsigned i = 0; i < steps; ++i) {
-        const unsigned half = i & 1;
-        if (i >= 2 && !mbar_wait_warp(&sh.acc_empty[half], (i / 2 - 1) & 1, p.status)) break;
-        if (!mbar_wait_warp(&sh.full[r.stage], r.parity, p.status)) {
-          mbar_drain(&sh.full[r.stage], r.parity);
-          break;
-        }
-        tmem_fence_after();
-        if (elect_one()) {
-          const uint64_t a = a0 + (r.offset >> 4), b = b0 + (r.offset >> 4);
-          const uint32_t d = tmem + half * kTileN;
+      unsigned i = 0;
+      bool ok = true;
+      while (ok && jobs.next(sh, p.status)) {
+        const unsigned end = i + uniform(sh.job[jobs.at].steps);
+        jobs.done(sh);
+        for (; i < end; ++i) {
+          const unsigned half = i & 1;
+          if (!mbar_wait_warp(&sh.full[r.stage], r.parity, p.status)) {
+            mbar_drain(&sh.full[r.stage], r.parity);
+            ok = false;
+            break;
+          }
+          if (i >= 2 && !mbar_wait_warp(&sh.acc_empty[half], (i / 2 - 1) & 1, p.status)) {
+            ok = false;
+            break;
+          }
+          tmem_fence_after();
+          if (elect_one()) {
+            const uint64_t a = a0 + (r.offset >> 4), b = b0 + (r.offset >> 4);
+            const uint32_t d = tmem + half * kTileN;
 #pragma unroll
-          for (unsigned j = 0; j < kStep / 32; ++j) mma_e4m3(d, a + 2 * j, b + b_step * j, idesc, j > 0);
-          mma_commit(&sh.empty[r.stage]);
-          mma_commit(&sh.acc_full[half]);
+            for (unsigned j = 0; j < kStep / 32; ++j) mma_e4m3(d, a + 2 * j, b + b_step * j, idesc, j > 0);
+            mma_commit(&sh.empty[r.stage]);
+            mma_commit(&sh.acc_full[half]);
+          }
+          __syncwarp();
+          r.advance(q);
         }
-        __syncwarp();
-        r.advance(q);
       }
     } else {
       // Scales: each lane of the two warps the products of two rows' scales with
       // the weights' for 2 x 128 outputs. Their loads run kAhead steps ahead, across units.
       const int t = tid - 64;
-      Segment g;
-      int st = 0;
-      bool more = next_segment<kTogether>(q, tb, order, run, g);
-      int64_t xa = 0, wa = 0;
-      int w_next = 0, w_second = 0;
-      auto enter = [&]() {
-        st = g.s0;
-        xa = (first_row(p, g.e) + g.tile * q.tile_rows + t) * q.KB;
-        const int64_t e = static_cast<int64_t>(g.e) * q.scale_rows * q.scale_cols;
-        const int b = p.glu ? g.mt : 2 * g.mt;  // first of the unit's two blocks of outputs
-        if (p.transposed) {
-          wa = e + b;
-          w_next = q.scale_cols;
-          w_second = b + 1 < q.scale_cols ? 1 : 0;
-        } else {
-          wa = e + static_cast<int64_t>(b) * q.scale_cols;
-          w_next = 1;
-          w_second = p.glu ? q.scale_rows / 2 * q.scale_cols : b + 1 < q.scale_rows ? q.scale_cols : 0;
-        }
-      };
-      if (more) enter();
+      Jobs jobs;
+      bool more = true;
+      int left = 0, rows = 0;       // of the job: steps, rows
+      int64_t xa = 0;               // the next step's first scale of x,
+      const float* w = nullptr;     // and of the weights,
+      int w_next = 0, w_second = 0; // how far the next and the second 128 outputs' are
       float x0[kAhead], x1[kAhead], w0[kAhead], w1[kAhead];
+      unsigned fetched = 0;
       auto fetch = [&](int i) {
         if (!more) return;
-        x0[i] = t < g.rows ? row_scale(p, xa + st) : 0.0f;
-        x1[i] = t + 64 < g.rows ? row_scale(p, xa + 64 * static_cast<int64_t>(q.KB) + st) : 0.0f;
-        const float* w = p.w_scale + wa + static_cast<int64_t>(st) * w_next;
+        if (left == 0) {
+          more = jobs.next(sh, p.status);
+          if (!more) return;
+          const Job& j = sh.job[jobs.at];
+          left = j.steps;
+          rows = j.rows;
+          xa = static_cast<int64_t>(j.row + t) * q.KB + j.s0;
+          w = p.w_scale + static_cast<int64_t>(j.e) * q.scale_rows * q.scale_cols;
+          const int b = p.glu ? j.mt : 2 * j.mt;  // first of the unit's two blocks of outputs
+          if (p.transposed) {
+            w += static_cast<int64_t>(j.s0) * q.scale_cols + b;
+            w_next = q.scale_cols;
+            w_second = b + 1 < q.scale_cols ? 1 : 0;
+          } else {
+            w += static_cast<int64_t>(b) * q.scale_cols + j.s0;
+            w_next = 1;
+            w_second = p.glu ? q.scale_rows / 2 * q.scale_cols : b + 1 < q.scale_rows ? q.scale_cols : 0;
+          }
+          jobs.done(sh);
+        }
+        x0[i] = t < rows ? row_scale(p, xa) : 0.0f;
+        x1[i] = t + 64 < rows ? row_scale(p, xa + 64 * static_cast<int64_t>(q.KB)) : 0.0f;
         w0[i] = __ldg(w);
         w1[i] = __ldg(w + w_second);
-        if (++st == g.s1) {
-          more = next_segment<kTogether>(q, tb, order, run, g);
-          if (more) enter();
-        }
+        ++xa;
+        w += w_next;
+        --left;
+        ++fetched;
       };
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) fetch(i);
       bool ok = true;
-      for (unsigned i0 = 0; ok && i0 < steps; i0 += kAhead) {
+      for (unsigned i0 = 0; ok && i0 < fetched; i0 += kAhead) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           const unsigned i = i0 + j, half = i & 1;
-          if (!ok || i >= steps) continue;
+          if (!ok || i >= fetched) continue;
           if (i >= 2) ok = mbar_wait_warp(&sh.acc_empty[half], (i / 2 - 1) & 1, p.status);
           if (!ok) continue;
           sh.scale[half][0][t] = x0[j] * w0[j];
@@ -329,15 +502,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // that its warpgroup has.
     const int group = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t mine = tmem + (static_cast<uint32_t>(warp & 3) << 21) + group * 64;
-    Segment g;
+    Jobs jobs;
     unsigned step = 0;
     bool ok = true;  // a warp whose wait has run out goes on without waiting: the others meet it
-    while (next_segment<kTogether>(q, tb, order, run, g)) {
+    while (results_agree(jobs.next(sh, p.status))) {
+      const Job& g = sh.job[jobs.at];
       uint64_t sums[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sums[i] = 0;
       const bool live = (warp & 3) * 32 < g.rows;  // some row of this warp's
-      for (int st = g.s0; st < g.s1; ++st, ++step) {
+      const unsigned end = step + uniform(g.steps);
+#pragma unroll 1
+      for (; step < end; ++step) {
         const unsigned half = step & 1;
         if (ok) ok = mbar_wait_warp(&sh.acc_full[half], step / 2 & 1, p.status);
         uint32_t v[32], u[32];
@@ -365,21 +541,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sh.acc_empty[half]);
         }
       }
-      if (g.s0 != 0 || g.s1 != q.KS) {
+      bool finishes = true;
+      if (g.steps != q.KS) {
         // A shared unit: the last block to arrive adds the parts, in order.
-        const int c_first = owner_of(total, blocks, g.unit * q.KS);
-        const int c_last = owner_of(total, blocks, (g.unit + 1) * q.KS - 1);
+        const int me = blockIdx.x, c_first = g.first, c_last = g.last;
+        // Four sums of a row beside the next row's four.
+        const int n = g.rows;
         auto part = [&](int block, bool starts) {
-          return q.partial + ((static_cast<int64_t>(block) * 2 + (starts ? 1 : 0)) * q.tile_rows + r) * kTileN + group * 64;
+          return reinterpret_cast<float4*>(q.partial) +
+                 (static_cast<int64_t>(block) * 2 + (starts ? 1 : 0)) * (kTileN / 4) * q.tile_rows + group * 32 * n + r;
         };
-        if (r < g.rows) {
-          float* to = part(me, g.s0 == 0);
+        if (r < n) {
+          float4* to = part(me, g.s0 == 0);
 #pragma unroll
-          for (int i = 0; i < 64; i += 2) {
+          for (int i = 0; i < 32; ++i) {
             float4 f;
-            unpack_f32x2(sums[i], f.x, f.y);
-            unpack_f32x2(sums[i + 1], f.z, f.w);
-            __stcg(reinterpret_cast<float4*>(to + (i >= 32 ? kBlock - 64 : 0) + 2 * i), f);
+            unpack_f32x2(sums[2 * i], f.x, f.y);
+            unpack_f32x2(sums[2 * i + 1], f.z, f.w);
+            __stcg(to, f);
+            to += n;
           }
         }
         result_sync();
@@ -393,53 +573,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         result_sync();
         const bool last = sh.last;
-        if (last && r < g.rows) {
+        if (last && r < n) {
 #pragma unroll
           for (int i = 0; i < 64; ++i) sums[i] = 0;
+#pragma unroll 1
           for (int b = c_first; b <= c_last; ++b) {
-            const float* from = part(b, b == c_first);
+            const float4* from = part(b, b == c_first);
 #pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              const float4 f = __ldcg(reinterpret_cast<const float4*>(from + (i >= 32 ? kBlock - 64 : 0) + 2 * i));
-              float a, c;
-              unpack_f32x2(sums[i], a, c);
-              sums[i] = pack_f32x2(a + f.x, c + f.y);
-              unpack_f32x2(sums[i + 1], a, c);
-              sums[i + 1] = pack_f32x2(a + f.z, c + f.w);
+            for (int i0 = 0; i0 < 32; i0 += 16) {  // (as many loads in flight as registers are free)
+              float4 f[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) f[i] = __ldcg(from + i * n);
+              from += 16 * n;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                uint64_t* to = sums + 2 * (i0 + i);
+                to[0] = add_f32x2(to[0], pack_f32x2(f[i].x, f[i].y));
+                to[1] = add_f32x2(to[1], pack_f32x2(f[i].z, f[i].w));
+              }
+              asm volatile("" ::: "memory");
             }
           }
         }
         result_sync();  // sh.last is free again
-        if (!last) continue;
+        finishes = last;
       }
-      // Finished sums: the first 128 outputs' half (with GLU the gates'), then the second's.
-      const int64_t row = first_row(p, g.e) + g.tile * q.tile_rows + r;
-      const bool writes = r < g.rows;
-      float a[64], b[64];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        unpack_f32x2(sums[i], a[2 * i], a[2 * i + 1]);
-        unpack_f32x2(sums[32 + i], b[2 * i], b[2 * i + 1]);
+      if (finishes) {
+        // Finished sums: the first 128 outputs' half (with GLU the gates'), then the second's.
+        const int64_t row = g.row + r;
+        const bool writes = r < g.rows;
+        float a[64], b[64];
+  #pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          unpack_f32x2(sums[i], a[2 * i], a[2 * i + 1]);
+          unpack_f32x2(sums[32 + i], b[2 * i], b[2 * i + 1]);
+        }
+        int o = g.mt * kTileN + group * 64;
+        if (p.glu) {
+          o = g.mt * kBlock + group * 64;
+  #pragma unroll
+          for (int i = 0; i < 64; ++i) a[i] = silu(a[i]) * b[i];
+        }
+        if (p.out_fp8) {
+          // The other half of a row's 128 outputs is in the other warpgroup.
+          sh.top[group][0][r] = largest(a);
+          if (!p.glu) sh.top[group][1][r] = largest(b);
+          result_sync();
+          if (writes) store_fp8(p, a, fmaxf(sh.top[0][0][r], sh.top[1][0][r]), row, o, outs, group == 0);
+          if (writes && !p.glu && o + kBlock < outs)
+            store_fp8(p, b, fmaxf(sh.top[0][1][r], sh.top[1][1][r]), row, o + kBlock, outs, group == 0);
+          result_sync();
+        } else if (writes) {
+          store_bf16(p, a, row, o, outs);
+          if (!p.glu) store_bf16(p, b, row, o + kBlock, outs);
+        }
       }
-      int o = g.mt * kTileN + group * 64;
-      if (p.glu) {
-        o = g.mt * kBlock + group * 64;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) a[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
-      }
-      if (p.out_fp8) {
-        // The other half of a row's 128 outputs is in the other warpgroup.
-        sh.top[group][0][r] = largest(a);
-        if (!p.glu) sh.top[group][1][r] = largest(b);
-        result_sync();
-        if (writes) store_fp8(p, a, fmaxf(sh.top[0][0][r], sh.top[1][0][r]), row, o, outs, group == 0);
-        if (writes && !p.glu && o + kBlock < outs)
-          store_fp8(p, b, fmaxf(sh.top[0][1][r], sh.top[1][1][r]), row, o + kBlock, outs, group == 0);
-        result_sync();
-      } else if (writes) {
-        store_bf16(p, a, row, o, outs);
-        if (!p.glu) store_bf16(p, b, row, o + kBlock, outs);
-      }
+      jobs.done(sh);
     }
   }
   __syncwarp();
@@ -448,6 +637,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 3) {
     tmem_fence_after();
     tmem_free(tmem, kTmemCols);
+  }
+  if (tid == 0) {  // the last block leaves the list as it was
+    __threadfence();
+    if (atomicAdd(q.taken + 1, 1u) == gridDim.x - 1) q.taken[0] = q.taken[1] = 0u;
   }
 }
 
@@ -467,10 +660,9 @@ int tile_rows_for(int E, int64_t max_rows) {
 
 size_t partial_bytes(int tile_rows) { return sizeof(float) * kMaxBlocks * 2 * tile_rows * kTileN; }
 
-template <bool kTogether>
 cudaError_t launch_products(const Params& q, const CUtensorMap& map, const RowMaps& maps, size_t smem, int dev, int sms,
                             cudaStream_t s) {
-  const auto kernel = expert_linear_fp8_kernel<kTogether>;
+  const auto kernel = expert_linear_fp8_kernel;
   const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), dev, smem);
   if (err != cudaSuccess) return err;
   return launch_kernel(kernel, dim3(std::min(sms, kMaxBlocks)), dim3(kThreads), smem, s, /*dependent=*/true, q, map,
@@ -478,6 +670,11 @@ cudaError_t launch_products(const Params& q, const CUtensorMap& map, const RowMa
 }
 
 }  // namespace
+
+bool expert_linear_fp8_units_ok(int E, int64_t max_rows, int M, bool glu) {
+  const int64_t tiles = max_rows / tile_rows_for(E, max_rows) + E, outs = glu ? M / 2 : M;
+  return tiles * (outs / (glu ? kBlock : kTileN) + 1) <= INT32_MAX;
+}
 
 size_t expert_linear_fp8_ws_bytes(int E, int64_t max_rows) { return 1024 + partial_bytes(tile_rows_for(E, max_rows)); }
 
@@ -494,6 +691,7 @@ cudaError_t launch_expert_linear_fp8(const ExpertLinearFp8Params& p, cudaStream_
   q.scale_rows = p.transposed ? q.KB : out_blocks;
   q.scale_cols = p.transposed ? out_blocks : q.KB;
   q.counters = reinterpret_cast<unsigned*>(p.ws);
+  q.taken = q.counters + kMaxBlocks;
   q.partial = reinterpret_cast<float*>(p.ws + 1024);
   q.stage_bytes = kTileBytes + static_cast<unsigned>(q.tile_rows) * kStep;
   const unsigned tables = static_cast<unsigned>(table_bytes(p.E));
@@ -534,7 +732,7 @@ cudaError_t launch_expert_linear_fp8(const ExpertLinearFp8Params& p, cudaStream_
   const int dev = current_device();
   const int sms = device_sms(dev);
   if (sms < 1) return cudaErrorInvalidDevice;
-  return launch_products<true>(q, map, maps, smem, dev, sms, s);
+  return launch_products(q, map, maps, smem, dev, sms, s);
 }
 
 }  // namespace ep

@@ -317,6 +317,7 @@ size_t expert_linear_ws_bytes(int E, int64_t max_rows, int K, bool fp8);
 cudaError_t launch_expert_linear(const ExpertLinearParams& p, cudaStream_t s);
 cudaError_t launch_route(const RouteParams& p, cudaStream_t s);
 cudaError_t launch_route_backward(const RouteParams& p, cudaStream_t s);
+bool expert_linear_fp8_units_ok(int E, int64_t max_rows, int M, bool glu);  // units are counted in 32 bits
 size_t expert_linear_fp8_ws_bytes(int E, int64_t max_rows);
 cudaError_t launch_expert_linear_fp8(const ExpertLinearFp8Params& p, cudaStream_t s);
 

@@ -174,11 +174,11 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
 }
 
 // ---- product of 8-bit operands ---------------------------------------------------
-// D[128, N] (+)= A[128, 32] B[N, 32]^T, both E4M3, fp32 sums. The instruction
+// D[M, N] (+)= A[M, 32] B[N, 32]^T, both E4M3, fp32 sums. The instruction
 // descriptor: fp32 sums (1) at bit 4, the operands' types (0: E4M3) at 7 and 10,
 // B transposed at 16, N / 8 at 17, M / 16 at 24.
-__device__ __forceinline__ uint32_t idesc_e4m3(int n, bool b_transposed) {
-  return 1u << 4 | (b_transposed ? 1u << 16 : 0u) | static_cast<uint32_t>(n / 8) << 17 | (128u / 16u) << 24;
+__device__ __forceinline__ uint32_t idesc_e4m3(unsigned m, unsigned n, bool b_transposed) {
+  return 1u << 4 | (b_transposed ? 1u << 16 : 0u) | n / 8 << 17 | m / 16 << 24;
 }
 
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {

@@ -138,6 +138,7 @@ FP8_SHAPES = [
     (640, 768, [130, 2, 17], True),
     (7168, 512, [1] * 8, True),
     (256, 1280, [300, 129], False),
+    (384, 768, [300, 131, 0, 250], True),
 ]
 
 

@@ -108,7 +108,10 @@ struct Share {
   int cut, cutters;  // units that are cut, blocks that share them
   int at, end;       // this block's steps of them
   __device__ Share(int units, int KS, int blocks, int me) : units(units), KS(KS), blocks(blocks) {
-    cut = units % blocks;
+    // A join at a call's end costs about 8 us, which pays only where few blocks would
+    // have work otherwise. (7168 inputs, one row, whole / cut: 48 units 37 / 32 us, 64
+    // 38 / 39, 80 39 / 48, 128 48 / 55; 100 rows, 80 units 38 / 49, 128 48 / 64.)
+    cut = units < blocks && 8 * units > 3 * blocks ? 0 : units % blocks;
     // Every block that takes part has steps: the join counts on it. (Of 32 experts
     // of 128 rows 8 units are left to cut: in us, shared by 2, 4, 8, 16 and 19 blocks
     // each, 232, 229, 237, 260 and 273; 2 units of 8 rows alone 22, 17, 18, 26, 38.)
@@ -574,10 +577,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         result_sync();
         const bool last = sh.last;
         if (last && r < n) {
+          // (Of two parts this block has one at hand, and which comes first makes no difference.)
+          const bool two = c_last == c_first + 1;
+          if (!two) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) sums[i] = 0;
+            for (int i = 0; i < 64; ++i) sums[i] = 0;
+          }
 #pragma unroll 1
           for (int b = c_first; b <= c_last; ++b) {
+            if (two && b == me) continue;
             const float4* from = part(b, b == c_first);
 #pragma unroll
             for (int i0 = 0; i0 < 32; i0 += 16) {  // (as many loads in flight as registers are free)

@@ -1085,18 +1085,21 @@ def expert_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Ten
 
 
 # ------------------------------------- the router and the 8-bit experts ----
-def _same_device(first: torch.Tensor, *tensors: Optional[torch.Tensor]) -> None:
+def _same_device(*tensors: Optional[torch.Tensor]) -> None:
     """The tensors lie on the current device, where the call's kernels run."""
     here = _get_device()
-    for t in (first, *tensors):
-        if t is not None and t.is_cuda and t.get_device() != here:
+    for t in tensors:
+        if t is not None and t.get_device() != here and t.is_cuda:
             raise ValueError(f"expected tensors on the current device, cuda:{here}")
 
 
+_SCORES = {"softmax": 0, "sigmoid": EP_ROUTE_SIGMOID}
+
+
 def _route_flags(score: str, renormalize: bool) -> int:
-    if score not in ("softmax", "sigmoid"):
+    if score not in _SCORES:
         raise ValueError(f"score: expected 'softmax' or 'sigmoid', not {score!r}")
-    return (EP_ROUTE_SIGMOID if score == "sigmoid" else 0) | (EP_ROUTE_RENORMALIZE if renormalize else 0)
+    return _SCORES[score] | (EP_ROUTE_RENORMALIZE if renormalize else 0)
 
 
 def route(logits: torch.Tensor, topk: int, bias: Optional[torch.Tensor] = None, score: str = "softmax",
@@ -1121,14 +1124,26 @@ def route(logits: torch.Tensor, topk: int, bias: Optional[torch.Tensor] = None, 
                           topk_idx, topk_weights, return_scores)
     flags = _route_flags(score, renormalize)
     _same_device(logits, bias, topk_idx, topk_weights)
-    shape = (logits.shape[0], topk)
+    at, stride, tokens, experts, kind = _logits(logits)
+    dev, shape = logits.device, (tokens, topk)
+    # (What is made here needs no check: the call's time is the host's until there are thousands of tokens.)
     if topk_idx is None:
-        topk_idx = torch.empty(shape, dtype=_I32, device=logits.device)
+        topk_idx = torch.empty(shape, dtype=_I32, device=dev)
+        idx_at = topk_idx.data_ptr()
+    else:
+        idx_at = _address(topk_idx, "topk_idx", _I32, shape)
     if topk_weights is None:
-        topk_weights = torch.empty(shape, dtype=_F32, device=logits.device)
-    scores = torch.empty(logits.shape, dtype=_F32, device=logits.device) if return_scores else None
-    ep_route(logits, topk, bias, groups, groups if topk_groups is None else topk_groups, group_best, flags, scale,
-             topk_idx, topk_weights, scores)
+        topk_weights = torch.empty(shape, dtype=_F32, device=dev)
+        weights_at = topk_weights.data_ptr()
+    else:
+        weights_at = _address(topk_weights, "topk_weights", _F32, shape)
+    scores = torch.empty((tokens, experts), dtype=_F32, device=dev) if return_scores else None
+    rc = lib().ep_route(at, stride, tokens, experts, topk,
+                        bias if bias is None else _address(bias, "bias", _F32, (experts,)), groups,
+                        groups if topk_groups is None else topk_groups, group_best, flags | kind, scale, idx_at,
+                        weights_at, scores if scores is None else scores.data_ptr(), _raw(None))
+    if rc != EP_OK:
+        raise EPError("ep_route", rc)
     return (topk_idx, topk_weights, scores) if return_scores else (topk_idx, topk_weights)
 
 

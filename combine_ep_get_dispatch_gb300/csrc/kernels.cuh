@@ -289,6 +289,7 @@ struct RouteParams {
   const int32_t* chosen;     // [N, K]
   void* grad_logits;         // [N, E], the logits' type
   int32_t* status;
+  int vec_logits, vec_bias, vec_scores, vec_grad;  // rows that can be read or written 16 bytes at a time
 };
 
 struct ExpertLinearFp8Params {

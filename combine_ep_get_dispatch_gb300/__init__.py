@@ -1087,10 +1087,13 @@ def expert_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Ten
 # ------------------------------------- the router and the 8-bit experts ----
 def _same_device(*tensors: Optional[torch.Tensor]) -> None:
     """The tensors lie on the current device, where the call's kernels run."""
-    here = _get_device()
+    here = None
     for t in tensors:
-        if t is not None and t.get_device() != here and t.is_cuda:
-            raise ValueError(f"expected tensors on the current device, cuda:{here}")
+        if t is not None and t.is_cuda:
+            if here is None:
+                here = _get_device()
+            if t.get_device() != here:
+                raise ValueError(f"expected tensors on the current device, cuda:{here}")
 
 
 _SCORES = {"softmax": 0, "sigmoid": EP_ROUTE_SIGMOID}

@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 10 : V == 16 ? 4 : 3) ro
     if (__any_sync(kAll, near_next)) mine = order_exactly<V>(p, token, mine, taken);
   }
   float s = mine >= 0 ? score(logit(p, row + mine)) : 0.0f;
-  if (p.renormalize) s = __fdividef(s, warp_sum(s) + kTiny);  // (2 ulp; the sum is under 2^6)
+  if (p.renormalize) s = s / (warp_sum(s) + kTiny);
   if (lane < p.K) {
     p.idx[token * p.K + lane] = mine;
     p.weights[token * p.K + lane] = s * p.scale;

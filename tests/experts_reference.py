@@ -12,14 +12,14 @@ def scores(z: np.ndarray, kind: str) -> np.ndarray:
     z = z.astype(np.float64)
     ok = ~np.isnan(z)
     s = np.zeros(z.shape)
-    with np.errstate(over="ignore"):
+    with np.errstate(over="ignore", invalid="ignore"):
         if kind == "sigmoid":
             s[ok] = 1.0 / (1.0 + np.exp(-z[ok]))
             return s
-    top = z[ok].max() if ok.any() else -np.inf
-    if top == -np.inf:
-        return s
-    e = np.where(z[ok] == top, 1.0, np.exp(np.where(z[ok] == top, 0.0, z[ok] - top)))
+        top = z[ok].max() if ok.any() else -np.inf
+        if top == -np.inf:
+            return s
+        e = np.where(z[ok] == top, 1.0, np.exp(np.where(z[ok] == top, 0.0, z[ok] - top)))
     s[ok] = e / e.sum()
     return s
 

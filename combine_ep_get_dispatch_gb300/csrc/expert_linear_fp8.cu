@@ -44,6 +44,7 @@ constexpr int kRowMaps = kTileRows / 16;  // boxes of 16, 32 .. 128 rows
 constexpr int kMaxBlocks = 160;         // blocks a workspace has room for
 constexpr int kThreads = 384;           // loads, products, scales (four warps), results (eight)
 constexpr int kResultThreads = 256;
+constexpr int kBufferPieces = 32 * 5;   // 16 bytes each: a warp's results on their way out
 constexpr int kMaxStages = 8;
 constexpr int kTmemCols = 512;          // two steps' sums
 constexpr int kMinStages = 2;           // fewest steps worth a block of their own
@@ -64,6 +65,7 @@ struct Params {
   int MT;         // units of a tile: an expert's output tiles
   int stages;
   unsigned stage_bytes;
+  unsigned buffer_bytes;  // of the warps that can have rows: results on their way out
   int scale_rows, scale_cols;  // blocks of W in either direction
   unsigned* counters;          // [kMaxBlocks]: arrivals at a shared unit
   unsigned* taken;             // whole units that blocks have taken, and blocks that are done
@@ -223,13 +225,33 @@ __device__ __forceinline__ uint4 bf16x8(const float* v) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// One thread's 64 results of `row`, outputs o .. o + 63.
-__device__ __forceinline__ void store_bf16(const ExpertLinearFp8Params& p, const float (&v)[64], int64_t row, int o,
-                                           int outs) {
-  uint16_t* to = static_cast<uint16_t*>(p.y) + row * outs + o;
+// A warp's 32 rows of 64 bytes to y, of which `n` rows and `bytes` of each are
+// there: by way of shared memory (`buffer`: 32 x 5 pieces of 16 bytes, the fifth
+// unused, so that rows meet different banks), so that an instruction writes 64
+// bytes of eight rows. (16 bytes of 32 rows each, a unit's results took 7 us, in
+// which the products of 18 steps could be made.)
+__device__ __forceinline__ void store_rows(uint8_t* to, int64_t pitch, int n, int bytes, uint4* buffer, const uint4 (&w)[4]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < 64; i += 8)
-    if (o + i < outs) *reinterpret_cast<uint4*>(to + i) = bf16x8(v + i);
+  for (int i = 0; i < 4; ++i) buffer[lane * 5 + i] = w[i];
+  __syncwarp();
+  const int row = lane >> 2, part = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (8 * i + row < n && part * 16 < bytes)
+      *reinterpret_cast<uint4*>(to + (8 * i + row) * pitch + part * 16) = buffer[(8 * i + row) * 5 + part];
+  __syncwarp();
+}
+
+// 64 results of each lane's row, outputs o .. o + 63; `row` is the warp's first of n.
+__device__ __forceinline__ void store_bf16(const ExpertLinearFp8Params& p, const float (&v)[64], int64_t row, int n, int o,
+                                           int outs, uint4* buffer) {
+#pragma unroll
+  for (int i = 0; i < 64; i += 32) {
+    const uint4 w[4] = {bf16x8(v + i), bf16x8(v + i + 8), bf16x8(v + i + 16), bf16x8(v + i + 24)};
+    store_rows(static_cast<uint8_t*>(p.y) + 2 * (row * outs + o + i), 2 * static_cast<int64_t>(outs), n,
+               2 * (outs - o - i), buffer, w);
+  }
 }
 
 // The largest magnitude of 64 results (a NaN is left out).
@@ -247,7 +269,6 @@ __device__ __forceinline__ void store_fp8(const ExpertLinearFp8Params& p, const 
   float sc = __fdiv_rn(m, 448.0f);
   if (p.out_pow2 && sc > 0.0f) sc = pow2_ceil(sc);
   if (p.out_ue8m0 && m > 0.0f) sc = fmaxf(sc, __uint_as_float(0x00400000u));  // 2^-127
-  uint8_t* to = static_cast<uint8_t*>(p.y) + row * outs + o;
   // v / s, correctly rounded: from one correctly rounded reciprocal y the quotient
   // v y is within an ulp, its remainder v - s v y is exact by a fused
   // multiply-add, and v y + remainder y rounds to v / s (Markstein, "Computation of
@@ -256,6 +277,7 @@ __device__ __forceinline__ void store_fp8(const ExpertLinearFp8Params& p, const 
   // a zero (s >= 2^-92) and y is a normal number (s <= 2^126).
   const bool quick = sc >= 0x1p-92f && sc <= 0x1p126f;
   const float y = quick ? __frcp_rn(sc) : 0.0f;
+  uint8_t* to = static_cast<uint8_t*>(p.y) + row * outs + o;
 #pragma unroll
   for (int i = 0; i < 64; i += 16) {
     uint32_t w[4];
@@ -293,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Shared sh;
   const ExpertLinearFp8Params& p = q.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
-  const Tables tb(reinterpret_cast<int*>(smem + q.stages * q.stage_bytes), p.E);
+  const Tables tb(reinterpret_cast<int*>(smem + q.stages * q.stage_bytes + q.buffer_bytes), p.E);
   if (tid == 0) {
     for (int i = 0; i < q.stages; ++i) {
       mbar_init(&sh.full[i], 1);
@@ -608,10 +630,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (finishes) {
         // Finished sums: the first 128 outputs' half (with GLU the gates'), then the second's.
-        const int64_t row = g.row + r;
-        const bool writes = r < g.rows;
+        const int64_t row = g.row + (warp & 3) * 32;
+        const int n = g.rows - (warp & 3) * 32;  // of the warp's rows
+        uint4* buffer = reinterpret_cast<uint4*>(smem + q.stages * q.stage_bytes) + (2 * (warp & 3) + group) * kBufferPieces;
         float a[64], b[64];
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < 32; ++i) {
           unpack_f32x2(sums[i], a[2 * i], a[2 * i + 1]);
           unpack_f32x2(sums[32 + i], b[2 * i], b[2 * i + 1]);
@@ -619,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int o = g.mt * kTileN + group * 64;
         if (p.glu) {
           o = g.mt * kBlock + group * 64;
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < 64; ++i) a[i] = silu(a[i]) * b[i];
         }
         if (p.out_fp8) {
@@ -627,13 +650,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           sh.top[group][0][r] = largest(a);
           if (!p.glu) sh.top[group][1][r] = largest(b);
           result_sync();
-          if (writes) store_fp8(p, a, fmaxf(sh.top[0][0][r], sh.top[1][0][r]), row, o, outs, group == 0);
-          if (writes && !p.glu && o + kBlock < outs)
-            store_fp8(p, b, fmaxf(sh.top[0][1][r], sh.top[1][1][r]), row, o + kBlock, outs, group == 0);
+          if (lane < n) store_fp8(p, a, fmaxf(sh.top[0][0][r], sh.top[1][0][r]), row + lane, o, outs, group == 0);
+          if (lane < n && !p.glu && o + kBlock < outs)
+            store_fp8(p, b, fmaxf(sh.top[0][1][r], sh.top[1][1][r]), row + lane, o + kBlock, outs, group == 0);
           result_sync();
-        } else if (writes) {
-          store_bf16(p, a, row, o, outs);
-          if (!p.glu) store_bf16(p, b, row, o + kBlock, outs);
+        } else if (n > 0) {
+          store_bf16(p, a, row, n, o, outs, buffer);
+          if (!p.glu) store_bf16(p, b, row, n, o + kBlock, outs, buffer);
         }
       }
       jobs.done(sh);
@@ -702,10 +725,11 @@ cudaError_t launch_expert_linear_fp8(const ExpertLinearFp8Params& p, cudaStream_
   q.taken = q.counters + kMaxBlocks;
   q.partial = reinterpret_cast<float*>(p.ws + 1024);
   q.stage_bytes = kTileBytes + static_cast<unsigned>(q.tile_rows) * kStep;
+  q.buffer_bytes = 2 * ((q.tile_rows + 31) / 32) * kBufferPieces * 16;
   const unsigned tables = static_cast<unsigned>(table_bytes(p.E));
-  const unsigned most = 227 * 1024 - sizeof(Shared) - 2048 - tables;
+  const unsigned most = 227 * 1024 - sizeof(Shared) - 2048 - tables - q.buffer_bytes;
   q.stages = std::min<int>(kMaxStages, most / q.stage_bytes);
-  const size_t smem = static_cast<size_t>(q.stages) * q.stage_bytes + tables + 1024;
+  const size_t smem = static_cast<size_t>(q.stages) * q.stage_bytes + q.buffer_bytes + tables + 1024;
 
   const EncodeTiled encode = encode_tiled();
   if (!encode) return cudaErrorNotSupported;

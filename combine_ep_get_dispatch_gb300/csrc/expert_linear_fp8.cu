@@ -331,13 +331,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
   }
-  if (warp == 3) tmem_alloc(&sh.tmem, kTmemCols);
   grid_dependency_wait();
-  launch_dependents();
+  // (Tensor memory only now: a kernel that this one waits for may still ask for some.)
+  if (warp == 3) tmem_alloc(&sh.tmem, kTmemCols);
   tile_experts(q, sh.scan, tb);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
+  launch_dependents();
   const uint32_t tmem = uniform(sh.tmem);
   const int outs = p.glu ? p.M / 2 : p.M;
   // A stage: rows of x, then weights (a product always reads 128 rows: with

@@ -293,6 +293,27 @@ def test_weights_beyond_32_bits():
     X.check_bf16(f64(dx)[:, at], *X.product(R.TABLE[g] * gs.astype(np.float64).repeat(128, axis=1), wv[:, at].T, False))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_and_results_beyond_32_bits(fp8):
+    """Rows whose codes, and whose results, start past 2^32 bytes."""
+    rng = np.random.default_rng(23)
+    K, M, total, at = 8192, 9216, 600_000, 599_000
+    codes, scales = codes_of(rng, M, K), np.exp(rng.normal(size=(M // 128, K // 128)) - 12).astype(np.float32)
+    x = torch.empty((total, K), dtype=torch.uint8, device="cuda")
+    xs = torch.empty((total, K // 128), device="cuda")
+    rows, row_scales = codes_of(rng, 5, K), np.exp(rng.normal(size=(5, K // 128)) - 6).astype(np.float32)
+    x[at:at + 5], xs[at:at + 5] = dev(rows), dev(row_scales)
+    made = ep.expert_linear_fp8(x, xs, dev(codes[None]), dev(scales[None]), ints([5]), ints([at]), use_fp8=fp8, max_rows=5)
+    pick = np.sort(rng.choice(M // 128, 2, replace=False))[:, None] * 128 + np.arange(128)  # whole blocks of outputs
+    value = R.TABLE[rows] * row_scales.astype(np.float64).repeat(128, axis=1)
+    y, err = X.product(value, (R.TABLE[codes] * X.blocks(scales.astype(np.float64), M, K))[pick.reshape(-1)], False)
+    if not fp8:
+        X.check_bf16(f64(made[at:at + 5])[:, pick.reshape(-1)], y, err)
+        return
+    X.check_fp8(made[0][at:at + 5].cpu().numpy()[:, pick.reshape(-1)], f64(made[1][at:at + 5])[:, pick[:, 0] // 128], y, err,
+                False)
+
+
 @pytest.mark.parametrize("transposed", [False, True])
 def test_in_a_graph_and_on_another_stream(transposed):
     c = Case(18, 512, 256, [3, 1, 20], transposed=transposed)
@@ -339,6 +360,29 @@ def test_many_units_and_blocks():
     got = f64(c.run())
     for e, rows in c.rows():
         X.check_bf16(got[rows], *c.expect(e, rows))
+
+
+@pytest.mark.parametrize("rows", [1, 40, 128])
+def test_every_number_of_units(rows):
+    """Units that are fewer than the blocks, whole and cut, about as many, and a few more."""
+    for outs in (256, 256 * 20, 256 * 57, 256 * 58, 256 * 151, 256 * 152 + 8, 256 * 160):
+        c = Case(rows + outs, 640, outs, [rows])
+        got = f64(c.run())
+        at = np.random.default_rng(outs).choice(outs, min(outs, 200), replace=False)
+        y, err = X.product(c.value[:rows], c.weights[0][at], False)
+        X.check_bf16(got[:rows, at], y, err)
+
+
+def test_one_workspace_for_calls_of_all_sizes():
+    """Calls one after the other, of other shapes and with nothing to do, leave a shared workspace as it was."""
+    cases = [Case(30, 1024, 768, [9, 0, 200, 41]), Case(31, 256, 4096, [3] * 9), Case(32, 2048, 512, [70, 140], transposed=True)]
+    ws = torch.zeros(max(ep.ep_expert_linear_fp8_workspace_bytes(9, 1000), *(
+        ep.ep_expert_linear_fp8_workspace_bytes(len(c.counts), sum(c.counts)) for c in cases)), dtype=torch.uint8, device="cuda")
+    want = [c.run()[np.flatnonzero(c.received())] for c in cases]
+    for _ in range(3):
+        for c, w in zip(cases, want):
+            assert torch.equal(c.run(workspace=ws)[np.flatnonzero(c.received())], w)
+            c.run(workspace=ws, row_count=torch.zeros_like(c.row_count))
 
 
 def test_nothing_to_do():

@@ -215,9 +215,10 @@ __device__ __forceinline__ float row_scale(const ExpertLinearFp8Params& p, int64
 // (With an IEEE division, whose rare cases are a call, a unit's 64 gates and 64
 // quotients a thread took as long as the products of 30 steps.)
 __device__ __forceinline__ float silu(float g) {
+  const float e = expf(-fabsf(g));
   float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(1.0f + expf(-g)));
-  return g * y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + e));  // (of a number from 1 to 2)
+  return g * (g < 0.0f ? e * y : y);
 }
 
 // Eight results to BF16.
@@ -262,42 +263,51 @@ __device__ __forceinline__ float largest(const float (&v)[64]) {
   return m;
 }
 
+// v / sc in E4M3, 64 of them. kQuick: correctly rounded from one correctly rounded
+// reciprocal y, by which the quotient t = v y is within an ulp, its remainder v - sc t
+// exact by a fused multiply-add, and t + remainder y rounds to v / sc (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// IBM J. Res. Dev. 34(1), 1990), as long as the remainder does not underflow where a
+// code is not a zero (sc >= 2^-92) and y is a normal number (sc <= 2^126).
+template <bool kQuick>
+__device__ __forceinline__ void store_codes(const float (&v)[64], float sc, uint8_t* to) {
+  const float y = kQuick ? __frcp_rn(sc) : 0.0f;
+  const uint64_t y2 = pack_f32x2(y, y), s2 = pack_f32x2(-sc, -sc);
+#pragma unroll
+  for (int i = 0; i < 64; i += 16) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      const float x0 = v[i + j], x1 = v[i + j + 1];
+      float u0, u1;
+      if (kQuick) {
+        const uint64_t x = pack_f32x2(x0, x1), t = mul_f32x2(x, y2);
+        unpack_f32x2(fma_f32x2(fma_f32x2(s2, t, x), y2, t), u0, u1);
+        // (a zero keeps its sign)
+        u0 = __uint_as_float(__float_as_uint(u0) | (__float_as_uint(x0) & 0x80000000u));
+        u1 = __uint_as_float(__float_as_uint(u1) | (__float_as_uint(x1) & 0x80000000u));
+      } else {
+        u0 = sc > 0.0f ? __fdiv_rn(x0, sc) : x0;
+        u1 = sc > 0.0f ? __fdiv_rn(x1, sc) : x1;
+      }
+      w[j / 4] |= pack_e4m3x2(u0, u1) << (8 * (j & 2));
+    }
+    *reinterpret_cast<uint4*>(to + i) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 // ... and to E4M3, as the dispatch quantises rows, with the scale of the 128
-// results that they are half of.
+// results that they are part of.
 __device__ __forceinline__ void store_fp8(const ExpertLinearFp8Params& p, const float (&v)[64], float m, int64_t row,
                                           int o, int outs, bool writes_scale) {
   float sc = __fdiv_rn(m, 448.0f);
   if (p.out_pow2 && sc > 0.0f) sc = pow2_ceil(sc);
   if (p.out_ue8m0 && m > 0.0f) sc = fmaxf(sc, __uint_as_float(0x00400000u));  // 2^-127
-  // v / s, correctly rounded: from one correctly rounded reciprocal y the quotient
-  // v y is within an ulp, its remainder v - s v y is exact by a fused
-  // multiply-add, and v y + remainder y rounds to v / s (Markstein, "Computation of
-  // elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev.
-  // 34(1), 1990), as long as the remainder does not underflow where a code is not
-  // a zero (s >= 2^-92) and y is a normal number (s <= 2^126).
-  const bool quick = sc >= 0x1p-92f && sc <= 0x1p126f;
-  const float y = quick ? __frcp_rn(sc) : 0.0f;
   uint8_t* to = static_cast<uint8_t*>(p.y) + row * outs + o;
-#pragma unroll
-  for (int i = 0; i < 64; i += 16) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float u[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x = v[i + 4 * j + k];
-        if (quick) {
-          const float t = x * y;
-          u[k] = copysignf(fmaf(fmaf(-sc, t, x), y, t), x);  // (a zero keeps its sign)
-        } else {
-          u[k] = sc > 0.0f ? __fdiv_rn(x, sc) : x;
-        }
-      }
-      w[j] = pack_e4m3x2(u[0], u[1]) | pack_e4m3x2(u[2], u[3]) << 16;
-    }
-    *reinterpret_cast<uint4*>(to + i) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  if (sc >= 0x1p-92f && sc <= 0x1p126f)
+    store_codes<true>(v, sc, to);
+  else
+    store_codes<false>(v, sc, to);
   if (!writes_scale) return;
   const int64_t at = row * (outs / kBlock) + o / kBlock;
   if (p.out_ue8m0)

@@ -236,6 +236,29 @@ def test_zero_rows_and_zero_scales():
     assert (s[1] == 0).all() and ((y[1] & 0x7F) == 0).all() and (s[[0, 2, 3]] > 0).all()
 
 
+def test_fp8_results_of_all_sizes():
+    """Scales from 2^-120 to 2^118, and rows of zeros of either sign beside them: the rule of ep_fp8_quantize."""
+    K = M = 128
+    w = torch.zeros((1, M, K), dtype=torch.uint8, device="cuda")
+    w[0, torch.arange(M), torch.arange(K)] = 0x38                 # the identity
+    ws = torch.ones((1, 1, 1), device="cuda")
+    powers = torch.arange(-120, 119, 7, device="cuda")
+    n = powers.numel()
+    x = dev(codes_of(np.random.default_rng(24), n, K))
+    x[::5, 3] = 0x80
+    xs = torch.ldexp(torch.ones(n, device="cuda"), powers)[:, None]
+    count, off = ints([n]), ints([0])
+    y = ep.expert_linear_fp8(x, xs, w, ws, count, off)            # exact: E4M3 times a power of two
+    for kw in (dict(), dict(round_scale=True), dict(use_ue8m0=True)):
+        q, s = ep.expert_linear_fp8(x, xs, w, ws, count, off, use_fp8=True, **kw)
+        want, ws_ = torch.empty_like(q), torch.empty_like(s)
+        ep.ep_fp8_quantize(y, want, ws_, ep.fp8_flags(True, **kw))
+        assert torch.equal(s, ws_)
+        # a sum of zeros is +0, whatever their signs
+        same = (q == want) | ((q & 0x7F) == 0) & ((want & 0x7F) == 0)
+        assert same.all()
+
+
 def test_reports_rows_it_skips():
     c = Case(15, 256, 24, [4, 4], regions=True, spare=0)
     want = c.run(max_rows=8)

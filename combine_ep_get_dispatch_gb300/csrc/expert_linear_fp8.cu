@@ -44,7 +44,6 @@ constexpr int kRowMaps = kTileRows / 16;  // boxes of 16, 32 .. 128 rows
 constexpr int kMaxBlocks = 160;         // blocks a workspace has room for
 constexpr int kThreads = 384;           // loads, products, scales (four warps), results (eight)
 constexpr int kResultThreads = 256;
-constexpr int kBufferPieces = 32 * 5;   // 16 bytes each: a warp's results on their way out
 constexpr int kMaxStages = 8;
 constexpr int kTmemCols = 512;          // two steps' sums
 constexpr int kMinStages = 2;           // fewest steps worth a block of their own
@@ -65,7 +64,6 @@ struct Params {
   int MT;         // units of a tile: an expert's output tiles
   int stages;
   unsigned stage_bytes;
-  unsigned buffer_bytes;  // of the warps that can have rows: results on their way out
   int scale_rows, scale_cols;  // blocks of W in either direction
   unsigned* counters;          // [kMaxBlocks]: arrivals at a shared unit
   unsigned* taken;             // whole units that blocks have taken, and blocks that are done
@@ -226,32 +224,23 @@ __device__ __forceinline__ uint4 bf16x8(const float* v) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// A warp's 32 rows of 64 bytes to y, of which `n` rows and `bytes` of each are
-// there: by way of shared memory (`buffer`: 32 x 5 pieces of 16 bytes, the fifth
-// unused, so that rows meet different banks), so that an instruction writes 64
-// bytes of eight rows. (16 bytes of 32 rows each, a unit's results took 7 us, in
-// which the products of 18 steps could be made.)
-__device__ __forceinline__ void store_rows(uint8_t* to, int64_t pitch, int n, int bytes, uint4* buffer, const uint4 (&w)[4]) {
-  const int lane = threadIdx.x & 31;
+// A row's 64 results, outputs o .. o + 63. (32 bytes a store, a whole sector: with
+// 16 a unit's results took 7 us, in which the products of 18 steps could be made.)
+__device__ __forceinline__ void store_bf16(const ExpertLinearFp8Params& p, const float (&v)[64], int64_t row, int o,
+                                           int outs) {
+  uint16_t* to = static_cast<uint16_t*>(p.y) + row * outs + o;
+  const bool whole = (reinterpret_cast<uintptr_t>(to) & 31) == 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) buffer[lane * 5 + i] = w[i];
-  __syncwarp();
-  const int row = lane >> 2, part = lane & 3;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (8 * i + row < n && part * 16 < bytes)
-      *reinterpret_cast<uint4*>(to + (8 * i + row) * pitch + part * 16) = buffer[(8 * i + row) * 5 + part];
-  __syncwarp();
-}
-
-// 64 results of each lane's row, outputs o .. o + 63; `row` is the warp's first of n.
-__device__ __forceinline__ void store_bf16(const ExpertLinearFp8Params& p, const float (&v)[64], int64_t row, int n, int o,
-                                           int outs, uint4* buffer) {
-#pragma unroll
-  for (int i = 0; i < 64; i += 32) {
-    const uint4 w[4] = {bf16x8(v + i), bf16x8(v + i + 8), bf16x8(v + i + 16), bf16x8(v + i + 24)};
-    store_rows(static_cast<uint8_t*>(p.y) + 2 * (row * outs + o + i), 2 * static_cast<int64_t>(outs), n,
-               2 * (outs - o - i), buffer, w);
+  for (int i = 0; i < 64; i += 16) {
+    const uint4 a = bf16x8(v + i), b = bf16x8(v + i + 8);
+    if (whole && o + i + 8 < outs) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + i), "r"(a.x), "r"(a.y), "r"(a.z),
+                   "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                   : "memory");
+    } else {
+      if (o + i < outs) *reinterpret_cast<uint4*>(to + i) = a;
+      if (o + i + 8 < outs) *reinterpret_cast<uint4*>(to + i + 8) = b;
+    }
   }
 }
 
@@ -325,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Shared sh;
   const ExpertLinearFp8Params& p = q.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
-  const Tables tb(reinterpret_cast<int*>(smem + q.stages * q.stage_bytes + q.buffer_bytes), p.E);
+  const Tables tb(reinterpret_cast<int*>(smem + q.stages * q.stage_bytes), p.E);
   if (tid == 0) {
     for (int i = 0; i < q.stages; ++i) {
       mbar_init(&sh.full[i], 1);
@@ -653,9 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (finishes) {
         // Finished sums: the first 128 outputs' half (with GLU the gates'), then the second's.
-        const int64_t row = g.row + (warp & 3) * 32;
-        const int n = g.rows - (warp & 3) * 32;  // of the warp's rows
-        uint4* buffer = reinterpret_cast<uint4*>(smem + q.stages * q.stage_bytes) + (2 * (warp & 3) + group) * kBufferPieces;
+        const int64_t row = g.row + r;
+        const bool writes = r < g.rows;
         float a[64], b[64];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -673,13 +661,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           sh.top[group][0][r] = largest(a);
           if (!p.glu) sh.top[group][1][r] = largest(b);
           result_sync();
-          if (lane < n) store_fp8(p, a, fmaxf(sh.top[0][0][r], sh.top[1][0][r]), row + lane, o, outs, group == 0);
-          if (lane < n && !p.glu && o + kBlock < outs)
-            store_fp8(p, b, fmaxf(sh.top[0][1][r], sh.top[1][1][r]), row + lane, o + kBlock, outs, group == 0);
+          if (writes) store_fp8(p, a, fmaxf(sh.top[0][0][r], sh.top[1][0][r]), row, o, outs, group == 0);
+          if (writes && !p.glu && o + kBlock < outs)
+            store_fp8(p, b, fmaxf(sh.top[0][1][r], sh.top[1][1][r]), row, o + kBlock, outs, group == 0);
           result_sync();
-        } else if (n > 0) {
-          store_bf16(p, a, row, n, o, outs, buffer);
-          if (!p.glu) store_bf16(p, b, row, n, o + kBlock, outs, buffer);
+        } else if (writes) {
+          store_bf16(p, a, row, o, outs);
+          if (!p.glu) store_bf16(p, b, row, o + kBlock, outs);
         }
       }
       jobs.done(sh);
@@ -748,11 +736,10 @@ cudaError_t launch_expert_linear_fp8(const ExpertLinearFp8Params& p, cudaStream_
   q.taken = q.counters + kMaxBlocks;
   q.partial = reinterpret_cast<float*>(p.ws + 1024);
   q.stage_bytes = kTileBytes + static_cast<unsigned>(q.tile_rows) * kStep;
-  q.buffer_bytes = 2 * ((q.tile_rows + 31) / 32) * kBufferPieces * 16;
   const unsigned tables = static_cast<unsigned>(table_bytes(p.E));
-  const unsigned most = 227 * 1024 - sizeof(Shared) - 2048 - tables - q.buffer_bytes;
+  const unsigned most = 227 * 1024 - sizeof(Shared) - 2048 - tables;
   q.stages = std::min<int>(kMaxStages, most / q.stage_bytes);
-  const size_t smem = static_cast<size_t>(q.stages) * q.stage_bytes + q.buffer_bytes + tables + 1024;
+  const size_t smem = static_cast<size_t>(q.stages) * q.stage_bytes + tables + 1024;
 
   const EncodeTiled encode = encode_tiled();
   if (!encode) return cudaErrorNotSupported;

@@ -156,7 +156,7 @@ __device__ __forceinline__ void locate(const Params& q, const Tables& tb, int un
   const int u = unit - tile0 * q.MT;
   j.mt = u / tiles;
   const int rows = uniform(tb.rows[j.e]), per = (rows + tiles - 1) / tiles, row = (u - j.mt * tiles) * per;
-  j.row = static_cast<int>(uniform(first_row(q.p, j.e))) + row;
+  j.row = uniform(tb.slot0[j.e]) + row;
   j.rows = min(per, rows - row);
 }
 
@@ -345,10 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
   }
+  if (tid == 32) prefetch_map(&map);
+  if (tid >= 64 && tid < 64 + q.tile_rows / 16) prefetch_map(&maps.box[tid - 64]);
   grid_dependency_wait();
   // (Tensor memory only now: a kernel that this one waits for may still ask for some.)
   if (warp == 3) tmem_alloc(&sh.tmem, kTmemCols);
-  tile_experts(q, sh.scan, tb);
+  tile_experts<true>(q, sh.scan, tb);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -367,10 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring r;
       Jobs jobs;
       bool again = false, jobs_again = false;  // the rings have been filled once
-      int next = 0;                            // the next whole unit, in the first lane
+      int next = share.cut + blockIdx.x;       // the next whole unit, in the first lane
       uint64_t filled = 0x0808080808080808ull;  // boxes of rows that each stage may hold
       auto take = [&]() {
-        if (lane == 0) next = share.cut + static_cast<int>(atomicAdd(q.taken, 1u));
+        if (lane == 0) next = share.cut + gridDim.x + static_cast<int>(atomicAdd(q.taken, 1u));
       };
       auto pass_on = [&](const Job& j) {
         if (jobs_again && !mbar_wait_warp(&sh.job_empty[jobs.at], jobs.parity ^ 1, p.status)) return false;
@@ -417,7 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
       };
-      take();
       bool ok = true;
       while (ok) {
         Job j;

@@ -52,7 +52,8 @@ struct Scan {
 };
 
 // Counts -> tiles, by a whole block of kThreads; ends with a block barrier.
-template <int kThreads, class Q>
+// kFirst: slot0 takes the experts' first rows instead (of those that have rows).
+template <bool kFirst = false, int kThreads, class Q>
 __device__ void tile_experts(const Q& q, Scan<kThreads>& sc, const Tables& tb) {
   constexpr int kPer = (EP_MAX_EXPERTS + kThreads - 1) / kThreads;
   const auto& p = q.p;
@@ -66,6 +67,7 @@ __device__ void tile_experts(const Q& q, Scan<kThreads>& sc, const Tables& tb) {
   for (int i = 0; i < kPer; ++i) {
     mine[i] = e0 + i < e1 ? rows_of(p, e0 + i, __ldg(p.count + e0 + i), first) : 0;
     rows += mine[i];
+    if (kFirst && e0 + i < e1) tb.slot0[e0 + i] = static_cast<int>(first);
   }
   // One scan of rows, slots and tiles at once. If there are more rows than
   // max_rows, what is over is taken off and the rest scanned again. (Rows are
@@ -124,7 +126,7 @@ __device__ void tile_experts(const Q& q, Scan<kThreads>& sc, const Tables& tb) {
   for (int i = 0; i < kPer; ++i) {
     if (e0 + i < e1) {
       tb.rows[e0 + i] = mine[i];
-      tb.slot0[e0 + i] = s0;
+      if (!kFirst) tb.slot0[e0 + i] = s0;
       tb.tile0[e0 + i] = t0;
     }
     s0 += round8(mine[i]);

@@ -36,9 +36,9 @@
 //
 // Measured (7168 inputs; copy rate 6.69 TB/s; in brackets bursts, before power holds
 // the clock down): 256 experts of 4 rows, 2 x 2048 gated outputs in FP8, 1036 us,
-// 7.2 TB/s; about 128 rows, 1500 us (1300, 6.0 TB/s); one token's eight experts 45 us;
+// 7.2 TB/s; about 128 rows, 1500 us (1290, 6.1 TB/s); one token's eight experts 43 us;
 // 32 experts of 2048 rows, 4096 outputs, 1715 us, 2.24 PFLOP/s (1560, 2.47); the
-// gradient of 16 experts of 1537 rows, 4096 to 7168, 736 us, 1.96 PFLOP/s.
+// gradient of 16 experts of 1537 rows, 4096 to 7168, 736 us, 1.96 PFLOP/s (693, 2.08).
 #include <algorithm>
 
 #include "common.cuh"
@@ -59,6 +59,8 @@ constexpr int kRowMaps = kTileRows / 16;  // boxes of 16, 32 .. 128 rows
 constexpr int kMaxBlocks = 160;         // blocks a workspace has room for
 constexpr int kThreads = 384;           // loads, products, scales (four warps), results (eight)
 constexpr int kResultThreads = 256;
+constexpr int kFewRows = 8;             // rows of a tile that a warp each finishes
+constexpr unsigned kFewBytes = kFewRows * kTileN * sizeof(float);
 constexpr int kMaxStages = 8;
 constexpr int kTmemCols = 512;          // two steps' sums
 constexpr int kMinStages = 2;           // fewest steps worth a block of their own
@@ -123,13 +125,14 @@ struct Share {
   int cut, cutters;  // units that are cut, blocks that share them
   int at, end;       // this block's steps of them
   __device__ Share(int units, int KS, int blocks, int me) : units(units), KS(KS), blocks(blocks) {
-    // A join at a call's end costs about 8 us, which pays only where few blocks would
-    // have work otherwise. (7168 inputs, one row, whole / cut: 48 units 37 / 32 us, 64
-    // 38 / 39, 80 39 / 48, 128 48 / 55; 100 rows, 80 units 38 / 49, 128 48 / 64.)
+    // A join at a call's end costs 4 to 10 us, which pays only where few blocks would
+    // have work otherwise. (7168 inputs, one row, whole / cut: 48 units 31 / 23 us, 64
+    // 32 / 29, 96 37 / 39, 128 44 / 47; 100 rows, 80 units 36 / 46; 2048 inputs, 30 rows, 80
+    // units 15 / 22.)
     cut = units < blocks && 8 * units > 3 * blocks ? 0 : units % blocks;
     // Every block that takes part has steps: the join counts on it. (Of 32 experts
     // of 128 rows 8 units are left to cut: in us, shared by 2, 4, 8, 16 and 19 blocks
-    // each, 232, 229, 237, 260 and 273; 2 units of 8 rows alone 22, 17, 18, 26, 38.)
+    // each, 232, 229, 237, 260 and 273.)
     cutters = min(min(blocks, kMaxParts * cut), max(cut * KS / kMinStages, 1));
     at = end = 0;
     if (me < cutters) {
@@ -267,6 +270,22 @@ __device__ __forceinline__ float largest(const float (&v)[64]) {
   return m;
 }
 
+// The scale of 128 results of which m is the largest magnitude, as the dispatch
+// quantises rows, and where it goes.
+__device__ __forceinline__ float scale_of(const ExpertLinearFp8Params& p, float m) {
+  float sc = __fdiv_rn(m, 448.0f);
+  if (p.out_pow2 && sc > 0.0f) sc = pow2_ceil(sc);
+  if (p.out_ue8m0 && m > 0.0f) sc = fmaxf(sc, __uint_as_float(0x00400000u));  // 2^-127
+  return sc;
+}
+__device__ __forceinline__ void store_scale(const ExpertLinearFp8Params& p, float sc, int64_t row, int block, int outs) {
+  const int64_t at = row * (outs / kBlock) + block;
+  if (p.out_ue8m0)
+    static_cast<uint8_t*>(p.y_scale)[at] = ue8m0_byte(sc);
+  else
+    static_cast<float*>(p.y_scale)[at] = sc;
+}
+
 // v / sc in E4M3, 64 of them. kQuick: correctly rounded from one correctly rounded
 // reciprocal y, by which the quotient t = v y is within an ulp, its remainder v - sc t
 // exact by a fused multiply-add, and t + remainder y rounds to v / sc (Markstein,
@@ -300,24 +319,44 @@ __device__ __forceinline__ void store_codes(const float (&v)[64], float sc, uint
   }
 }
 
-// ... and to E4M3, as the dispatch quantises rows, with the scale of the 128
-// results that they are part of.
+// ... and to E4M3, with the scale of the 128 results that they are part of.
 __device__ __forceinline__ void store_fp8(const ExpertLinearFp8Params& p, const float (&v)[64], float m, int64_t row,
                                           int o, int outs, bool writes_scale) {
-  float sc = __fdiv_rn(m, 448.0f);
-  if (p.out_pow2 && sc > 0.0f) sc = pow2_ceil(sc);
-  if (p.out_ue8m0 && m > 0.0f) sc = fmaxf(sc, __uint_as_float(0x00400000u));  // 2^-127
+  const float sc = scale_of(p, m);
   uint8_t* to = static_cast<uint8_t*>(p.y) + row * outs + o;
   if (sc >= 0x1p-92f && sc <= 0x1p126f)
     store_codes<true>(v, sc, to);
   else
     store_codes<false>(v, sc, to);
-  if (!writes_scale) return;
-  const int64_t at = row * (outs / kBlock) + o / kBlock;
-  if (p.out_ue8m0)
-    static_cast<uint8_t*>(p.y_scale)[at] = ue8m0_byte(sc);
-  else
-    static_cast<float*>(p.y_scale)[at] = sc;
+  if (writes_scale) store_scale(p, sc, row, o / kBlock, outs);
+}
+
+// A row's results by a warp: lane l has outputs 4 l .. 4 l + 3 of either 128 (a, b).
+__device__ __forceinline__ void finish_row(const ExpertLinearFp8Params& p, float4 a, float4 b, int64_t row, int mt,
+                                           int outs) {
+  const int lane = threadIdx.x & 31;
+  const auto store = [&](const float4& v, int block) {
+    const int o = block * kBlock + 4 * lane;
+    if (!p.out_fp8) {
+      if (o < outs)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + row * outs + o) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      return;
+    }
+    if (block * kBlock >= outs) return;
+    const float m = fmaxf(fmaxf(fmaxf(0.0f, fabsf(v.x)), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));  // (no NaN)
+    const float sc = scale_of(p, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
+    const float d = sc > 0.0f ? sc : 1.0f;
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + row * outs + o) =
+        pack_e4m3x2(__fdiv_rn(v.x, d), __fdiv_rn(v.y, d)) | pack_e4m3x2(__fdiv_rn(v.z, d), __fdiv_rn(v.w, d)) << 16;
+    if (lane == 0) store_scale(p, sc, row, block, outs);
+  };
+  if (p.glu) {
+    store(make_float4(silu(a.x) * b.x, silu(a.y) * b.y, silu(a.z) * b.z, silu(a.w) * b.w), mt);
+  } else {
+    store(a, 2 * mt);
+    store(b, 2 * mt + 1);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -329,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Shared sh;
   const ExpertLinearFp8Params& p = q.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
-  const Tables tb(reinterpret_cast<int*>(smem + q.stages * q.stage_bytes), p.E);
+  const Tables tb(reinterpret_cast<int*>(smem + q.stages * q.stage_bytes + kFewBytes), p.E);
   if (tid == 0) {
     for (int i = 0; i < q.stages; ++i) {
       mbar_init(&sh.full[i], 1);
@@ -594,16 +633,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sh.acc_empty[half]);
         }
       }
+      // With few rows a lane would form 64 gated outputs alone, and join them alone: a
+      // warp takes a row instead. (One token's eight experts 45.0 us, so 43.2; four rows,
+      // 16 units in four parts each, 24.0, so 17.6.)
+      const bool few = g.rows <= kFewRows;
       bool finishes = true;
       if (g.steps != q.KS) {
         // A shared unit: the last block to arrive adds the parts, in order.
         const int me = blockIdx.x, c_first = g.first, c_last = g.last;
         // Four sums of a row beside the next row's four.
         const int n = g.rows;
-        auto part = [&](int block, bool starts) {
+        auto parts = [&](int block, bool starts) {
           return reinterpret_cast<float4*>(q.partial) +
-                 (static_cast<int64_t>(block) * 2 + (starts ? 1 : 0)) * (kTileN / 4) * q.tile_rows + group * 32 * n + r;
+                 (static_cast<int64_t>(block) * 2 + (starts ? 1 : 0)) * (kTileN / 4) * q.tile_rows;
         };
+        auto part = [&](int block, bool starts) { return parts(block, starts) + group * 32 * n + r; };
         if (r < n) {
           float4* to = part(me, g.s0 == 0);
 #pragma unroll
@@ -626,7 +670,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         result_sync();
         const bool last = sh.last;
-        if (last && r < n) {
+        if (last && few) {
+          // A warp a row: all of a row's sums of all parts on their way at once.
+          const int mine = warp - 4;
+          if (mine < n) {
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+#pragma unroll 4
+            for (int first = c_first; first <= c_last; ++first) {
+              const float4* from = parts(first, first == c_first) + (lane >> 4) * 32 * n + (lane & 15) * n + mine;
+              const float4 x = __ldcg(from), y = __ldcg(from + 16 * n);
+              a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+              b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
+            }
+            finish_row(p, a, b, g.row + mine, g.mt, outs);
+          }
+        } else if (last && r < n) {
           // (Of two parts this block has one at hand, and which comes first makes no difference.)
           const bool two = c_last == c_first + 1;
           if (!two) {
@@ -654,9 +712,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         result_sync();  // sh.last is free again
-        finishes = last;
+        finishes = last && !few;
       }
-      if (finishes) {
+      if (finishes && few) {
+        float4* rows = reinterpret_cast<float4*>(smem + q.stages * q.stage_bytes);
+        if (r < g.rows) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float4 f;
+            unpack_f32x2(sums[2 * i], f.x, f.y);
+            unpack_f32x2(sums[2 * i + 1], f.z, f.w);
+            rows[r * (kTileN / 4) + group * 16 + (i < 16 ? i : i + 16)] = f;
+          }
+        }
+        result_sync();
+        const int mine = warp - 4;
+        if (mine < g.rows) {
+          const float4 a = rows[mine * (kTileN / 4) + lane], b = rows[mine * (kTileN / 4) + 32 + lane];
+          finish_row(p, a, b, g.row + mine, g.mt, outs);
+        }
+        result_sync();
+      } else if (finishes) {
         // Finished sums: the first 128 outputs' half (with GLU the gates'), then the second's.
         const int64_t row = g.row + r;
         const bool writes = r < g.rows;
@@ -753,9 +829,9 @@ cudaError_t launch_expert_linear_fp8(const ExpertLinearFp8Params& p, cudaStream_
   q.partial = reinterpret_cast<float*>(p.ws + 1024);
   q.stage_bytes = kTileBytes + static_cast<unsigned>(q.tile_rows) * kStep;
   const unsigned tables = static_cast<unsigned>(table_bytes(p.E));
-  const unsigned most = 227 * 1024 - sizeof(Shared) - 2048 - tables;
+  const unsigned most = 227 * 1024 - sizeof(Shared) - 2048 - tables - kFewBytes;
   q.stages = std::min<int>(kMaxStages, most / q.stage_bytes);
-  const size_t smem = static_cast<size_t>(q.stages) * q.stage_bytes + tables + 1024;
+  const size_t smem = static_cast<size_t>(q.stages) * q.stage_bytes + kFewBytes + tables + 1024;
 
   const EncodeTiled encode = encode_tiled();
   if (!encode) return cudaErrorNotSupported;

@@ -19,7 +19,7 @@
 // softmax. kSigmoidNear and kSoftmaxNear are twice that, and kSumNear what the
 // rounded sums of two such values add, relative to the largest.
 //
-// What bounds it: a call of few tokens its launch (4 us on the device, 14 from
+// What bounds it: a call of few tokens its launch (4 us on the device, 12 from
 // Python); with many, its instructions (about 1200 a token of 256 experts in 8
 // groups, 4 issued in 5 cycles). The bytes (1 KB of logits a token) take a tenth of
 // the time. Measured: 16384 tokens x 256 experts, 8 of 4 of 8 groups with a bias 25 us;

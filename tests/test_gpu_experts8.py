@@ -396,6 +396,19 @@ def test_every_number_of_units(rows):
         X.check_bf16(got[:rows, at], y, err)
 
 
+@pytest.mark.parametrize("K,M,counts,transposed", [
+    (128, 128, "many", False), (16384, 24, [2, 9], False), (16384, 256, [1, 33], True), (128, 16384, [17, 3], False),
+    (256, 128, "many", True)])
+def test_largest_sizes(K, M, counts, transposed):
+    """As many experts, and as many inputs, as there may be."""
+    if counts == "many":
+        counts = np.random.default_rng(5).integers(0, 3, ep.EP_MAX_EXPERTS).tolist()
+    c = Case(K + M + 40, K, M, counts, transposed=transposed)
+    got = f64(c.run())
+    for e, rows in c.rows():
+        X.check_bf16(got[rows], *c.expect(e, rows))
+
+
 def test_one_workspace_for_calls_of_all_sizes():
     """Calls one after the other, of other shapes and with nothing to do, leave a shared workspace as it was."""
     cases = [Case(30, 1024, 768, [9, 0, 200, 41]), Case(31, 256, 4096, [3] * 9), Case(32, 2048, 512, [70, 140], transposed=True)]

@@ -69,6 +69,22 @@ def test_choices_closer_than_fp32_can_tell(score, G, kept):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,kept", [(40, 1, 1), (256, 8, 4), (300, 3, 2), (512, 1, 1), (1000, 8, 3), (1024, 32, 9)])
+@pytest.mark.parametrize("tied", [12, 45])
+def test_some_choices_closer_than_fp32_can_tell(score, E, G, kept, tied):
+    """Of each token's experts some are the best by far and equal to half an ulp, few enough to compare or too many."""
+    g = torch.Generator().manual_seed(E + tied)
+    z = (torch.randn(1, E, generator=g) * 0.5).repeat(24, 1)
+    bias = torch.randn(E, generator=g) * 0.01
+    top = torch.randperm(E, generator=g)[:min(tied, E)]
+    bias[top] = torch.from_numpy((3.0 - X.scores(z[0].numpy(), score)).astype(np.float32))[top]
+    z += torch.randn(24, E, generator=g) * 1e-7
+    check(z, 8, bias, score, G, kept, 2)
+    check(z, 32, bias, score, G, kept, 1, renormalize=False)
+    check(z.to(torch.bfloat16), 8, bias, score, G, kept, 2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_sums_of_groups_closer_than_fp32_can_tell(score):
     """Groups with the same two best logits in another order, and with neighbours of them."""
     z = torch.full((16, 32), -4.0)

@@ -1126,25 +1126,36 @@ def route(logits: torch.Tensor, topk: int, bias: Optional[torch.Tensor] = None, 
         return _on_stream(stream, route, logits, topk, bias, score, groups, topk_groups, group_best, renormalize, scale,
                           topk_idx, topk_weights, return_scores)
     flags = _route_flags(score, renormalize)
-    _same_device(logits, bias, topk_idx, topk_weights)
     at, stride, tokens, experts, kind = _logits(logits)
     dev, shape = logits.device, (tokens, topk)
+    here = _get_device()
+    if dev.index != here:
+        _same_device(logits)
     # (What is made here needs no check: the call's time is the host's until there are thousands of tokens.)
     if topk_idx is None:
         topk_idx = torch.empty(shape, dtype=_I32, device=dev)
         idx_at = topk_idx.data_ptr()
     else:
+        _same_device(topk_idx)
         idx_at = _address(topk_idx, "topk_idx", _I32, shape)
     if topk_weights is None:
         topk_weights = torch.empty(shape, dtype=_F32, device=dev)
         weights_at = topk_weights.data_ptr()
     else:
+        _same_device(topk_weights)
         weights_at = _address(topk_weights, "topk_weights", _F32, shape)
-    scores = torch.empty((tokens, experts), dtype=_F32, device=dev) if return_scores else None
-    rc = lib().ep_route(at, stride, tokens, experts, topk,
-                        bias if bias is None else _address(bias, "bias", _F32, (experts,)), groups,
-                        groups if topk_groups is None else topk_groups, group_best, flags | kind, scale, idx_at,
-                        weights_at, scores if scores is None else scores.data_ptr(), _raw(None))
+    bias_at = None
+    if bias is not None:
+        bias_at = _address(bias, "bias", _F32, (experts,))
+        if bias.get_device() != here:
+            _same_device(bias)
+    scores = scores_at = None
+    if return_scores:
+        scores = torch.empty((tokens, experts), dtype=_F32, device=dev)
+        scores_at = scores.data_ptr()
+    rc = (_lib or lib()).ep_route(at, stride, tokens, experts, topk, bias_at, groups,
+                                  groups if topk_groups is None else topk_groups, group_best, flags | kind, scale, idx_at,
+                                  weights_at, scores_at, _raw_stream(here) if _raw_stream is not None else _raw(None))
     if rc != EP_OK:
         raise EPError("ep_route", rc)
     return (topk_idx, topk_weights, scores) if return_scores else (topk_idx, topk_weights)

@@ -68,6 +68,12 @@ constexpr int kMaxParts = 4;            // most blocks that share a unit
 constexpr int kJobs = 4;                // jobs between the loads and the results
 constexpr int kTakeAhead = 8;           // steps before a unit's end at which the next is taken
 constexpr int kAhead = 4;               // steps' scales in flight
+// The scales of step i are handed over once those of step i + kAhead - 1 are on
+// their way, whose job has been passed on by then. It has if all loads before it
+// have been issued, for which the products of step i + kAhead - 2 - stages and the
+// results of step i + kAhead - 4 - stages have to be done, and if the results of job
+// i + kAhead - 1 - kJobs are (a job may be one step): all before step i.
+static_assert(kAhead <= kJobs && kAhead <= 4, "scales would be waited for by what they wait for");
 // Registers of a thread: 168 at launch, of which four warps give 80 each to the
 // eight that hold the sums (3 x 168 = 88 + 2 x 208).
 constexpr int kLoadRegs = 88, kResultRegs = 208;

@@ -504,7 +504,7 @@ def ep_expert_linear(x, x_scale, x_rows, in_features, row_count, row_offset, row
 
 
 def _logits(t: torch.Tensor):
-    """(address, token stride, tokens, experts, flags) of [tokens, experts] bf16 or fp32 logits, rows apart as they may be."""
+    """(address, token stride, tokens, experts, flags) of [tokens, experts] bf16 or fp32 logits; rows may lie apart."""
     if t.dim() != 2 or t.dtype not in (_BF16, _F32) or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("logits: expected a CUDA tensor [tokens, experts] of bf16 or fp32, experts contiguous")
     n, experts = t.shape
@@ -1089,11 +1089,12 @@ def _same_device(*tensors: Optional[torch.Tensor]) -> None:
     """The tensors lie on the current device, where the call's kernels run."""
     here = None
     for t in tensors:
-        if t is not None and t.is_cuda:
-            if here is None:
+        if t is not None:
+            at = t.get_device()
+            if at != here and at >= 0:
                 here = _get_device()
-            if t.get_device() != here:
-                raise ValueError(f"expected tensors on the current device, cuda:{here}")
+                if at != here:
+                    raise ValueError(f"expected tensors on the current device, cuda:{here}")
 
 
 _SCORES = {"softmax": 0, "sigmoid": EP_ROUTE_SIGMOID}
@@ -1184,7 +1185,7 @@ def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: t
 
 def expert_linear_fp8_workspace(x: torch.Tensor, weight: torch.Tensor, max_rows: Optional[int] = None) -> torch.Tensor:
     """A zero-filled workspace for expert_linear_fp8 (or its backward) of rows shaped like x, to keep between calls."""
-    rows = x.numel() // x.shape[-1] if max_rows is None else int(max_rows)
+    rows = x.shape[:-1].numel() if max_rows is None else int(max_rows)
     need = ep_expert_linear_fp8_workspace_bytes(weight.shape[0], rows)
     if need == 0:
         raise EPError("expert_linear_fp8", EP_ERR_INVALID_ARG)
@@ -1198,46 +1199,49 @@ def _expert_linear_fp8(x, x_scale, weight, weight_scale, row_count, row_offset, 
     E, M, K = weight.shape
     if transposed:
         M, K = K, M
-    rows = x.numel() // K if K else 0
     lead = x.shape[:-1]
+    rows = lead.numel()
     if x.shape[-1] != K or x_scale.shape != (*lead, K // 128) or row_count.shape != (E,):
         raise ValueError("x, x_scale, row_count: expected [.., channels] of the weight's, a scale for each 128 of "
                          "them, and a count for each expert")
-    parts = 2 if glu else 1
-    blocks = (E, parts * -(-(M // parts) // 128), K // 128)
-    if transposed:
-        blocks = (E, K // 128, -(-M // 128))
+    outs = M // 2 if glu else M
+    blocks = (E, K // 128, -(-M // 128)) if transposed else (E, (2 if glu else 1) * -(-outs // 128), K // 128)
     if weight_scale.shape != blocks:
         raise ValueError(f"weight_scale: expected shape {blocks}, a scale for each 128 x 128 block")
+    region = 0
     if row_offset is None:
         if x.dim() != 3 or x.shape[0] != E:
             raise ValueError("x: expected [num_experts, cap, channels] without row_offset")
+        region = x.shape[1]
     elif row_offset.numel() < E:
         raise ValueError("row_offset: expected an offset for each expert")
-    if not use_fp8 and (round_scale or use_ue8m0 or out_scale is not None):
-        raise ValueError("round_scale, use_ue8m0 and out_scale go with use_fp8")
-    shape = (*lead, M // parts)
-    if out is None:
-        out = torch.empty(shape, dtype=_U8 if use_fp8 else _BF16, device=x.device)
-    elif out.shape != shape:
+    flags = (EP_LINEAR_GLU if glu else 0) | (EP_LINEAR_TRANSPOSED if transposed else 0)
+    if x_scale.dtype is _U8:
+        flags |= EP_LINEAR_X_UE8M0
+    shape = (*lead, outs)
+    if out is not None and out.shape != shape:
         raise ValueError(f"out: expected shape {shape}")
     if use_fp8:
-        shape = (*lead, M // parts // 128)
+        flags |= EP_LINEAR_OUT_FP8 | (EP_LINEAR_OUT_ROUND_SCALE if round_scale else 0) | \
+            (EP_LINEAR_OUT_UE8M0 if use_ue8m0 else 0)
+        if out is None:
+            out = torch.empty(shape, dtype=_U8, device=x.device)
+        shape = (*lead, outs // 128)
         if out_scale is None:
             out_scale = torch.empty(shape, dtype=_U8 if use_ue8m0 else _F32, device=x.device)
         elif out_scale.shape != shape:
             raise ValueError(f"out_scale: expected shape {shape}")
-    _same_device(x, x_scale, weight, weight_scale, row_count, row_offset, out, out_scale, workspace, status)
+    else:
+        if round_scale or use_ue8m0 or out_scale is not None:
+            raise ValueError("round_scale, use_ue8m0 and out_scale go with use_fp8")
+        if out is None:
+            out = torch.empty(shape, dtype=_BF16, device=x.device)
     limit = rows if max_rows is None else int(max_rows)
     if workspace is None:
         workspace = expert_linear_fp8_workspace(x, weight, limit)
-    flags = (EP_LINEAR_GLU if glu else 0) | (EP_LINEAR_TRANSPOSED if transposed else 0) | \
-        (EP_LINEAR_X_UE8M0 if x_scale.dtype is _U8 else 0)
-    if use_fp8:
-        flags |= EP_LINEAR_OUT_FP8 | (EP_LINEAR_OUT_ROUND_SCALE if round_scale else 0) | \
-            (EP_LINEAR_OUT_UE8M0 if use_ue8m0 else 0)
-    ep_expert_linear_fp8(x, x_scale, rows, K, row_count, row_offset, x.shape[1] if row_offset is None else 0, limit,
-                         weight, weight_scale, M, flags, out, out_scale, workspace, status)
+    _same_device(x, x_scale, weight, weight_scale, row_count, row_offset, out, out_scale, workspace, status)
+    ep_expert_linear_fp8(x, x_scale, rows, K, row_count, row_offset, region, limit, weight, weight_scale, M, flags, out,
+                         out_scale, workspace, status)
     return (out, out_scale) if use_fp8 else out
 
 

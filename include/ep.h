@@ -809,11 +809,12 @@ size_t ep_expert_linear_fp8_workspace_bytes(int num_experts, int64_t max_rows);
  * in_features] in E4M3 and a scale for each 128 x 128 block:
  *   y[r, o] = sum_b (x_scale[r, b] * w_scale[e, o / 128, b]) * sum_{k in b} x[r, k] w[e, o, k].
  * Sums are fp32, as is the product of the two scales, which has to be a finite
- * number (a block of zeros may have the scale 0). With EP_LINEAR_GLU, W_e's first out_features / 2 rows are gates g and the
- * others u, and y = silu(g) * u in fp32; gates and ups then have blocks of their
- * own. y is rounded once: to BF16, or with EP_LINEAR_OUT_FP8 to E4M3 by the rule
- * of ep_fp8_quantize applied to the fp32 values (one scale for each 128 outputs
- * of a row), which is the next product's x.
+ * number (a block of zeros may have the scale 0). With EP_LINEAR_GLU, W_e's first
+ * out_features / 2 rows are gates g and the others u, and y = silu(g) * u in fp32;
+ * gates and ups then have blocks of their own. y is rounded once: to BF16, or
+ * with EP_LINEAR_OUT_FP8 to E4M3 by the rule of ep_fp8_quantize applied to the
+ * fp32 values (one scale for each 128 outputs of a row), which is the next
+ * product's x. A NaN among a row's codes or scales stays in that row.
  *
  * With EP_LINEAR_TRANSPOSED, y_row = x_row W_e for W_e [in_features,
  * out_features]: given the E4M3 gradient of a product's outputs as x, and that

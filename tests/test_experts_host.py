@@ -125,3 +125,12 @@ def test_shapes_and_types_are_checked():
             ep.expert_linear_fp8(**(good | bad))
     with pytest.raises(ValueError, match="x, x_scale"):  # the gradient's rows have the outputs' channels
         ep.expert_linear_fp8_backward(x, s, w, ws, n, off)
+
+
+def test_no_channels_are_refused():
+    u8 = dict(dtype=torch.uint8)
+    n, off = torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+    for call in (ep.expert_linear_fp8, ep.expert_linear_fp8_backward):
+        w = torch.zeros(3, 0, 0, **u8)
+        with pytest.raises((ValueError, ep.EPError)):
+            call(torch.zeros(4, 0, **u8), torch.zeros(4, 0), w, torch.zeros(3, 0, 0), n, off)

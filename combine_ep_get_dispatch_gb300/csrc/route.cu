@@ -108,14 +108,20 @@ __device__ __forceinline__ int place(int e) { return e + (e >> 5); }
 // Whether this lane's group g is kept; every lane knows its group's best two
 // values (-inf: none), and lanes g * lanes on are group g's. near < 0: the values
 // are exact. Otherwise `close` is set where the last group kept and the first left
-// out are closer than that.
+// out are closer than that. (Of two values half the sum is compared: the sum of two of
+// the type's lowest would be -inf, a group of which no expert is left. What is lost of
+// numbers below 2^-125 is below any `near`.)
 __device__ __forceinline__ bool keeps_group(const RouteParams& p, float best, float second, int g, int lanes, float near,
                                             bool& close) {
   const float none = -inf();
   float largest = 0.0f;
-  if (p.group_best == 2 && second > none) {
-    largest = fmaxf(fabsf(best), fabsf(second));
-    best += second;
+  if (p.group_best == 2) {
+    near *= 0.5f;
+    best *= 0.5f;
+    if (second > none) {
+      largest = fmaxf(fabsf(best), 0.5f * fabsf(second));
+      best = fmaf(0.5f, second, best);
+    }
   }
   const bool real = g < p.groups;
   int ahead = 0;

@@ -255,3 +255,23 @@ def test_in_a_graph_and_on_another_stream(score):
     want = ep.route(z, 6, **args)
     assert torch.equal(idx, want[0]) and torch.equal(w, want[1])
     assert torch.equal(d, ep.route_backward(dw, z, idx, score=score))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,kept,K", [(32, 8, 5, 20), (32, 4, 3, 20), (60, 6, 4, 32), (24, 12, 8, 12)])
+@pytest.mark.parametrize("best", [1, 2])
+def test_groups_whose_biases_add_up_past_fp32(score, E, G, kept, K, best):
+    """Biases of the type's lowest and largest values: a sum of two has no fp32, and is none of "no expert is left"."""
+    g = torch.Generator().manual_seed(14)
+    z, size = torch.randn(16, E, generator=g) * 1.5, E // G
+    low, most = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    for value in (low, most, low / 2, most / 2):
+        bias = torch.randn(E, generator=g) * 0.1
+        bias[size:-size] = value           # all groups but two
+        check(z, K, bias, score, G, kept, best)
+        bias[::2] *= 0.999                 # and values that differ
+        check(z, K, bias, score, G, kept, best)
+        bias[:] = value                    # every group
+        check(z, K, bias, score, G, kept, best)
+    bias[:size], bias[size:] = low, float("-inf")
+    check(z, K, bias, score, G, kept, best)

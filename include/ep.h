@@ -748,7 +748,8 @@ int ep_expert_linear(const void* x, const uint8_t* x_scale, int64_t x_rows, int 
  * index; values closer than fp32 can tell are compared in 64 bits, so that the
  * choice is that of the formula. The weights are the chosen experts' scores,
  * without the bias: w_k = scale * s_k / (sum_j s_j + 1e-20) with
- * EP_ROUTE_RENORMALIZE, otherwise scale * s_k.
+ * EP_ROUTE_RENORMALIZE, otherwise scale * s_k. Weights are made of fp32 scores:
+ * one below 2^-126 may count as 0 there, in the gradient too.
  *
  * An expert whose logit or bias is -inf or NaN is never chosen, and a NaN has
  * score 0 and no part in the softmax. A token with fewer than num_topk experts

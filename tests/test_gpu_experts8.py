@@ -427,3 +427,42 @@ def test_nothing_to_do():
     y = torch.full((c.total, 128), 5.0, dtype=torch.bfloat16, device="cuda")
     c.run(out=y, max_rows=0)
     assert (y == 5.0).all()
+
+
+@pytest.mark.parametrize("n", [7, 40])
+def test_fp8_results_that_are_no_numbers(n):
+    """Rows with infinities, NaN and the smallest numbers: the rule of ep_fp8_quantize, few rows and many."""
+    K = M = 128
+    w = torch.zeros((1, M, K), dtype=torch.uint8, device="cuda")
+    w[0, torch.arange(M), torch.arange(K)] = 0x38                 # the identity
+    ws = torch.ones((1, 1, 1), device="cuda")
+    x = dev(codes_of(np.random.default_rng(25), n, K))
+    powers = torch.tensor([127, -126, 120, 119, -125, 0, 124], device="cuda").repeat(6)[:n]
+    xs = torch.ldexp(torch.ones(n, device="cuda"), powers)[:, None]
+    x[1::7, :] &= 0x81                                            # a smallest code, or zero
+    y = ep.expert_linear_fp8(x, xs, w, ws, ints([n]), ints([0]))
+    with np.errstate(over="ignore", invalid="ignore"):
+        v = (R.TABLE[x.cpu().numpy()] * f64(xs)).astype(np.float32)   # exact, or past fp32
+        m = np.abs(v).max(1)
+        for form, kw in (("fp32", dict()), ("round", dict(round_scale=True)), ("ue8m0", dict(use_ue8m0=True))):
+            q, s = ep.expert_linear_fp8(x, xs, w, ws, ints([n]), ints([0]), use_fp8=True, **kw)
+            scale = m / np.float32(448)
+            if form != "fp32":
+                f, e = np.frexp(scale)
+                scale = np.where(np.isfinite(scale), np.ldexp(np.float32(1), e - (f == 0.5)), scale)
+            if form == "ue8m0":
+                scale = np.maximum(scale, np.float32(2.0 ** -127))
+            got = f64(s)[:, 0]
+            if form == "ue8m0":
+                got = np.where(got == 255, np.inf, 2.0 ** (got - 127))
+            assert np.array_equal(got, scale.astype(np.float64))
+            want = torch.from_numpy(v / scale[:, None].astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8)
+            q = q.cpu()
+            nan = ((q & 0x7F) == 0x7F) & ((want & 0x7F) == 0x7F)
+            assert ((q == want) | nan | ((q & 0x7F) == 0) & ((want & 0x7F) == 0)).all()
+            codes, scales = torch.empty_like(q, device="cuda"), torch.empty_like(s)
+            ep.ep_fp8_quantize(y, codes, scales, ep.fp8_flags(True, **kw))
+            rows = torch.from_numpy(np.nonzero((f64(y) == v).all(1))[0])  # those that BF16 holds
+            assert rows.numel() >= 4 * (n // 7) and torch.equal(scales.cpu()[rows], s.cpu()[rows])
+            codes = codes.cpu()[rows]
+            assert ((codes == q[rows]) | nan[rows] | ((codes & 0x7F) == 0) & ((q[rows] & 0x7F) == 0)).all()

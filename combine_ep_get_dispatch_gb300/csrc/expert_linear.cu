@@ -639,11 +639,11 @@ __global__ void __launch_bounds__(kThreads)
         if (q.mult == 2) {
           float l[8];
           tmem_load8(l, acc + rows8 + c0);
-          tmem_wait_load();
+          tmem_wait_load(v, l);
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] += l[i];
         } else {
-          tmem_wait_load();
+          tmem_wait_load(v);
         }
         if (whole) {
           finish(v, c0);

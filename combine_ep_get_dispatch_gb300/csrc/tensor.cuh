@@ -99,13 +99,11 @@ __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fenc
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // Eight columns of this thread's lane (warp w of a warpgroup: lanes 32 w ..).
-__device__ __forceinline__ void tmem_load8(float* v, uint32_t addr) {
-  uint32_t r[8];
+// (Straight into v: a copy of a register would read it before the wait.)
+__device__ __forceinline__ void tmem_load8(float (&v)[8], uint32_t addr) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                : "r"(addr));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // 32 columns of it.
@@ -121,7 +119,24 @@ __device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t addr) {
       : "r"(addr));
 }
 
-__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// What tmem_load8 asked for has arrived in v (and in w). Each register is an operand:
+// what reads one that is not may be moved in front of the wait.
+__device__ __forceinline__ void tmem_wait_load(float (&v)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]),
+                 "+f"(v[5]), "+f"(v[6]), "+f"(v[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_load(float (&v)[8], float (&w)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]),
+                 "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(w[0]), "+f"(w[1]),
+                 "+f"(w[2]), "+f"(w[3]), "+f"(w[4]), "+f"(w[5]), "+f"(w[6]),
+                 "+f"(w[7])
+               :
+               : "memory");
+}
 
 // ---- shared-memory matrix descriptors ----------------------------------------
 // Rows of 128 bytes in the 128-byte swizzle (16-byte piece c of row r lies at

@@ -29,7 +29,7 @@ def waits(text):
     return found
 
 
-@pytest.mark.parametrize("name", ["expert_linear_fp8.cu"])
+@pytest.mark.parametrize("name", ["expert_linear_fp8.cu", "tensor.cuh"])
 def test_a_wait_names_every_register_that_it_waits_for(name):
     found = waits(source(name))
     assert found
@@ -38,3 +38,15 @@ def test_a_wait_names_every_register_that_it_waits_for(name):
         for array, n in arrays.items():
             tied = {int(i) for i in re.findall(r'"\+[rf]"\(%s\[(\d+)\]\)' % array, body)}
             assert tied == set(range(n)), (function, array, set(range(n)) - tied)
+
+
+@pytest.mark.parametrize("name", ["expert_linear.cu", "expert_linear_fp8.cu"])
+def test_what_is_loaded_is_waited_for_before_it_is_read(name):
+    text = source(name)
+    names = {f for n in ("tensor.cuh", name) for f, _, _ in waits(source(n))}
+    loads = list(re.finditer(r"tmem_load\d+\((\w+),", text))
+    assert names and loads
+    for m in loads:
+        after = text[m.end():]
+        use = re.search(r"\b%s\b" % m.group(1), after)
+        assert re.search(r"\b(%s)\((\w+, )?$" % "|".join(names), after[:use.start()]), text[m.start():m.end() + use.end()]

@@ -130,12 +130,21 @@ struct Share {
   int units, KS, blocks;
   int cut, cutters;  // units that are cut, blocks that share them
   int at, end;       // this block's steps of them
-  __device__ Share(int units, int KS, int blocks, int me) : units(units), KS(KS), blocks(blocks) {
-    // A join at a call's end costs 4 to 10 us, which pays only where few blocks would
-    // have work otherwise. (7168 inputs, one row, whole / cut: 48 units 31 / 23 us, 64
-    // 32 / 29, 96 37 / 39, 128 44 / 47; 100 rows, 80 units 36 / 46; 2048 inputs, 30 rows, 80
-    // units 15 / 22.)
-    cut = units < blocks && 8 * units > 3 * blocks ? 0 : units % blocks;
+  // few: the tiles have up to kFewRows rows on average.
+  __device__ Share(int units, int KS, int blocks, int me, bool few) : units(units), KS(KS), blocks(blocks) {
+    // With fewer units than blocks, cutting them saves a block three quarters of a
+    // unit's steps (kMaxParts), or what the blocks at hand allow: half of them feed all
+    // of HBM's rate, so that from blocks / 2 units on nothing is saved. The join costs
+    // as much as 6 steps with few rows and 22 with more (a step is 0.36 us), and 10 and
+    // 31 where the cuts fall unevenly on the units. (One expert's units, whole / cut, in us;
+    // 7168 inputs, 1 row: 16 units 28.1 / 15.4, 38 28.8 / 19.5, 60 29.5 / 28.1, 68 29.7 / 29.9;
+    // 128 rows: 16 30.8 / 24.9, 38 31.2 / 29.8, 48 32.1 / 36.3. 2048 inputs, 1 row: 16 12.6 / 11.2,
+    // 38 13.1 / 12.9, 48 13.2 / 15.7; 32 rows: 16 12.7 / 16.8, 48 13.2 / 21.6. 1024 inputs, 1 row:
+    // 4 8.6 / 8.5, 48 10.5 / 14.1. 16384 inputs, 9 rows: 56 57.1 / 52.3.)
+    const bool even = kMaxParts * units <= blocks;
+    const int saved = KS * (blocks - max(2 * units, blocks / 4)) / blocks;
+    const int join = few ? (even ? 6 : 10) : even ? 22 : 31;
+    cut = units < blocks && saved <= join ? 0 : units % blocks;
     // Every block that takes part has steps: the join counts on it. (Of 32 experts
     // of 128 rows 8 units are left to cut: in us, shared by 2, 4, 8, 16 and 19 blocks
     // each, 232, 229, 237, 260 and 273.)
@@ -411,7 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     give_registers<kLoadRegs>();
     if (warp == 0) {
       // Loads. This warp finds the block's jobs and passes them on.
-      Share share(uniform(tb.tile0[p.E]) * q.MT, q.KS, gridDim.x, blockIdx.x);
+      const int tiles = uniform(tb.tile0[p.E]);
+      const unsigned rows =  // of all tiles, from their scan
+          __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? static_cast<unsigned>(sh.scan.rows[lane]) : 0u);
+      Share share(tiles * q.MT, q.KS, gridDim.x, blockIdx.x, rows <= static_cast<unsigned>(kFewRows * tiles));
       Ring r;
       Jobs jobs;
       bool again = false, jobs_again = false;  // the rings have been filled once

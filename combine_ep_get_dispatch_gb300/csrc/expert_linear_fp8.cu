@@ -80,10 +80,8 @@ constexpr int kLoadRegs = 88, kResultRegs = 208;
 
 struct Params {
   ExpertLinearFp8Params p;
-  int mult;       // columns a row (expert_tiles.cuh): 1
   int tile_rows;  // rows of a full tile
-  int KB;         // steps of a unit
-  int KS;         // the same
+  int KS;         // steps of a unit: blocks of 128 inputs
   int MT;         // units of a tile: an expert's output tiles
   int stages;
   unsigned stage_bytes;
@@ -564,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Job& j = sh.job[jobs.at];
           left = j.steps;
           rows = j.rows;
-          xa = static_cast<int64_t>(j.row + t) * q.KB + j.s0;
+          xa = static_cast<int64_t>(j.row + t) * q.KS + j.s0;
           w = p.w_scale + static_cast<int64_t>(j.e) * q.scale_rows * q.scale_cols;
           const int b = p.glu ? j.mt : 2 * j.mt;  // first of the unit's two blocks of outputs
           if (p.transposed) {
@@ -579,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           jobs.done(sh);
         }
         x0[i] = t < rows ? row_scale(p, xa) : 0.0f;
-        x1[i] = t + 64 < rows ? row_scale(p, xa + 64 * static_cast<int64_t>(q.KB)) : 0.0f;
+        x1[i] = t + 64 < rows ? row_scale(p, xa + 64 * static_cast<int64_t>(q.KS)) : 0.0f;
         w0[i] = __ldg(w);
         w1[i] = __ldg(w + w_second);
         ++xa;
@@ -835,14 +833,13 @@ cudaError_t launch_expert_linear_fp8(const ExpertLinearFp8Params& p, cudaStream_
   if (p.max_rows <= 0 || p.x_rows <= 0) return cudaSuccess;
   Params q{};
   q.p = p;
-  q.mult = 1;
   q.tile_rows = tile_rows_for(p.E, p.max_rows);
-  q.KB = q.KS = p.K / kStep;
+  q.KS = p.K / kStep;
   q.MT = p.glu ? (p.M / 2 + kBlock - 1) / kBlock : (p.M + kTileN - 1) / kTileN;
   const int parts = p.glu ? 2 : 1;
   const int out_blocks = parts * ((p.M / parts + kBlock - 1) / kBlock);
-  q.scale_rows = p.transposed ? q.KB : out_blocks;
-  q.scale_cols = p.transposed ? out_blocks : q.KB;
+  q.scale_rows = p.transposed ? q.KS : out_blocks;
+  q.scale_cols = p.transposed ? out_blocks : q.KS;
   q.counters = reinterpret_cast<unsigned*>(p.ws);
   q.taken = q.counters + kMaxBlocks;
   q.partial = reinterpret_cast<float*>(p.ws + 1024);

@@ -778,9 +778,10 @@ int ep_route(const void* logits, int64_t logits_stride, int num_tokens, int num_
  * expert's score has ds_k = scale / S * (dw_k - sum_j dw_j w'_j), or scale * dw_k
  * without EP_ROUTE_RENORMALIZE, and every score grad_scores besides. Then
  * dz_i = s_i (ds_i - sum_j s_j ds_j) for the softmax, s_i (1 - s_i) ds_i for the
- * sigmoid (without a difference from 1: experts with scores next to 1 keep their
- * gradient); sums in fp32, rounded once to the logits' type. The scores are
- * computed from the logits anew. An index -1 adds nothing; an expert that a
+ * sigmoid; sums in fp32, rounded once to the logits' type. The scores are computed
+ * from the logits anew. Nothing here is a difference of nearly equal numbers where
+ * one score is next to 1: 1 - s_i is formed without one, and gradients enter the sums
+ * relative to that of the largest score. An index -1 adds nothing; an expert that a
  * token names twice gets both gradients.
  *
  *   grad_weights   [num_tokens, num_topk] fp32

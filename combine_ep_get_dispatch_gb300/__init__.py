@@ -1284,7 +1284,9 @@ def expert_linear_fp8_backward(grad_y: torch.Tensor, grad_scale: torch.Tensor, w
     (ep_fp8_quantize makes them of a bf16 gradient); weight [E, out, in] and
     weight_scale as in the product, out and in multiples of 128. The rest as
     there. Returns [.., in] bf16, or (E4M3, scales) with use_fp8. The weights are
-    taken as constants.
+    taken as constants. Of a gated product grad_y is the gradient of gates and
+    ups (of multiples of 128 each), one after the other as the product without
+    glu gives them; the gate's own derivative is the caller's.
     """
     if stream is not None:
         return _on_stream(stream, expert_linear_fp8_backward, grad_y, grad_scale, weight, weight_scale, row_count,

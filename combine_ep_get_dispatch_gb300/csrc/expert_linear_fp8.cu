@@ -35,10 +35,10 @@
 // that was.
 //
 // Measured (7168 inputs; copy rate 6.69 TB/s; in brackets bursts, before power holds
-// the clock down): 256 experts of 4 rows, 2 x 2048 gated outputs in FP8, 1036 us,
-// 7.2 TB/s; about 128 rows, 1500 us (1290, 6.1 TB/s); one token's eight experts 43 us;
-// 32 experts of 2048 rows, 4096 outputs, 1720 us, 2.24 PFLOP/s (1520, 2.53); the
-// gradient of 16 experts of 1537 rows, 4096 to 7168, 730 us, 1.98 PFLOP/s (690, 2.09).
+// the clock down): 256 experts of 4 rows, 2 x 2048 gated outputs in FP8, 1003 us,
+// 7.4 TB/s; about 128 rows, 1430 us (1290, 6.1 TB/s); one token's eight experts 42 us;
+// 32 experts of 2048 rows, 4096 outputs, 1700 us, 2.26 PFLOP/s (1520, 2.53); the
+// gradient of 16 experts of 1537 rows, 4096 to 7168, 725 us, 1.99 PFLOP/s (690, 2.09).
 #include <algorithm>
 
 #include "common.cuh"

@@ -22,8 +22,8 @@
 // What bounds it: a call of few tokens its launch (4 us on the device, 12 from
 // Python); with many, its instructions (about 1200 a token of 256 experts in 8
 // groups, 4 issued in 5 cycles). The bytes (1 KB of logits a token) take a tenth of
-// the time. Measured: 16384 tokens x 256 experts, 8 of 4 of 8 groups with a bias 25 us;
-// softmax alone 16 us; 131072 tokens 149 and 112 us. The gradient of 16384 x 256: sigmoid
+// the time. Measured: 16384 tokens x 256 experts, 8 of 4 of 8 groups with a bias 22 us;
+// softmax alone 16 us; 131072 tokens 150 and 116 us. The gradient of 16384 x 256: sigmoid
 // 9.9 us, 3.5 TB/s, softmax 14.9 us; 131072 tokens 70 us.
 #include <math.h>
 
@@ -479,8 +479,10 @@ __device__ __forceinline__ void sort_down(unsigned (&key)[V], unsigned& order) {
   for (int j = 0; j < V; ++j) order |= at[j] << (4 * (j & 7));
 }
 
-// V: experts a lane. (Ten blocks an SM for up to 256 experts: with the 72 registers
-// that the kernel takes of itself, seven, softmax alone took 20 us instead of 16.)
+// V: experts a lane. (Ten blocks an SM for up to 256 experts, in 48 registers, of which
+// V = 8 spills 144 bytes and V = 4 68. With seven blocks and 72 registers, without
+// spills to speak of, softmax alone took 17.4 us instead of 16.4 for 16384 tokens and 128
+// instead of 116 for 131072; with groups and a bias 156 instead of 149 to 154.)
 template <int V>
 __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 10 : V == 16 ? 4 : 3) route_kernel(const RouteParams p) {
   extern __shared__ unsigned long long shared_values[];

@@ -664,12 +664,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const Route
   dw = e >= 0 ? dw * p.scale : 0.0f;
   const Scorer score = scorer(p, s);
   if (p.renormalize) {
-    // Gradients relative to that of the largest score: where it has nearly all of the sum,
-    // its own less the mean would be a difference of equal numbers.
+    // Where one score has most of the sum, gradients relative to its own: its own less the
+    // mean would be a difference of nearly equal numbers. (Where none has, the mean is no
+    // one's, and a difference from some large gradient would cost the small ones their bits.)
     const float w = e >= 0 ? score(z) : 0.0f;
     const float sum = warp_sum(w) + kTiny;
     const unsigned bits = __float_as_uint(w), most = __reduce_max_sync(kAll, bits);
-    const float base = __shfl_sync(kAll, dw, __ffs(__ballot_sync(kAll, bits == most)) - 1);
+    float base = __shfl_sync(kAll, dw, __ffs(__ballot_sync(kAll, bits == most)) - 1);
+    if (__uint_as_float(most) <= 0.5f * sum) base = 0.0f;
     dw = e >= 0 ? dw - base : 0.0f;
     dw = (dw - warp_sum(dw * (w / sum)) + base * (kTiny / sum)) / sum;  // (the quotients add up to 1 - kTiny / sum)
   }
@@ -690,17 +692,18 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const Route
       d[j] = slope == 0.0f ? 0.0f : slope * d[j];
     }
   } else {
-    // Relative to the largest score's, as above; the scores add up to 1.
     float base = 0.0f, dot = 0.0f;
-    bool largest = false;
+    if (score.inverse > 0.5f) {  // the largest score is most of their sum, 1: as above
+      bool largest = false;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (s[j] == score.top) {
-        base = d[j];
-        largest = true;
+      for (int j = 0; j < V; ++j) {
+        if (s[j] == score.top) {
+          base = d[j];
+          largest = true;
+        }
       }
+      base = __shfl_sync(kAll, base, __ffs(__ballot_sync(kAll, largest)) - 1);
     }
-    base = __shfl_sync(kAll, base, __ffs(__ballot_sync(kAll, largest)) - 1);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       s[j] = score(s[j]);

@@ -781,7 +781,7 @@ int ep_route(const void* logits, int64_t logits_stride, int num_tokens, int num_
  * sigmoid; sums in fp32, rounded once to the logits' type. The scores are computed
  * from the logits anew. Nothing here is a difference of nearly equal numbers where
  * one score is next to 1: 1 - s_i is formed without one, and gradients enter the sums
- * relative to that of the largest score. An index -1 adds nothing; an expert that a
+ * relative to that of the score that is more than half of theirs, if one is. An index -1 adds nothing; an expert that a
  * token names twice gets both gradients.
  *
  *   grad_weights   [num_tokens, num_topk] fp32

@@ -119,3 +119,22 @@ def test_gradient_of_tokens_that_are_sure(built, dtype, kind, renormalize, score
     want, err = backward(z.double().numpy(), idx.numpy(), dw.numpy(), None if ds is None else ds.numpy(), kind,
                          renormalize, 2.5)
     assert_near(got.double().cpu().numpy(), want, err, 2.0 ** -8 if dtype is torch.bfloat16 else 2.0 ** -24)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("spread", [0.01, 0.3])
+@pytest.mark.parametrize("E,K", [(448, 4), (992, 3), (1024, 9)])
+def test_gradient_of_tokens_that_are_sure_of_nothing(built, dtype, kind, renormalize, spread, E, K):
+    """Scores of a thousandth, and a few large gradients among zeros: those stay as near to 0 as they are."""
+    g = torch.Generator().manual_seed(E + K)
+    N = 40
+    z = (torch.randn(N, E, generator=g) * spread).to(dtype)
+    idx = torch.rand(N, E, generator=g).argsort(1)[:, :K].to(torch.int32)
+    idx[:20, 0] = z[:20].float().argmax(1)     # the best among the chosen, twice where it was
+    dw = torch.randn(N, K, generator=g)
+    got = ep.route_backward(dw.cuda(), z.cuda(), idx.cuda(), score=kind, renormalize=renormalize)
+    want, err = backward(z.double().numpy(), idx.numpy(), dw.numpy(), None, kind, renormalize, 1.0)
+    assert_near(got.double().cpu().numpy(), want, err, 2.0 ** -8 if dtype is torch.bfloat16 else 2.0 ** -24)
